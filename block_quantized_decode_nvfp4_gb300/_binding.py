@@ -23,6 +23,13 @@ BQD_PATH_MMA = 3
 BQD_PATH_DIRECT = 4
 BQD_PATH_TILES = 5
 BQD_LAUNCH_PDL = 1
+BQD_F32 = 0
+BQD_BF16 = 1
+BQD_E4M3 = 2
+BQD_SLOTS_TABLE_FULL = 1
+BQD_SLOTS_TOKENS_CUT = 2
+BQD_ROPE_HALVES = 0
+BQD_ROPE_PAIRS = 1
 
 _lib = None
 
@@ -34,6 +41,14 @@ class BqdError(RuntimeError):
         if status == 5 and _lib is not None:
             msg += ": " + lib().bqd_last_cuda_error().decode()
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)} ({msg})")
+
+
+class KVCache(C.Structure):
+    """bqd_kv_cache: the paged K and V arrays of one layer (see bqd.h)."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("num_pages", C.c_int64), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("page_size", C.c_int32), ("heads", C.c_int32),
+                ("head_dim", C.c_int32), ("type", C.c_int32)]
 
 
 _vp, _i64, _i32, _f32, _sz = C.c_void_p, C.c_int64, C.c_int, C.c_float, C.c_size_t
@@ -76,6 +91,14 @@ SIGNATURES = {
     "moe_grouped_gemv_noalloc": (_i32, [_vp] * 12 + [_i32, _i32, _i32, _i32, _i32, _vp]),
     "moe_layer": (_i32, [_vp] * 10 + [_sz, _i32, _i32, _i32, _i32, _i32, _vp]),
     "moe_layer_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "paged_slots": (_i32, [_vp, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "qk_norm_rope_cache": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i64, _i32, _i32, _vp,
+                                  _vp, _vp, C.POINTER(KVCache), _i64, _i32, _vp]),
+    "tree_attention": (_i32, [_vp, _i64, C.POINTER(KVCache), _vp, _i64, _vp, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _sz,
+                              _i64, _i64, _i32, _vp]),
+    "tree_attention_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32, _i32]),
+    "token_logprobs": (_i32, [_vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _i64, _i64, _vp]),
+    "token_logprobs_workspace_bytes": (_sz, [_i64, _i64, _i32]),
 }
 
 
@@ -305,3 +328,59 @@ def bqd_moe_read_status(workspace, stream=None) -> int:
     if st not in (BQD_OK, 8):
         raise BqdError(st, "bqd_moe_read_status")
     return out.value
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None) -> KVCache:
+    """Descriptor of a paged cache: k and v tensors [pages][page_size][heads][head_dim], bfloat16, or float8_e4m3fn
+    (or its bytes, uint8) with fp32 scales per head. A cache that holds a page's tokens by heads is passed as a view
+    with its dimensions in this order (k.transpose(1, 2)). The tensors must outlive the descriptor."""
+    import torch
+    types = {torch.bfloat16: BQD_BF16, torch.float8_e4m3fn: BQD_E4M3, torch.uint8: BQD_E4M3}
+    if k.dtype not in types or v.dtype != k.dtype or k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("kv_cache: k and v are [pages][page_size][heads][head_dim], of one type (bfloat16 or "
+                         "float8_e4m3fn) and one layout")
+    if k.shape[3] > 1 and k.stride(3) != 1:
+        raise ValueError("kv_cache: a head's elements are contiguous")
+    return KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.stride(0), k.stride(1), k.stride(2),
+                   k.shape[1], k.shape[2], k.shape[3], types[k.dtype])
+
+
+def paged_slots(context_lens, new_lens, free_pages, num_free, block_table, R, table_width, page_size, depths,
+                token_offsets, slots, positions, token_capacity, counts, stream=None):
+    """Block table, slots and positions of a step's new tokens from the requests' lengths."""
+    _check(lib().paged_slots(_ptr(context_lens), _ptr(new_lens), _ptr(free_pages), num_free, _ptr(block_table), R,
+                             table_width, page_size, _ptr(depths), _ptr(token_offsets), _ptr(slots), _ptr(positions),
+                             token_capacity, _ptr(counts), _stream(stream)), "paged_slots")
+
+
+def qk_norm_rope_cache(q, k, v, in_type, q_pitch, k_pitch, v_pitch, q_weight, k_weight, eps, cos_sin, max_pos,
+                       rot_dim, rot_style, positions, slots, q_out, cache, T, Hq, stream=None):
+    """Norm and rotation of q and k heads, q to q_out (bf16), k and v into the cache at each token's slot."""
+    _check(lib().qk_norm_rope_cache(_ptr(q), _ptr(k), _ptr(v), in_type, q_pitch, k_pitch, v_pitch, _ptr(q_weight),
+                                    _ptr(k_weight), eps, _ptr(cos_sin), max_pos, rot_dim, rot_style, _ptr(positions),
+                                    _ptr(slots), _ptr(q_out), C.byref(cache), T, Hq, _stream(stream)),
+           "qk_norm_rope_cache")
+
+
+def tree_attention(q, q_pitch, cache, block_table, table_width, context_lens, token_offsets, mask, mask_words, scale,
+                   out, lse, workspace, workspace_bytes, R, T, Hq, stream=None):
+    """Attention of a step's new tokens (decode, a drafted chain or a drafted tree) over the paged cache."""
+    _check(lib().tree_attention(_ptr(q), q_pitch, C.byref(cache), _ptr(block_table), table_width, _ptr(context_lens),
+                                _ptr(token_offsets), _ptr(mask), mask_words, scale, _ptr(out), _ptr(lse),
+                                _ptr(workspace), workspace_bytes, R, T, Hq, _stream(stream)), "tree_attention")
+
+
+def tree_attention_workspace_bytes(R, T, Hq, Hkv, D) -> int:
+    return lib().tree_attention_workspace_bytes(R, T, Hq, Hkv, D)
+
+
+def token_logprobs(logits, in_type, pitch, tokens, logprob, entropy, top_ids, top_logprobs, topk, workspace,
+                   workspace_bytes, T, V, stream=None):
+    """Log probability of given tokens, entropy and the topk alternatives of logits rows."""
+    _check(lib().token_logprobs(_ptr(logits), in_type, pitch, _ptr(tokens), _ptr(logprob), _ptr(entropy),
+                                _ptr(top_ids), _ptr(top_logprobs), topk, _ptr(workspace), workspace_bytes, T, V,
+                                _stream(stream)), "token_logprobs")
+
+
+def token_logprobs_workspace_bytes(T, V, topk) -> int:
+    return lib().token_logprobs_workspace_bytes(T, V, topk)

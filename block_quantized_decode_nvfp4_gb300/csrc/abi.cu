@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "attn.h"
 #include "bqd.h"
 #include "gemm.h"
 #include "gemv.h"
@@ -17,6 +18,14 @@ namespace {
 constexpr int kMaxN = 16;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Lists of integers may start anywhere (a free list that is used up from its
+// front, the tail of a table): their elements' alignment is enough.
+template <typename T>
+bool elem_aligned(const T* p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (sizeof(T) - 1)) == 0;
+}
 
 // The current device must be compute capability 10.3 (sm_103a code only).
 bqd_status check_arch()
@@ -538,6 +547,206 @@ bqd_status bqd_moe_read_status(const void* workspace, int32_t* status_out, cudaS
         return BQD_ERR_LAUNCH;
     *status_out = v;
     return v ? BQD_ERR_DEVICE : BQD_OK;
+}
+
+// ---------------------------------------------------------------- the step around attention
+static bool page_size_ok(int64_t p) { return p >= 1 && p <= 4096 && (p & (p - 1)) == 0; }
+
+static bqd_status check_cache(const bqd_kv_cache* c)
+{
+    if (!c) return BQD_ERR_NULL;
+    if (c->type != BQD_BF16 && c->type != BQD_E4M3) return BQD_ERR_SHAPE;
+    if (!page_size_ok(c->page_size) || c->heads < 1 || c->heads > 1024) return BQD_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return BQD_ERR_SHAPE;
+    if (c->num_pages < 0 || c->num_pages >= (int64_t(1) << 40) / c->page_size) return BQD_ERR_SHAPE;
+    const int64_t vec = c->type == BQD_BF16 ? 8 : 16;  // elements in 16 bytes
+    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+        if (s < 0 || s >= (int64_t(1) << 40) || s % vec != 0) return BQD_ERR_SHAPE;
+    if (c->num_pages > 0 && c->page_stride > (int64_t(1) << 60) / c->num_pages) return BQD_ERR_SHAPE;
+    if (c->num_pages > 0 && (!c->k || !c->v)) return BQD_ERR_NULL;
+    for (const void* p : {static_cast<const void*>(c->k), static_cast<const void*>(c->v),
+                          static_cast<const void*>(c->k_scale), static_cast<const void*>(c->v_scale)})
+        if (!aligned16(p)) return BQD_ERR_ALIGN;
+    return BQD_OK;
+}
+
+bqd_status paged_slots(const int32_t* context_lens, const int32_t* new_lens, const int32_t* free_pages,
+                       int64_t num_free, int32_t* block_table, int64_t R, int64_t table_width, int page_size,
+                       const int32_t* depths, int32_t* token_offsets, int64_t* slots, int32_t* positions,
+                       int64_t token_capacity, int32_t* counts, cudaStream_t stream)
+{
+    if (R < 0 || R >= (1 << 24) || table_width < 0 || num_free < 0 || num_free >= (int64_t(1) << 31) ||
+        token_capacity < 0 || token_capacity >= (int64_t(1) << 31) || !page_size_ok(page_size))
+        return BQD_ERR_SHAPE;
+    if (R > 0 && table_width >= (int64_t(1) << 40) / R) return BQD_ERR_SHAPE;
+    if (!token_offsets || !counts) return BQD_ERR_NULL;
+    if (R > 0 && (!context_lens || !new_lens || (table_width > 0 && !block_table))) return BQD_ERR_NULL;
+    if (num_free > 0 && !free_pages) return BQD_ERR_NULL;
+    if (token_capacity > 0 && (!slots || !positions)) return BQD_ERR_NULL;
+    if (!elem_aligned(context_lens) || !elem_aligned(new_lens) || !elem_aligned(free_pages) ||
+        !elem_aligned(block_table) || !elem_aligned(depths) || !elem_aligned(token_offsets) || !elem_aligned(slots) ||
+        !elem_aligned(positions) || !elem_aligned(counts))
+        return BQD_ERR_ALIGN;
+    bqd_status st = check_arch();
+    if (st != BQD_OK) return st;
+    bqd::SlotsArgs a{};
+    a.context = context_lens;
+    a.fresh = new_lens;
+    a.free_pages = free_pages;
+    a.depths = depths;
+    a.table = block_table;
+    a.offsets = token_offsets;
+    a.positions = positions;
+    a.counts = counts;
+    a.slots = slots;
+    a.num_free = num_free;
+    a.R = R;
+    a.width = table_width;
+    a.capacity = token_capacity;
+    while ((1 << a.page_shift) < page_size) ++a.page_shift;
+    return from_cuda(bqd::launch_paged_slots(a, stream));
+}
+
+bqd_status qk_norm_rope_cache(const void* q, const void* k, const void* v, int in_type, int64_t q_pitch,
+                              int64_t k_pitch, int64_t v_pitch, const float* q_weight, const float* k_weight,
+                              float eps, const float* cos_sin, int64_t max_pos, int rot_dim, int rot_style,
+                              const int32_t* positions, const int64_t* slots, uint16_t* q_out,
+                              const bqd_kv_cache* cache, int64_t T, int Hq, cudaStream_t stream)
+{
+    bqd_status st = check_cache(cache);
+    if (st != BQD_OK) return st;
+    if (in_type != BQD_F32 && in_type != BQD_BF16) return BQD_ERR_SHAPE;
+    const int64_t D = cache->head_dim, vec = in_type == BQD_F32 ? 4 : 8;
+    if (T < 0 || T >= (int64_t(1) << 31) || Hq < 1 || Hq > 65535) return BQD_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || (rot_style != BQD_ROPE_HALVES && rot_style != BQD_ROPE_PAIRS))
+        return BQD_ERR_SHAPE;
+    if (max_pos < 0 || max_pos > (int64_t(1) << 31)) return BQD_ERR_SHAPE;
+    if (q_pitch < Hq * D || k_pitch < cache->heads * D || v_pitch < cache->heads * D) return BQD_ERR_SHAPE;
+    for (int64_t p : {q_pitch, k_pitch, v_pitch})
+        if (p % vec != 0 || p >= (int64_t(1) << 31)) return BQD_ERR_SHAPE;
+    if (T == 0) return BQD_OK;
+    if (!q || !k || !v || !slots || !q_out) return BQD_ERR_NULL;
+    if (rot_dim > 0 && (!cos_sin || !positions)) return BQD_ERR_NULL;
+    for (const void* p : {q, k, v, static_cast<const void*>(q_weight), static_cast<const void*>(k_weight),
+                          static_cast<const void*>(cos_sin), static_cast<const void*>(q_out)})
+        if (!aligned16(p)) return BQD_ERR_ALIGN;
+    if (!elem_aligned(positions) || !elem_aligned(slots)) return BQD_ERR_ALIGN;
+    if ((st = check_arch()) != BQD_OK) return st;
+    bqd::QkRopeArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_pitch = q_pitch;
+    a.k_pitch = k_pitch;
+    a.v_pitch = v_pitch;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.slots = slots;
+    a.q_out = q_out;
+    a.eps = eps;
+    a.max_pos = max_pos;
+    a.T = T;
+    a.rot = rot_dim;
+    a.pairs = rot_style == BQD_ROPE_PAIRS;
+    a.Hq = Hq;
+    a.cache = *cache;
+    return from_cuda(bqd::launch_qk_norm_rope_cache(a, in_type, stream));
+}
+
+static bool attn_sizes_ok(int64_t R, int64_t T, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    if (R < 0 || T < 0 || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 64) return false;
+    if (D != 64 && D != 128 && D != 256) return false;
+    return R < (int64_t(1) << 24) / Hkv && T < (int64_t(1) << 31) / Hq;
+}
+
+size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int D)
+{
+    if (!attn_sizes_ok(R, T, Hq, Hkv, D)) return 0;
+    return bqd::tree_attention_ws(R, T, Hq, Hkv, D);
+}
+
+bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache* cache, const int32_t* block_table,
+                          int64_t table_width, const int32_t* context_lens, const int32_t* token_offsets,
+                          const uint64_t* mask, int mask_words, float scale, uint16_t* out, float* lse,
+                          void* workspace, size_t workspace_bytes, int64_t R, int64_t T, int Hq, cudaStream_t stream)
+{
+    bqd_status st = check_cache(cache);
+    if (st != BQD_OK) return st;
+    if (!attn_sizes_ok(R, T, Hq, cache->heads, cache->head_dim)) return BQD_ERR_SHAPE;
+    if (q_pitch < static_cast<int64_t>(Hq) * cache->head_dim || q_pitch % 8 != 0 || q_pitch >= (int64_t(1) << 31))
+        return BQD_ERR_SHAPE;
+    if (table_width < 0 || (R > 0 && table_width >= (int64_t(1) << 40) / R)) return BQD_ERR_SHAPE;
+    if (mask && (mask_words < 1 || mask_words > (1 << 20))) return BQD_ERR_SHAPE;
+    if (T == 0 || R == 0) return BQD_OK;
+    if (!q || !context_lens || !token_offsets || !out || (table_width > 0 && !block_table)) return BQD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out)) return BQD_ERR_ALIGN;
+    if (!elem_aligned(block_table) || !elem_aligned(context_lens) || !elem_aligned(token_offsets) ||
+        !elem_aligned(mask) || !elem_aligned(lse))
+        return BQD_ERR_ALIGN;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < bqd::tree_attention_ws(R, T, Hq, cache->heads, cache->head_dim))
+        return BQD_ERR_WORKSPACE;
+    if ((st = check_arch()) != BQD_OK) return st;
+    bqd::AttnArgs a{};
+    a.q = q;
+    a.table = block_table;
+    a.context = context_lens;
+    a.offsets = token_offsets;
+    a.mask = mask;
+    a.out = out;
+    a.lse = lse;
+    a.ws = workspace;
+    a.q_pitch = q_pitch;
+    a.width = table_width;
+    a.R = R;
+    a.T = T;
+    a.scale = scale;
+    a.mask_words = mask_words;
+    a.Hq = Hq;
+    a.cache = *cache;
+    return from_cuda(bqd::launch_tree_attention(a, stream));
+}
+
+size_t token_logprobs_workspace_bytes(int64_t T, int64_t V, int topk)
+{
+    if (T < 0 || T >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31) || topk < 0 || topk > 32 || topk > V)
+        return 0;
+    return bqd::token_logprobs_ws(T, V, topk);
+}
+
+bqd_status token_logprobs(const void* logits, int in_type, int64_t pitch, const int32_t* tokens, float* logprob,
+                          float* entropy, int32_t* top_ids, float* top_logprobs, int topk, void* workspace,
+                          size_t workspace_bytes, int64_t T, int64_t V, cudaStream_t stream)
+{
+    if (in_type != BQD_F32 && in_type != BQD_BF16) return BQD_ERR_SHAPE;
+    if (T < 0 || T >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31) || topk < 0 || topk > 32 || topk > V)
+        return BQD_ERR_SHAPE;
+    if (pitch < V || pitch >= (int64_t(1) << 31)) return BQD_ERR_SHAPE;
+    if (T == 0) return BQD_OK;
+    if (!logits || (logprob && !tokens) || (topk > 0 && (!top_ids || !top_logprobs))) return BQD_ERR_NULL;
+    if (!aligned16(logits) || !elem_aligned(tokens) || !elem_aligned(logprob) || !elem_aligned(entropy) ||
+        !elem_aligned(top_ids) || !elem_aligned(top_logprobs))
+        return BQD_ERR_ALIGN;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < bqd::token_logprobs_ws(T, V, topk))
+        return BQD_ERR_WORKSPACE;
+    bqd_status st = check_arch();
+    if (st != BQD_OK) return st;
+    bqd::LogprobArgs a{};
+    a.x = logits;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_logprobs = top_logprobs;
+    a.top_ids = top_ids;
+    a.ws = workspace;
+    a.pitch = pitch;
+    a.T = T;
+    a.V = static_cast<int>(V);
+    a.topk = topk;
+    return from_cuda(bqd::launch_token_logprobs(a, in_type, stream));
 }
 
 }  // extern "C"

@@ -524,6 +524,156 @@ bqd_status moe_grouped_gemv_noalloc(const uint8_t* gu_codes, const uint8_t* gu_s
  */
 bqd_status bqd_moe_read_status(const void* workspace, int32_t* status_out, cudaStream_t stream);
 
+/*
+ * ---- The step around attention: slots, q/k/v into the cache, attention, scores ----
+ *
+ * The paged KV cache. K and V are two device arrays of num_pages pages of
+ * page_size tokens; element d of kv head h of token i of page p is at
+ *   p * page_stride + i * token_stride + h * head_stride + d   (elements)
+ * in both, so pages may hold tokens by heads or heads by tokens. A token's
+ * SLOT is p * page_size + i. Strides are multiples of 16 bytes.
+ * BQD_E4M3 caches hold value / scale rounded to E4M3 (saturating at 448),
+ * with one fp32 scale per kv head for K and one for V.
+ * In the calls below, lists of lengths, pages, slots, positions, tokens and
+ * masks, and per-token results other than vectors, need the alignment of
+ * their elements only; the other arrays 16 bytes, as everywhere.
+ */
+enum {
+    BQD_F32 = 0,  /* element types */
+    BQD_BF16 = 1,
+    BQD_E4M3 = 2
+};
+
+typedef struct bqd_kv_cache {
+    void* k;               /* device, 16-byte aligned */
+    void* v;               /* device, 16-byte aligned, the layout of k */
+    const float* k_scale;  /* device [heads]; BQD_E4M3 only (NULL: 1) */
+    const float* v_scale;  /* device [heads]; BQD_E4M3 only (NULL: 1) */
+    int64_t num_pages;     /* num_pages * page_size < 2^40 */
+    int64_t page_stride, token_stride, head_stride;
+    int32_t page_size;     /* a power of two, 1 .. 4096 */
+    int32_t heads;         /* kv heads, 1 .. 1024 */
+    int32_t head_dim;      /* 64, 128 or 256 */
+    int32_t type;          /* BQD_BF16 or BQD_E4M3 */
+} bqd_kv_cache;
+
+/*
+ * paged_slots -- where a step's new tokens go, from the requests' lengths.
+ * Request r has context_lens[r] tokens in the cache and appends new_lens[r]
+ * (negative lengths count as 0; a request may append none). Its cached
+ * tokens fill the first ceil(context / page_size) entries of its row of
+ * block_table [R][table_width]. The call
+ *  - takes the pages the requests lack from free_pages [num_free], front to
+ *    back in request order, and writes them into the table;
+ *  - token_offsets [R + 1]: the first token of each request (exclusive
+ *    prefix sum of new_lens; values stop at 2^31 - 1);
+ *  - for token t = token_offsets[r] + j: slots[t] (int64), the slot of
+ *    logical position context_lens[r] + j, and positions[t] =
+ *    context_lens[r] + depths[t] (+ j where depths is NULL): tokens of a
+ *    draft tree share a position with their siblings but not a slot;
+ *  - slots and positions of t in [total, token_capacity): -1;
+ *  - counts [4]: tokens, pages taken, pages short, BQD_SLOTS_* bits.
+ * A page that the list cannot give, or that the table has no column for,
+ * leaves its tokens with slot -1; a missing page's table entry is -1. Tokens
+ * past token_capacity are not written. Entries of the table that the step
+ * does not fill keep their values. R >= 0, table_width >= 0, num_free >= 0,
+ * token_capacity >= 0, R * table_width < 2^40; page_size as in bqd_kv_cache;
+ * num_free and token_capacity < 2^31, R < 2^24.
+ */
+enum {
+    BQD_SLOTS_TABLE_FULL = 1,  /* a request outgrew table_width */
+    BQD_SLOTS_TOKENS_CUT = 2   /* more tokens than token_capacity */
+};
+bqd_status paged_slots(const int32_t* context_lens, const int32_t* new_lens, const int32_t* free_pages,
+                       int64_t num_free, int32_t* block_table, int64_t R, int64_t table_width, int page_size,
+                       const int32_t* depths, int32_t* token_offsets, int64_t* slots, int32_t* positions,
+                       int64_t token_capacity, int32_t* counts, cudaStream_t stream);
+
+/*
+ * qk_norm_rope_cache -- one pass over a step's projections: q heads are
+ * normed, rotated and written to q_out; k heads are normed, rotated and
+ * stored in the cache; v heads are stored in the cache.
+ *   q: [T][Hq][D], k, v: [T][cache->heads][D], in_type BQD_F32 (what the
+ *      GEMVs write) or BQD_BF16; each with its own row pitch in elements
+ *      (a multiple of 16 bytes), so the three may be parts of one row.
+ *   norm: x * rsqrt(mean(x^2) + eps) * weight over the D elements of a head;
+ *      q_weight, k_weight: fp32 [D]; NULL: no norm.
+ *   rotation of the first rot_dim elements (a multiple of 16, 0 .. D) by the
+ *      angles of the token's position: (a, b) -> (a cos - b sin, b cos +
+ *      a sin); pairs (i, i + rot_dim / 2) for BQD_ROPE_HALVES, (2i, 2i + 1)
+ *      for BQD_ROPE_PAIRS. cos_sin: fp32 [max_pos][rot_dim], the cosines of
+ *      the rot_dim / 2 angles and then their sines.
+ *   positions: int32 [T]; slots: int64 [T]. A token whose slot is outside
+ *      the cache (-1: padding) is not stored. A token whose position is
+ *      outside [0, max_pos) is not stored and its q_out row is zero
+ *      (with rot_dim 0 positions are not read and may be NULL).
+ *   q_out: bf16 [T][Hq][D].
+ * All arithmetic is fp32, rounded once (to nearest even) where it is stored.
+ * Two tokens of one call must not share a slot. Hq >= 1, T >= 0.
+ */
+enum { BQD_ROPE_HALVES = 0, BQD_ROPE_PAIRS = 1 };
+bqd_status qk_norm_rope_cache(const void* q, const void* k, const void* v, int in_type, int64_t q_pitch,
+                              int64_t k_pitch, int64_t v_pitch, const float* q_weight, const float* k_weight,
+                              float eps, const float* cos_sin, int64_t max_pos, int rot_dim, int rot_style,
+                              const int32_t* positions, const int64_t* slots, uint16_t* q_out,
+                              const bqd_kv_cache* cache, int64_t T, int Hq, cudaStream_t stream);
+
+/*
+ * tree_attention -- attention of a step's new tokens over the paged cache:
+ *   out[t][h] = sum_l p_l v_l, p = softmax over the visible l of
+ *   scale * q[t][h] . k_l, with kv head h / (Hq / cache->heads).
+ * Token t = token_offsets[r] + i of request r sees the request's cached
+ * tokens l < context_lens[r] and, of its new tokens (logical positions
+ * context_lens[r] + j, already in the cache), those with bit j set in
+ * mask[t] (uint64 words [T][mask_words], bit j % 64 of word j / 64; j past
+ * the words is hidden). mask NULL: j <= i, a chain. One new token per
+ * request is plain decode. What a token does not see has no influence on
+ * its result, whatever is stored there (infinities and NaN included).
+ *   q: bf16, row pitch q_pitch elements (>= Hq * D, a multiple of 8).
+ *   block_table [R][table_width] int32; tokens whose page id is outside
+ *      [0, num_pages), or past the table, are not seen.
+ *   token_offsets [R + 1] int32, values clamped to [0, T], ascending;
+ *      context_lens [R] int32 (negative: 0). Read on the device: the same
+ *      launch serves any lengths (CUDA graphs).
+ *   out: bf16 [T][Hq][D]; lse: fp32 [T][Hq], log(sum exp(score)), may be
+ *      NULL. A token that sees nothing gets out = 0 and lse = -inf. Rows of
+ *      tokens that belong to no request are not written.
+ *   workspace: tree_attention_workspace_bytes(...) bytes, 16-byte aligned.
+ * Scores, softmax and sums are fp32; the probabilities enter the product
+ * with V as bf16 (relative error 2^-9 each). Hq a multiple of cache->heads, Hq / heads
+ * <= 64; R * heads < 2^24, T * Hq < 2^31.
+ */
+bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache* cache, const int32_t* block_table,
+                          int64_t table_width, const int32_t* context_lens, const int32_t* token_offsets,
+                          const uint64_t* mask, int mask_words, float scale, uint16_t* out, float* lse,
+                          void* workspace, size_t workspace_bytes, int64_t R, int64_t T, int Hq, cudaStream_t stream);
+
+/* Bytes of device workspace tree_attention needs for these sizes (0 if a size is out of range). */
+size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int D);
+
+/*
+ * token_logprobs -- what a step answers with, from its logits rows:
+ *   logprob[t] = x[t][tokens[t]] - lse(x[t]); a token outside [0, V): -inf
+ *   entropy[t] = -sum p log p, p = softmax(x[t]) (terms with p = 0 are 0)
+ *   top_ids, top_logprobs [T][topk]: the topk largest logits in descending
+ *      order, equal values by ascending index (-0 equals +0), with their log
+ *      probabilities.
+ * logits: BQD_F32 or BQD_BF16 [T][V], row pitch in elements (any >= V).
+ * Logits of -inf have probability 0. A row that is -inf throughout has
+ * log probability -inf everywhere and entropy 0. A NaN or +inf in a row
+ * makes its log probabilities and entropy NaN; among the alternatives NaN
+ * ranks below -inf. tokens with logprob, entropy, and top_ids with
+ * top_logprobs may be NULL; topk 0 .. 32, at most V.
+ * workspace: token_logprobs_workspace_bytes(T, V, topk) bytes, 16-byte
+ * aligned. T >= 0, 1 <= V < 2^31.
+ */
+bqd_status token_logprobs(const void* logits, int in_type, int64_t pitch, const int32_t* tokens, float* logprob,
+                          float* entropy, int32_t* top_ids, float* top_logprobs, int topk, void* workspace,
+                          size_t workspace_bytes, int64_t T, int64_t V, cudaStream_t stream);
+
+/* Bytes of device workspace token_logprobs needs for these sizes (0 if a size is out of range). */
+size_t token_logprobs_workspace_bytes(int64_t T, int64_t V, int topk);
+
 #ifdef __cplusplus
 }
 #endif
