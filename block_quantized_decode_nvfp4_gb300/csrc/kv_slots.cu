@@ -2,12 +2,16 @@
 //
 // Request r: have = ceil(c / p) pages, lacks need = ceil((c + n) / p) - have,
 // takes free pages first .. first + need - 1 (first: sum of the needs before
-// it). Token (r, j) sits at logical position c + j: slot = table[r][(c + j)
-// / p] * p + (c + j) % p. Integer work on a few hundred KB at most: what
-// bounds it is latency.
+// it). Token (r, j) sits at logical position c + j, block b = (c + j) / p:
+// its page is the table's for b < have, else free page first + b - have.
 //
-// Simple form: one CTA scans the requests a block at a time, then a warp per
-// request writes its pages and tokens.
+// Integer work on a few hundred KB at most: what bounds it is latency, so it
+// is one launch without a pass between the prefix sums and their use. Every
+// CTA scans all requests, kChunk at a time in shared memory (a second read of
+// the lengths costs less than a second launch), and meanwhile writes its own
+// share of the tokens, found by a search of the chunk's sums, and its own
+// share of the requests' new pages. Pages of new blocks are taken from the
+// list and not from the table, which another CTA may be writing.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -19,10 +23,14 @@ namespace bqd {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
+constexpr int kPer = 4;  // requests per thread and chunk
+constexpr int kChunk = kThreads * kPer;
+constexpr int kTokens = 1024;  // tokens per CTA at least (four per thread)
+constexpr int kMaxCtas = 152;
 
 struct Need {
-    int64_t c, n;  // cached and new tokens
+    int64_t c, n;        // cached and new tokens
     int64_t have, want;  // pages, within the table
 };
 
@@ -37,97 +45,119 @@ __device__ __forceinline__ Need need_of(const SlotsArgs& a, int64_t r)
     return x;
 }
 
-// Inclusive scan of (tokens, pages) over the block; totals in the last thread.
-__device__ __forceinline__ void block_scan(int64_t& t, int64_t& p, int64_t (*sh)[2])
-{
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-#pragma unroll
-    for (int d = 1; d < kWarp; d <<= 1) {
-        const int64_t a = __shfl_up_sync(0xFFFFFFFFu, t, d), b = __shfl_up_sync(0xFFFFFFFFu, p, d);
-        if (lane >= d) {
-            t += a;
-            p += b;
-        }
-    }
-    if (lane == kWarp - 1) {
-        sh[warp][0] = t;
-        sh[warp][1] = p;
-    }
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        t += sh[w][0];
-        p += sh[w][1];
-    }
-    __syncthreads();
-}
-
 __global__ void __launch_bounds__(kThreads) paged_slots_kernel(const SlotsArgs a)
 {
-    __shared__ int64_t sh[kThreads / kWarp][2], s_tok[kThreads], s_page[kThreads], s_base[2];
-    __shared__ int s_flags;
+    __shared__ int64_t s_tok[kChunk + 1], s_page[kChunk + 1];  // exclusive sums of the chunk's requests
+    __shared__ int64_t s_warp[kThreads / kWarp][2];
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    if (threadIdx.x == 0) {
-        s_base[0] = s_base[1] = 0;
-        s_flags = 0;
-    }
-    __syncthreads();
-    for (int64_t r0 = 0; r0 < a.R; r0 += kThreads) {
-        const int64_t r = r0 + threadIdx.x;
-        int64_t t = 0, p = 0;
-        if (r < a.R) {
-            const Need x = need_of(a, r);
-            t = x.n;
-            p = x.want - x.have;
-            if (((x.c + x.n + (int64_t(1) << a.page_shift) - 1) >> a.page_shift) > a.width && x.n > 0)
-                atomicOr(&s_flags, BQD_SLOTS_TABLE_FULL);
+    const int64_t share = (a.capacity + gridDim.x - 1) / gridDim.x;
+    const int64_t t0 = min(share * blockIdx.x, a.capacity), t1 = min(t0 + share, a.capacity);
+    int64_t tokens = 0, pages = 0;  // before the chunk
+    bool full = false;
+    for (int64_t r0 = 0; r0 < a.R; r0 += kChunk) {
+        const int count = static_cast<int>(min(static_cast<int64_t>(kChunk), a.R - r0));
+        int64_t tk[kPer], pg[kPer], st = 0, sp = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int k = threadIdx.x * kPer + i;
+            tk[i] = pg[i] = 0;
+            if (k < count) {
+                const Need x = need_of(a, r0 + k);
+                tk[i] = x.n;
+                pg[i] = x.want - x.have;
+                full |= x.n > 0 && ((x.c + x.n - 1) >> a.page_shift) >= a.width;
+            }
+            st += tk[i];
+            sp += pg[i];
         }
-        const int64_t t0 = t, p0 = p;
-        block_scan(t, p, sh);
-        const int64_t bt = s_base[0], bp = s_base[1];
-        s_tok[threadIdx.x] = bt + t - t0;
-        s_page[threadIdx.x] = bp + p - p0;
-        if (r < a.R) a.offsets[r] = static_cast<int32_t>(min(bt + t - t0, int64_t(0x7FFFFFFF)));
+        int64_t it = st, ip = sp;
+#pragma unroll
+        for (int d = 1; d < kWarp; d <<= 1) {
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, it, d), v = __shfl_up_sync(0xFFFFFFFFu, ip, d);
+            if (lane >= d) {
+                it += u;
+                ip += v;
+            }
+        }
+        if (lane == kWarp - 1) {
+            s_warp[warp][0] = it;
+            s_warp[warp][1] = ip;
+        }
         __syncthreads();
+        int64_t bt = tokens, bp = pages;
+        for (int w = 0; w < kThreads / kWarp; ++w) {
+            if (w < warp) {
+                bt += s_warp[w][0];
+                bp += s_warp[w][1];
+            }
+            tokens += s_warp[w][0];
+            pages += s_warp[w][1];
+        }
+        bt += it - st;
+        bp += ip - sp;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int k = threadIdx.x * kPer + i;
+            s_tok[k] = bt;
+            s_page[k] = bp;
+            bt += tk[i];
+            bp += pg[i];
+        }
         if (threadIdx.x == kThreads - 1) {
-            s_base[0] = bt + t;
-            s_base[1] = bp + p;
-        }
-        for (int i = warp; i < kThreads && r0 + i < a.R; i += kThreads / kWarp) {
-            const int64_t rr = r0 + i;
-            const Need x = need_of(a, rr);
-            int32_t* row = a.table + rr * a.width;
-            for (int64_t b = x.have + lane; b < x.want; b += kWarp) {
-                const int64_t f = s_page[i] + b - x.have;
-                row[b] = f < a.num_free ? a.free_pages[f] : -1;
-            }
-            __syncwarp();
-            for (int64_t j = lane; j < x.n; j += kWarp) {
-                const int64_t tk = s_tok[i] + j;
-                if (tk >= a.capacity) break;
-                const int64_t pos = x.c + j, b = pos >> a.page_shift;
-                int64_t slot = -1;
-                if (b < a.width) {
-                    const int32_t page = row[b];
-                    if (page >= 0)
-                        slot = (static_cast<int64_t>(page) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-                }
-                a.slots[tk] = slot;
-                a.positions[tk] = static_cast<int32_t>(x.c + (a.depths ? a.depths[tk] : j));
-            }
+            s_tok[kChunk] = bt;
+            s_page[kChunk] = bp;
         }
         __syncthreads();
+        if (blockIdx.x == 0)
+            for (int k = threadIdx.x; k < count; k += kThreads)
+                a.offsets[r0 + k] = static_cast<int32_t>(min(s_tok[k], int64_t(0x7FFFFFFF)));
+        // new pages of requests blockIdx.x, blockIdx.x + gridDim.x, ...
+        for (int64_t k = blockIdx.x + static_cast<int64_t>(warp) * gridDim.x; k < count;
+             k += static_cast<int64_t>(gridDim.x) * (kThreads / kWarp)) {
+            const int64_t f0 = s_page[k], need = s_page[k + 1] - f0;
+            if (need == 0) continue;
+            const Need x = need_of(a, r0 + k);
+            int32_t* row = a.table + (r0 + k) * a.width + x.have;
+            for (int64_t b = lane; b < need; b += kWarp) row[b] = f0 + b < a.num_free ? a.free_pages[f0 + b] : -1;
+        }
+        // this CTA's tokens of the chunk's requests
+        for (int64_t t = max(t0, s_tok[0]) + threadIdx.x; t < min(t1, s_tok[kChunk]); t += kThreads) {
+            int lo = 0, hi = count;  // the last k with s_tok[k] <= t: requests without tokens come before it
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s_tok[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const Need x = need_of(a, r0 + lo);
+            const int64_t j = t - s_tok[lo], b = (x.c + j) >> a.page_shift;
+            int64_t slot = -1;
+            if (b < a.width) {
+                const int64_t f = s_page[lo] + b - x.have;
+                const int32_t page = b < x.have ? a.table[(r0 + lo) * a.width + b] : f < a.num_free ? a.free_pages[f] : -1;
+                if (page >= 0)
+                    slot = (static_cast<int64_t>(page) << a.page_shift) + ((x.c + j) & ((1 << a.page_shift) - 1));
+            }
+            a.slots[t] = slot;
+            a.positions[t] = static_cast<int32_t>(x.c + (a.depths ? a.depths[t] : j));
+        }
+        __syncthreads();  // the next chunk overwrites the sums
     }
-    const int64_t total = s_base[0], pages = s_base[1];
-    for (int64_t t = total + threadIdx.x; t < a.capacity; t += kThreads) {
+    for (int64_t t = max(t0, tokens) + threadIdx.x; t < t1; t += kThreads) {
         a.slots[t] = -1;
         a.positions[t] = -1;
     }
-    if (threadIdx.x == 0) {
-        a.offsets[a.R] = static_cast<int32_t>(min(total, int64_t(0x7FFFFFFF)));
-        a.counts[0] = static_cast<int32_t>(min(total, int64_t(0x7FFFFFFF)));
-        a.counts[1] = static_cast<int32_t>(min(pages, a.num_free));
-        a.counts[2] = static_cast<int32_t>(min(max(pages - a.num_free, int64_t(0)), int64_t(0x7FFFFFFF)));
-        a.counts[3] = s_flags | (total > a.capacity ? BQD_SLOTS_TOKENS_CUT : 0);
+    if (blockIdx.x == 0) {
+        full = __syncthreads_or(full);
+        if (threadIdx.x == 0) {
+            const int64_t top = 0x7FFFFFFF;
+            a.offsets[a.R] = static_cast<int32_t>(min(tokens, top));
+            a.counts[0] = static_cast<int32_t>(min(tokens, top));
+            a.counts[1] = static_cast<int32_t>(min(pages, a.num_free));
+            a.counts[2] = static_cast<int32_t>(min(max(pages - a.num_free, int64_t(0)), top));
+            a.counts[3] = (full ? BQD_SLOTS_TABLE_FULL : 0) | (tokens > a.capacity ? BQD_SLOTS_TOKENS_CUT : 0);
+        }
     }
 }
 
@@ -135,7 +165,10 @@ __global__ void __launch_bounds__(kThreads) paged_slots_kernel(const SlotsArgs a
 
 cudaError_t launch_paged_slots(const SlotsArgs& a, cudaStream_t s)
 {
-    paged_slots_kernel<<<1, kThreads, 0, s>>>(a);
+    const int64_t by_tokens = (a.capacity + kTokens - 1) / kTokens, by_requests = (a.R + 63) / 64;
+    const int64_t want = by_tokens > by_requests ? by_tokens : by_requests;
+    const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want > kMaxCtas ? kMaxCtas : want);
+    paged_slots_kernel<<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

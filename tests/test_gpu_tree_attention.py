@@ -174,7 +174,8 @@ def test_tokens_of_no_request_are_not_written():
     cache, q, table, off, mask, scale, out, lse = case([30, 40], [2, 3], 8, 2, 64, seed=12)
     qq = torch.cat([q, q, q])
     o2, l2 = run_attention(cache, qq, table, [30, 40], off, None, scale)
-    assert torch.equal(o2[:5], out) and torch.all(o2[5:] == 7.0) and torch.all(l2[5:] == 7.0)
+    check_attention(cache, qq, table, [30, 40], off, None, scale, o2, l2, what="padded")
+    assert torch.all(o2[5:] == 7.0) and torch.all(l2[5:] == 7.0)
     # offsets past T are clamped to it
     o3, l3 = run_attention(cache, q, table, [30, 40], [0, 2, 9], None, scale)
     assert torch.isfinite(o3.float()).all()
