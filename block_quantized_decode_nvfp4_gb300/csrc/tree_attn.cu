@@ -1,113 +1,797 @@
 // tree_attn.cu -- attention of drafted tokens (a chain or a tree; one token:
 // decode) over the paged cache.
 //
-// out = sum_l p_l v_l / sum_l p_l with p_l = exp(s_l - m), s_l = scale q . k_l
-// over the visible l, m the running maximum: a partial result over some of
-// the tokens is (m, z = sum p, o = sum p v), and two of them join as
-// m = max(m1, m2), z = z1 e^(m1 - m) + z2 e^(m2 - m), o likewise. lse = m +
-// log z. A partial that saw nothing has m = -inf, z = 0.
+// out = sum_l p_l v_l / sum_l p_l with p_l = 2^(s_l - m), s_l = log2(e) scale
+// q . k_l over the visible l, m the running maximum: a partial result over
+// some of the tokens is (m, z = sum p, o = sum p v), and two of them join as
+// m = max(m1, m2), z = z1 2^(m1 - m) + z2 2^(m2 - m), o likewise. lse =
+// (m + log2 z) ln 2. A partial that saw nothing has m = -inf, z = 0.
 //
-// Simple form: one CTA per (token, query head), its warps taking tokens in
-// turn, a lane holding D / 32 elements; joined in shared memory.
+// Rows. The new tokens of a request times the G = Hq / Hkv query heads of a
+// kv head are the rows that share its keys and values: row = token * G + head
+// within the group. An item is (request, kv head, tile of 16 RG rows); the
+// bound is the one read of its keys and values (4 D rows flops a token
+// against 4 D bytes: below the tensor cores' rate for tens of rows).
+//
+// Split. Lengths are known to the device only, and a batch is ragged, so the
+// work of all items is laid out in units of kUnit tokens, and each of the
+// grid's CTAs (two per SM) takes an equal share of the line, at most two
+// items' ends among them being partial. A CTA writes the items that lie within its share; of an item
+// that crosses a boundary each CTA writes its part to the workspace, and a
+// second kernel joins them in ascending order (results do not depend on
+// timing). A CTA finds its place by one scan of the requests' unit counts.
+//
+// A CTA's four warps are 4 / RG token groups of RG warps, a warp per 16 rows.
+// A token group streams blocks of 16 tokens through a shared-memory ring of
+// its own (cp.async, 16 bytes a lane, waited for by the group alone: no
+// barrier of the whole CTA in the loop) and holds its own (m, z, o) in
+// registers; the groups join at the end of an item. Products run on
+// mma.sync m16n8k16: scores from q (A, registers) and keys (B), then the
+// probabilities, rounded, are the A operand as they lie in the score
+// accumulators, and the values B.
+//  - bf16 cache: B operands by ldmatrix (transposed for the values); p is
+//    rounded to bf16, its relative 2^-9 averages over the tokens.
+//  - E4M3 cache: codes become f16 (exact) after the shared-memory read, which
+//    takes 16 bytes of a token at a time: the order of the d along k, and of
+//    the output columns along n, is permuted to fit. q enters as f16 times a
+//    power of two per row that brings the row's largest element to 2^14
+//    (what that drops is below 2^-38 of it); p is scaled by 2^12 before its
+//    rounding to f16, so that p down to 2^-26 keeps 11 bits.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "attn.h"
 #include "common.cuh"
+#include "host_util.h"
+#include "stream.cuh"
 
 namespace bqd {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kGrid = 2 * 152;     // two CTAs per SM
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / kWarp;
+constexpr int kBlock = 16;         // tokens a token group takes at a time
+constexpr int kUnit = 64;          // tokens per unit of the split
+constexpr int kRows16 = 16;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kPShift = 12.f;    // E4M3: log2 of the scale p carries
 
-__device__ __forceinline__ float cache_elem(const bqd_kv_cache& c, const void* base, int64_t i)
+struct Meta {  // of a CTA's unfinished last item: whose it is and the last CTA with a part of it
+    int32_t r, h, tile, last;  // r = -1: none
+};
+
+__host__ __device__ constexpr size_t meta_bytes() { return (kGrid * sizeof(Meta) + 255) / 256 * 256; }
+__host__ __device__ constexpr size_t part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
+
+template <int D, int RG, bool F8>
+struct Shape {
+    static constexpr int kRows = kRows16 * RG;
+    static constexpr int kGroups = kWarps / RG;            // token groups
+    static constexpr int kRowBytes = D * (F8 ? 1 : 2);
+    static constexpr int kStage = 2 * kBlock * kRowBytes;  // K and V of one block
+    static constexpr int kMost = (F8 ? 64 : 96) * 1024 / (kGroups * kStage);
+    static constexpr int kStages = kMost < 3 ? 3 : kMost > 8 ? 8 : kMost;
+    static constexpr int kRing = kGroups * kStages * kStage;
+    static constexpr int kJoin = kWarps * kRows16 * D * 4;
+    static constexpr int kMain = kRing > kJoin ? kRing : kJoin;
+    static constexpr bool kQReg = D <= 128;                // q in registers (beside 64 of o)
+    static constexpr int kQBytes = kQReg ? 0 : RG * (D / 16) * 512;
+    static constexpr int kSmem = kMain + kQBytes;
+};
+
+struct Req {
+    int o0, n;      // first token, new tokens
+    int64_t ctx;    // cached tokens
+    int64_t len;    // tokens to look at
+    int tiles;
+    int64_t nb;     // units per item
+};
+
+__device__ __forceinline__ Req request(const AttnArgs& a, int64_t r, int rows)
 {
-    return c.type == BQD_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i])
-                              : e4m3_to_float(static_cast<const uint8_t*>(base)[i]);
+    Req q;
+    const int T = static_cast<int>(a.T);
+    q.o0 = min(max(a.offsets[r], 0), T);
+    q.n = min(max(a.offsets[r + 1], q.o0), T) - q.o0;
+    q.ctx = max(a.context[r], 0);
+    q.len = min(q.ctx + q.n, a.width * a.cache.page_size);
+    q.tiles = static_cast<int>((static_cast<int64_t>(q.n) * (a.Hq / a.cache.heads) + rows - 1) / rows);
+    q.nb = max(int64_t(1), (q.len + kUnit - 1) / kUnit);
+    return q;
 }
 
-__global__ void __launch_bounds__(kThreads) tree_attn_kernel(const AttnArgs a)
+__device__ __forceinline__ int64_t units_of(const AttnArgs& a, int64_t r, int rows)
 {
-    __shared__ float s_m[kWarps], s_z[kWarps], s_o[kWarps][256];
+    const Req q = request(a, r, rows);
+    return q.nb * q.tiles * a.cache.heads;
+}
+
+// Total units, and the request that holds unit `start` of CTA blockIdx.x's
+// share with the units before it. Each thread sums a run of requests.
+__device__ __forceinline__ void find_share(const AttnArgs& a, int rows, int64_t* sh, int64_t& start, int64_t& end,
+                                           int64_t& total, int64_t& r, int64_t& base)
+{
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, D = a.cache.head_dim, E = D / kWarp, kvh = h / (a.Hq / a.cache.heads);
-    // the request of token t: the last r with offsets[r] <= t < offsets[r + 1]
-    int64_t lo = 0, hi = a.R;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.offsets[mid + 1] <= t)
-            lo = mid + 1;
-        else
-            hi = mid;
+    const int64_t per = (a.R + kThreads - 1) / kThreads;
+    const int64_t r0 = min(threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
+    int64_t mine = 0;
+    for (int64_t i = r0; i < r1; ++i) mine += units_of(a, i, rows);
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < kWarp; d <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += v;
     }
-    if (lo >= a.R || t < a.offsets[lo]) return;
-    const int64_t r = lo, o0 = max(0, a.offsets[r]), n = min(static_cast<int64_t>(a.offsets[r + 1]), a.T) - o0;
-    const int64_t i = t - o0, ctx = max(0, a.context[r]);
-    float q[8], o[8], m = -INFINITY, z = 0.f;
-    const float ks = (a.cache.type == BQD_E4M3 && a.cache.k_scale) ? a.cache.k_scale[kvh] : 1.f;
-    const float vs = (a.cache.type == BQD_E4M3 && a.cache.v_scale) ? a.cache.v_scale[kvh] : 1.f;
-    for (int e = 0; e < 8; ++e) {
-        o[e] = 0.f;
-        q[e] = e < E ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.q)[t * a.q_pitch + h * D + lane * E + e])
-                     : 0.f;
-    }
-    for (int64_t l = warp; l < ctx + n; l += kWarps) {
-        if (l >= ctx) {
-            const int64_t j = l - ctx;
-            const bool see = a.mask ? (j / 64 < a.mask_words && ((a.mask[t * a.mask_words + j / 64] >> (j % 64)) & 1))
-                                    : j <= i;
-            if (!see) continue;
-        }
-        const int64_t b = l / a.cache.page_size;
-        if (b >= a.width) break;
-        const int32_t page = a.table[r * a.width + b];
-        if (page < 0 || page >= a.cache.num_pages) continue;
-        const int64_t at = page * a.cache.page_stride + l % a.cache.page_size * a.cache.token_stride +
-                           kvh * a.cache.head_stride + lane * E;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += q[e] * cache_elem(a.cache, a.cache.k, at + e);
-        s = warp_sum(s) * (a.scale * ks);
-        const float mn = fmaxf(m, s);
-        const float f = m == -INFINITY ? 0.f : expf(m - mn);  // a first token of score -inf: exp(nan) below
-        const float p = s == -INFINITY ? 0.f : expf(s - mn);
-        z = z * f + p;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * cache_elem(a.cache, a.cache.v, at + e);
-        m = mn;
-    }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_z[warp] = z;
-    }
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    if (lane == kWarp - 1) sh[warp] = incl;
     __syncthreads();
-    float mm = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w]);
-    float zz = 0.f, f[kWarps];
+    total = 0;
+    int64_t before = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        f[w] = s_m[w] == -INFINITY ? 0.f : expf(s_m[w] - mm);
-        zz += s_z[w] * f[w];
+        if (w < warp) before += sh[w];
+        total += sh[w];
     }
-    for (int d = threadIdx.x; d < D; d += kThreads) {
-        float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += s_o[w][d] * f[w];
-        a.out[(t * a.Hq + h) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(zz == 0.f ? 0.f : v * vs / zz));
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);  // each of them has a unit at least
+    start = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+    end = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    const int64_t first = before + incl - mine;
+    if (start < end && start >= first && start < first + mine) {
+        int64_t b = first, i = r0;
+        for (;; ++i) {
+            const int64_t u = units_of(a, i, rows);
+            if (start < b + u) break;
+            b += u;
+        }
+        sh[kWarps] = i;
+        sh[kWarps + 1] = b;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[t * a.Hq + h] = zz == 0.f ? -INFINITY : mm + logf(zz);
+    __syncthreads();
+    r = sh[kWarps];
+    base = sh[kWarps + 1];
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool F8>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (F8)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+            "%2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+            "%1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F8>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if (F8) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Byte offset of 16-byte chunk `ch` of token row `row` in a block. The chunk
+// index is permuted by the row so that the reads of a phase fall into
+// different banks: ldmatrix takes one chunk of 8 rows; the E4M3 reads take
+// chunks c .. c + 3 of two adjacent rows (keys) or two chunks of every other
+// row (values); 64-byte rows share a 128-byte line in pairs.
+template <int RB, bool F8>
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch)
+{
+    if (!F8) return static_cast<uint32_t>(row * RB + ((ch ^ (row & 7)) << 4));
+    const int f = ((row >> 1) & 3) << 1;
+    if (RB == 64) return static_cast<uint32_t>((row >> 1) * 128 + (((((row & 1) << 2) | ch) ^ f) << 4));
+    return static_cast<uint32_t>(row * RB + ((ch ^ f ^ ((row & 1) << 2)) << 4));
+}
+
+// Whether query token i of the request sees draft j (j < 0: a cached token).
+__device__ __forceinline__ bool sees(const AttnArgs& a, int64_t t, int i, int64_t j)
+{
+    if (j < 0) return true;
+    if (!a.mask) return j <= i;
+    return (j >> 6) < a.mask_words && ((a.mask[t * a.mask_words + (j >> 6)] >> (j & 63)) & 1);
+}
+
+template <int D, int RG, bool F8>
+__global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a)
+{
+    using S = Shape<D, RG, F8>;
+    constexpr int NT = D / 8;     // n tiles of the output; d of column n of tile j:
+    constexpr int KS = D / 16;    // k steps of the scores
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_find[kWarps + 2];
+    __shared__ uint32_t s_vis[kWarps][8];
+    __shared__ float s_m[kWarps][kRows16], s_z[kWarps][kRows16];
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    const int rg = warp % RG, tg = warp / RG;  // row group, token group
+    const int g = lane >> 2, c = lane & 3;     // row (and column) and k positions in mma fragments
+    const int G = a.Hq / a.cache.heads;
+    const uint32_t ring = smem_u32(smem) + tg * (S::kStages * S::kStage);
+
+    int64_t u, end, total, r, base;
+    find_share(a, S::kRows, s_find, u, end, total, r, base);
+    Meta* meta = static_cast<Meta*>(a.ws);
+    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + meta_bytes());
+    if (threadIdx.x == 0) meta[blockIdx.x].r = -1;
+    int page_shift = 31 - __clz(a.cache.page_size);
+
+    while (u < end) {
+        const Req q = request(a, r, S::kRows);
+        const int64_t item = (u - base) / q.nb, b0 = (u - base) % q.nb, cnt = min(q.nb - b0, end - u);
+        const int h = static_cast<int>(item / q.tiles), tile = static_cast<int>(item % q.tiles);
+        const int64_t l0 = b0 * kUnit, l1 = min((b0 + cnt) * kUnit, q.len);
+        const int32_t* table = a.table + r * a.width;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(q.n) * G - static_cast<int64_t>(tile) * S::kRows,
+                                              static_cast<int64_t>(S::kRows)));
+        // this thread's two rows
+        const int row0 = tile * S::kRows + rg * kRows16 + g, row1 = row0 + 8;
+        const int i0 = row0 / G, i1 = row1 / G;
+        const bool live0 = i0 < q.n, live1 = i1 < q.n;
+        const int64_t t0 = q.o0 + (live0 ? i0 : 0), t1 = q.o0 + (live1 ? i1 : 0);
+        const uint16_t* q0 = a.q + t0 * a.q_pitch + static_cast<int64_t>(h * G + row0 % G) * D;
+        const uint16_t* q1 = a.q + t1 * a.q_pitch + static_cast<int64_t>(h * G + row1 % G) * D;
+        float c0 = a.scale * kLog2e, c1 = c0;  // score to log2 units, per row
+
+        // ---- q fragments
+        uint32_t qf[S::kQReg ? KS : 1][4];
+        const uint32_t qsm = smem_u32(smem) + S::kMain + (rg * KS * 32 + lane) * 16;
+        {
+            uint32_t f[KS][4];
+            if (F8) {
+                float mx0 = 0.f, mx1 = 0.f;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int d = 64 * (s / 4) + 16 * c + 4 * (s % 4);
+                    const uint2 x = live0 ? *reinterpret_cast<const uint2*>(q0 + d) : make_uint2(0, 0);
+                    const uint2 y = live1 ? *reinterpret_cast<const uint2*>(q1 + d) : make_uint2(0, 0);
+                    f[s][0] = x.x, f[s][2] = x.y, f[s][1] = y.x, f[s][3] = y.y;
+                    mx0 = fmaxf(mx0, fmaxf(fmaxf(fabsf(bf16_lo(x.x)), fabsf(bf16_hi(x.x))),
+                                           fmaxf(fabsf(bf16_lo(x.y)), fabsf(bf16_hi(x.y)))));
+                    mx1 = fmaxf(mx1, fmaxf(fmaxf(fabsf(bf16_lo(y.x)), fabsf(bf16_hi(y.x))),
+                                           fmaxf(fabsf(bf16_lo(y.y)), fabsf(bf16_hi(y.y)))));
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, o));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, o));
+                }
+                // 2^(14 - e) for a largest element of [2^e, 2^(e + 1)); e kept within [-100, 100]
+                const int e0 = min(max(static_cast<int>(__float_as_uint(mx0) >> 23), 27), 227);
+                const int e1 = min(max(static_cast<int>(__float_as_uint(mx1) >> 23), 27), 227);
+                const float up0 = __uint_as_float((127 + 14 + 127 - e0) << 23), up1 = __uint_as_float((127 + 14 + 127 - e1) << 23);
+                c0 *= __uint_as_float((e0 - 14) << 23);
+                c1 *= __uint_as_float((e1 - 14) << 23);
+                if (a.cache.k_scale) {
+                    c0 *= a.cache.k_scale[h];
+                    c1 *= a.cache.k_scale[h];
+                }
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float up = (e & 1) ? up1 : up0;
+                        f[s][e] = pack2<true>(bf16_lo(f[s][e]) * up, bf16_hi(f[s][e]) * up);
+                    }
+            } else {
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int d = 16 * s + 2 * c;
+                    f[s][0] = live0 ? *reinterpret_cast<const uint32_t*>(q0 + d) : 0u;
+                    f[s][1] = live1 ? *reinterpret_cast<const uint32_t*>(q1 + d) : 0u;
+                    f[s][2] = live0 ? *reinterpret_cast<const uint32_t*>(q0 + d + 8) : 0u;
+                    f[s][3] = live1 ? *reinterpret_cast<const uint32_t*>(q1 + d + 8) : 0u;
+                }
+            }
+            if (S::kQReg) {
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qf[S::kQReg ? s : 0][e] = f[s][e];
+            } else if (tg == 0) {
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    *reinterpret_cast<uint4*>(smem + S::kMain + ((rg * KS + s) * 32 + lane) * 16) =
+                        make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+            }
+        }
+        if (!S::kQReg) __syncthreads();
+
+        // ---- the token group's stream
+        const int64_t first = l0 + tg * kBlock;
+        const int nblk = first < l1 ? static_cast<int>((l1 - first + S::kGroups * kBlock - 1) / (S::kGroups * kBlock)) : 0;
+        auto entry = [&](int64_t l) -> int32_t { return l < l1 ? table[l >> page_shift] : -1; };
+        int32_t ent = entry(first + (lane & 15));  // table entry of the next block to fetch, a token per lane
+        auto fetch = [&](int i) {  // block i into its stage
+            if (i < nblk) {
+                const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock) + (lane & 15);
+                const bool ok = ent >= 0 && ent < a.cache.num_pages;
+                const int64_t off = ok ? (ent * a.cache.page_stride + (l & (a.cache.page_size - 1)) * a.cache.token_stride +
+                                          h * a.cache.head_stride) * (F8 ? 1 : 2)
+                                       : 0;
+                const uint32_t vis = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+                ent = entry(l + S::kGroups * kBlock);
+                if (rg == 0 && lane == 0) s_vis[tg][i % S::kStages] = vis;
+                const uint32_t st = ring + (i % S::kStages) * S::kStage;
+                constexpr int CPR = S::kRowBytes / 16;  // chunks per row
+#pragma unroll
+                for (int it = 0; it < kBlock * CPR / (kWarp * RG); ++it) {
+                    const int ch = (it * RG + rg) * kWarp + lane, row = ch / CPR, cc = ch % CPR;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row) + cc * 16;
+                    const bool real = (vis >> row) & 1;
+                    const uint32_t at = st + chunk_at<S::kRowBytes, F8>(row, cc);
+                    cp_async16(at, static_cast<const uint8_t*>(a.cache.k) + o, real);
+                    cp_async16(at + S::kStage / 2, static_cast<const uint8_t*>(a.cache.v) + o, real);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
+
+        float o[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f;  // z: this lane's columns only
+
+        for (int i = 0; i < nblk; ++i) {
+            cp_wait<S::kStages - 2>();
+            if (RG == 1)
+                __syncwarp();
+            else
+                named_sync(1 + tg, RG * kWarp);
+            fetch(i + S::kStages - 1);
+            const uint32_t ks = ring + (i % S::kStages) * S::kStage, vs = ks + S::kStage / 2;
+            const uint32_t vis = s_vis[tg][i % S::kStages];
+            const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock);
+            float s[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+            // scores
+            if (!F8) {
+                const int mrow = (lane & 7) + ((lane >> 4) << 3), mch = (lane >> 3) & 1;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4], qa[4];
+                    ldsm4(ks + chunk_at<S::kRowBytes, F8>(mrow, 2 * k + mch), b);
+                    if (S::kQReg) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) qa[e] = qf[S::kQReg ? k : 0][e];
+                    } else {
+                        const uint4 x = lds128(qsm + k * 512);
+                        qa[0] = x.x, qa[1] = x.y, qa[2] = x.z, qa[3] = x.w;
+                    }
+                    mma16816<F8>(s[0], qa, b[0], b[1]);
+                    mma16816<F8>(s[1], qa, b[2], b[3]);
+                }
+            } else {
+#pragma unroll
+                for (int k4 = 0; k4 < KS / 4; ++k4) {
+                    const uint4 x = lds128(ks + chunk_at<S::kRowBytes, F8>(g, 4 * k4 + c));
+                    const uint4 y = lds128(ks + chunk_at<S::kRowBytes, F8>(g + 8, 4 * k4 + c));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e4 = 0; e4 < 4; ++e4) {
+                        const int k = 4 * k4 + e4;
+                        uint32_t qa[4];
+                        if (S::kQReg) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) qa[e] = qf[S::kQReg ? k : 0][e];
+                        } else {
+                            const uint4 w = lds128(qsm + k * 512);
+                            qa[0] = w.x, qa[1] = w.y, qa[2] = w.z, qa[3] = w.w;
+                        }
+                        mma16816<F8>(s[0], qa, e4m3x2_to_f16x2(xs[e4] & 0xFFFFu), e4m3x2_to_f16x2(xs[e4] >> 16));
+                        mma16816<F8>(s[1], qa, e4m3x2_to_f16x2(ys[e4] & 0xFFFFu), e4m3x2_to_f16x2(ys[e4] >> 16));
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                s[nt][0] *= c0;
+                s[nt][1] *= c0;
+                s[nt][2] *= c1;
+                s[nt][3] *= c1;
+            }
+            // what is hidden
+            const bool drafts = l + kBlock > q.ctx;
+            if (vis != 0xFFFFu || drafts) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int tok = 8 * nt + 2 * c + e;
+                        const bool v = (vis >> tok) & 1;
+                        const int64_t j = l + tok - q.ctx;
+                        if (!v || !sees(a, t0, i0, j)) s[nt][e] = -INFINITY;
+                        if (!v || !sees(a, t1, i1, j)) s[nt][2 + e] = -INFINITY;
+                    }
+            }
+            // running maximum
+            float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+            float n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1) {
+                n0 = fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, x));
+                n1 = fmaxf(n1, __shfl_xor_sync(0xFFFFFFFFu, n1, x));
+            }
+            n0 = fmaxf(n0, m0);
+            n1 = fmaxf(n1, m1);
+            if (__any_sync(0xFFFFFFFFu, n0 != m0 || n1 != m1)) {
+                const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+                z0 *= f0;
+                z1 *= f1;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][0] *= f0;
+                    o[j][1] *= f0;
+                    o[j][2] *= f1;
+                    o[j][3] *= f1;
+                }
+                m0 = n0;
+                m1 = n1;
+            }
+            const float sub0 = (m0 == -INFINITY ? 0.f : m0) - (F8 ? kPShift : 0.f);
+            const float sub1 = (m1 == -INFINITY ? 0.f : m1) - (F8 ? kPShift : 0.f);
+            uint32_t pa[4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const float p0 = ex2(s[nt][0] - sub0), p1 = ex2(s[nt][1] - sub0);
+                const float p2 = ex2(s[nt][2] - sub1), p3 = ex2(s[nt][3] - sub1);
+                z0 += p0 + p1;
+                z1 += p2 + p3;
+                pa[2 * nt] = pack2<F8>(p0, p1);
+                pa[2 * nt + 1] = pack2<F8>(p2, p3);
+            }
+            // A draft's value may be infinite or NaN and hidden from some of
+            // the rows, where 0 * v must count nothing: such elements leave
+            // the product (zeros in the stage) and are added to the rows that
+            // see them. Looked for in blocks with drafts only; every token
+            // before them is seen by all rows.
+            if (drafts) {
+                bool odd = false;
+                constexpr int CPR = S::kRowBytes / 16;
+                for (int ch = lane; ch < kBlock * CPR; ch += kWarp) {
+                    const uint4 x = lds128(vs + chunk_at<S::kRowBytes, F8>(ch / CPR, ch % CPR));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int b = 0; b < (F8 ? 4 : 2); ++b)
+                            odd |= F8 ? ((w[e] >> (8 * b)) & 0x7Fu) == 0x7Fu : ((w[e] >> (16 * b)) & 0x7F80u) == 0x7F80u;
+                }
+                if (__any_sync(0xFFFFFFFFu, odd)) {
+                    for (int tok = 0; tok < kBlock; ++tok) {
+                        if (!((vis >> tok) & 1)) continue;
+                        const bool see0 = sees(a, t0, i0, l + tok - q.ctx), see1 = sees(a, t1, i1, l + tok - q.ctx);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int d = F8 ? NT * (2 * c + e) + j : 8 * j + 2 * c + e;
+                                float v;
+                                const uint32_t at = vs + (F8 ? chunk_at<S::kRowBytes, F8>(tok, d / 16) + d % 16
+                                                             : chunk_at<S::kRowBytes, F8>(tok, d / 8) + d % 8 * 2);
+                                if (F8) {
+                                    uint32_t b;
+                                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(at) : "memory");
+                                    v = e4m3_to_float(b);
+                                } else {
+                                    uint16_t b;
+                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(at) : "memory");
+                                    v = __uint_as_float(static_cast<uint32_t>(b) << 16);
+                                }
+                                if (!isfinite(v)) {
+                                    if (see0) o[j][e] += v;
+                                    if (see1) o[j][2 + e] += v;
+                                }
+                            }
+                    }
+                    // all reads above come before the zeros below
+                    if (RG == 1)
+                        __syncwarp();
+                    else
+                        named_sync(1 + tg, RG * kWarp);
+                    if (rg == 0)
+                        for (int x = lane; x < S::kStage / 2 / 4; x += kWarp) {
+                            uint32_t w;
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vs + 4 * x) : "memory");
+#pragma unroll
+                            for (int b = 0; b < (F8 ? 4 : 2); ++b)
+                                if (F8 ? ((w >> (8 * b)) & 0x7Fu) == 0x7Fu : ((w >> (16 * b)) & 0x7F80u) == 0x7F80u)
+                                    w &= ~((F8 ? 0xFFu : 0xFFFFu) << (F8 ? 8 * b : 16 * b));
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vs + 4 * x), "r"(w) : "memory");
+                        }
+                    if (RG == 1)
+                        __syncwarp();
+                    else
+                        named_sync(1 + tg, RG * kWarp);
+                }
+            }
+            // o += p v
+            if (!F8) {
+                const int mrow = (lane & 7) + (((lane >> 3) & 1) << 3), mch = lane >> 4;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4];
+                    ldsm4t(vs + chunk_at<S::kRowBytes, F8>(mrow, 2 * k + mch), b);
+                    mma16816<F8>(o[2 * k], pa, b[0], b[1]);
+                    mma16816<F8>(o[2 * k + 1], pa, b[2], b[3]);
+                }
+            } else {
+                // tokens 2c, 2c + 1, 2c + 8, 2c + 9; the NT d from NT g
+                constexpr int W = NT / 4;       // words per token
+                constexpr int WL = W < 4 ? W : 4;  // words per load
+#pragma unroll
+                for (int w0 = 0; w0 < W; w0 += WL) {
+                    uint32_t x[4][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = 2 * c + (e & 1) + 8 * (e >> 1), byte = NT * g + 4 * w0;
+                        const uint32_t at = vs + chunk_at<S::kRowBytes, F8>(tok, byte / 16) + byte % 16;
+                        if (WL == 4) {
+                            const uint4 y = lds128(at);
+                            x[e][0] = y.x, x[e][1] = y.y, x[e][2] = y.z, x[e][3] = y.w;
+                        } else {
+                            const uint2 y = lds64(at);
+                            x[e][0] = y.x, x[e][1] = y.y;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < WL; ++w) {
+                        const uint32_t lo0 = __byte_perm(x[0][w], x[1][w], 0x5140), hi0 = __byte_perm(x[0][w], x[1][w], 0x7362);
+                        const uint32_t lo1 = __byte_perm(x[2][w], x[3][w], 0x5140), hi1 = __byte_perm(x[2][w], x[3][w], 0x7362);
+                        const int j = 4 * (w0 + w);
+                        mma16816<F8>(o[j], pa, e4m3x2_to_f16x2(lo0 & 0xFFFFu), e4m3x2_to_f16x2(lo1 & 0xFFFFu));
+                        mma16816<F8>(o[j + 1], pa, e4m3x2_to_f16x2(lo0 >> 16), e4m3x2_to_f16x2(lo1 >> 16));
+                        mma16816<F8>(o[j + 2], pa, e4m3x2_to_f16x2(hi0 & 0xFFFFu), e4m3x2_to_f16x2(hi1 & 0xFFFFu));
+                        mma16816<F8>(o[j + 3], pa, e4m3x2_to_f16x2(hi0 >> 16), e4m3x2_to_f16x2(hi1 >> 16));
+                    }
+                }
+            }
+        }
+
+        // ---- join the token groups: everything of a warp to shared memory
+        cp_wait<0>();
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+            z0 += __shfl_xor_sync(0xFFFFFFFFu, z0, x);
+            z1 += __shfl_xor_sync(0xFFFFFFFFu, z1, x);
+        }
+        __syncthreads();  // the rings are read no more
+        if (c == 0) {
+            s_m[warp][g] = m0;
+            s_m[warp][g + 8] = m1;
+            s_z[warp][g] = z0;
+            s_z[warp][g + 8] = z1;
+        }
+        float* join = reinterpret_cast<float*>(smem) + warp * (kRows16 * D);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d = F8 ? NT * (2 * c + e) + j : 8 * j + 2 * c + e;
+                join[g * D + d] = o[j][e];
+                join[(g + 8) * D + d] = o[j][2 + e];
+            }
+        __syncthreads();
+        const bool whole = b0 == 0 && cnt == q.nb;
+        float* part = parts + (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * part_floats(S::kRows, D);
+        const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[h] : 1.f;
+        for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), d = x % (D / 4) * 4, rw = row / kRows16, rr = row % kRows16;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < S::kGroups; ++w) m = fmaxf(m, s_m[w * RG + rw][rr]);
+            float z = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < S::kGroups; ++w) {
+                const float mw = s_m[w * RG + rw][rr];
+                const float f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mw - m);
+                const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
+                                                                  ((w * RG + rw) * kRows16 + rr) * D + d);
+                z += s_z[w * RG + rw][rr] * f;
+                v.x += y.x * f;
+                v.y += y.y * f;
+                v.z += y.z * f;
+                v.w += y.w * f;
+            }
+            if (whole) {
+                const int grow = tile * S::kRows + row;
+                const int64_t at = (q.o0 + grow / G) * static_cast<int64_t>(a.Hq) + h * G + grow % G;
+                const float k = z == 0.f ? 0.f : vscale / z;
+                uint2 w;
+                w.x = pack2<false>(z == 0.f ? 0.f : v.x * k, z == 0.f ? 0.f : v.y * k);
+                w.y = pack2<false>(z == 0.f ? 0.f : v.z * k, z == 0.f ? 0.f : v.w * k);
+                *reinterpret_cast<uint2*>(a.out + at * D + d) = w;
+                if (d == 0 && a.lse)
+                    a.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z) - (F8 ? kPShift : 0.f)) * kLn2;
+            } else {
+                *reinterpret_cast<float4*>(part + row * D + d) = v;
+                if (d == 0) {
+                    part[S::kRows * D + row] = m;
+                    part[S::kRows * D + S::kRows + row] = z;
+                }
+            }
+        }
+        if (b0 == 0 && !whole && threadIdx.x == 0) {
+            // the last CTA whose share begins before the item's end
+            const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), ends = u + q.nb;
+            Meta md;
+            md.r = static_cast<int32_t>(r);
+            md.h = h;
+            md.tile = tile;
+            md.last = static_cast<int32_t>((ends * ctas + total - 1) / total - 1);
+            meta[blockIdx.x] = md;
+        }
+        __syncthreads();
+        u += cnt;
+        if (u < end) {
+            int64_t next = base + q.nb * q.tiles * a.cache.heads;
+            while (u == next) {  // the next request with rows
+                ++r;
+                base = next;
+                next += units_of(a, r, S::kRows);
+            }
+        }
+    }
+}
+
+// Joins the parts of the item that CTA blockIdx.x of the first kernel began
+// and did not finish: its own second part, then the first parts of the CTAs
+// after it, in order. blockIdx.y: four rows each, D / 4 threads a row.
+template <int D, int RG, bool F8>
+__global__ void __launch_bounds__(D) tree_attn_join_kernel(const AttnArgs a)
+{
+    using S = Shape<D, RG, F8>;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Meta md = static_cast<const Meta*>(a.ws)[blockIdx.x];
+    if (md.r < 0) return;
+    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + meta_bytes());
+    const int row = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    const Req q = request(a, md.r, S::kRows);
+    const int G = a.Hq / a.cache.heads;
+    const int64_t grow = static_cast<int64_t>(md.tile) * S::kRows + row;
+    if (grow >= static_cast<int64_t>(q.n) * G) return;
+    constexpr size_t P = part_floats(S::kRows, D);
+    const int b = blockIdx.x;
+    auto part = [&](int k) { return parts + (k == b ? 2 * k + 1 : 2 * k) * P; };
+    float m = -INFINITY;
+    for (int k = b; k <= md.last; ++k) m = fmaxf(m, part(k)[S::kRows * D + row]);
+    float z = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = b; k <= md.last; ++k) {
+        const float* p = part(k);
+        const float mw = p[S::kRows * D + row];
+        const float f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mw - m);
+        const float4 y = *reinterpret_cast<const float4*>(p + row * D + d);
+        z += p[S::kRows * D + S::kRows + row] * f;
+        v.x += y.x * f;
+        v.y += y.y * f;
+        v.z += y.z * f;
+        v.w += y.w * f;
+    }
+    const int64_t at = (q.o0 + grow / G) * static_cast<int64_t>(a.Hq) + md.h * G + grow % G;
+    const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[md.h] : 1.f;
+    const float k = z == 0.f ? 0.f : vscale / z;
+    uint2 w;
+    w.x = pack2<false>(z == 0.f ? 0.f : v.x * k, z == 0.f ? 0.f : v.y * k);
+    w.y = pack2<false>(z == 0.f ? 0.f : v.z * k, z == 0.f ? 0.f : v.w * k);
+    *reinterpret_cast<uint2*>(a.out + at * D + d) = w;
+    if (d == 0 && a.lse) a.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z) - (F8 ? kPShift : 0.f)) * kLn2;
+}
+
+// Row groups: 16 rows unless the requests have more on average (two halve the
+// reads of the keys and values for wide drafts).
+int row_groups(int64_t R, int64_t T, int Hq, int Hkv) { return T * (Hq / Hkv) > 16 * R ? 2 : 1; }
+
+template <int D, int RG, bool F8>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s)
+{
+    using S = Shape<D, RG, F8>;
+    static OccCache occ;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    blocks_per_sm(occ, reinterpret_cast<const void*>(&tree_attn_kernel<D, RG, F8>), dev, kThreads, S::kSmem);
+    tree_attn_kernel<D, RG, F8><<<kGrid, kThreads, S::kSmem, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kGrid, S::kRows / 4);
+    cfg.blockDim = dim3(D);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, RG, F8>, a);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
+{
+    const bool f8 = a.cache.type == BQD_E4M3;
+    if (row_groups(a.R, a.T, a.Hq, a.cache.heads) == 1) return f8 ? launch<D, 1, true>(a, s) : launch<D, 1, false>(a, s);
+    return f8 ? launch<D, 2, true>(a, s) : launch<D, 2, false>(a, s);
 }
 
 }  // namespace
 
-size_t tree_attention_ws(int64_t, int64_t, int, int, int) { return 16; }
+size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D)
+{
+    const int rows = kRows16 * row_groups(R, T, Hq, Hkv);
+    return meta_bytes() + 2 * kGrid * part_floats(rows, D) * sizeof(float);
+}
 
 cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t s)
 {
-    tree_attn_kernel<<<dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(a.Hq)), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    switch (a.cache.head_dim) {
+        case 64: return launch_d<64>(a, s);
+        case 128: return launch_d<128>(a, s);
+        default: return launch_d<256>(a, s);
+    }
 }
 
 }  // namespace bqd
