@@ -62,5 +62,6 @@ struct LogprobArgs {
 };
 size_t token_logprobs_ws(int64_t T, int64_t V, int topk);
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int in_type, cudaStream_t s);
+cudaError_t read_and_clear_logprobs_error(unsigned int* out);
 
 }  // namespace bqd

@@ -5,14 +5,17 @@
 // rot elements turn by their position's angles, (a, b) -> (a cos - b sin,
 // b cos + a sin). Each input element is read once and each output written
 // once; the bound is memory (a launch's latency for the few tokens of a
-// decode step).
+// decode step), and next to it the instructions per element.
 //
-// A warp takes kHeads consecutive heads of a token, all loaded before the
-// first is used, with D / 32 consecutive elements of each head in a lane: the
-// mean square is one warp sum, and the other element of a rotated pair is the
-// lane's own (pairs) or sits rot / 2 elements away in one lane (halves:
-// rot / 2 is a multiple of the lane's share). The token's cosines and sines
-// are read once for all of its heads in the warp.
+// A head takes D / 16 lanes of 16 elements, so a warp does 2, 4 or 8 heads of
+// a token in a step, and the shuffles, addresses and the square root are
+// shared by 16 elements a lane. The D / 2 pairs of a head (the rotated ones,
+// then the rest two by two) go to its lanes in order, eight each: both ends
+// of a pair are in one lane, the rotation needs no exchange, and a lane's
+// elements are two runs of eight (rot / 2 is a multiple of 8). Arithmetic is
+// two elements an instruction. A lane keeps the weights of its places from
+// step to step; a step's loads are issued before the step before it is
+// worked on.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,242 +23,242 @@
 
 #include "attn.h"
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace bqd {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kHeads = 4;
+constexpr int kThreads = 256;
+constexpr int kRun = 8;  // elements of one of a lane's two runs
 
-template <int N>
-__device__ __forceinline__ void load_f32(const float* p, float (&x)[N])
-{
-    if constexpr (N == 1) {
-        x[0] = __ldg(p);
-    } else if constexpr (N == 2) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(p));
-        x[0] = v.x, x[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-        }
-    }
-}
-
-// E elements of a row as they come: raw words, unpacked later so that a
-// warp's loads are all in flight together.
-template <typename T, int E>
+// Eight elements of a row as they come.
+template <typename T>
 struct Raw {
-    static constexpr int kWords = E * static_cast<int>(sizeof(T)) / 4;
-    uint32_t w[kWords];
+    static constexpr int kVec = kRun * static_cast<int>(sizeof(T)) / 16;
+    uint4 v[kVec];
     __device__ __forceinline__ void load(const T* p)
     {
-        if constexpr (kWords == 1) {
-            w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-        } else if constexpr (kWords == 2) {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
-            w[0] = v.x, w[1] = v.y;
-        } else {
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-            }
-        }
+        for (int i = 0; i < kVec; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
     }
-    __device__ __forceinline__ void get(float (&x)[E]) const
+    __device__ __forceinline__ void get(uint64_t (&x)[kRun / 2]) const
     {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if constexpr (sizeof(T) == 4)
-                x[i] = __uint_as_float(w[i]);
-            else
-                x[i] = (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+            for (int i = 0; i < kVec; ++i) {
+                x[2 * i] = pack(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                x[2 * i + 1] = pack(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
+            }
+        } else {
+            x[0] = pack(bf16_lo(v[0].x), bf16_hi(v[0].x));
+            x[1] = pack(bf16_lo(v[0].y), bf16_hi(v[0].y));
+            x[2] = pack(bf16_lo(v[0].z), bf16_hi(v[0].z));
+            x[3] = pack(bf16_lo(v[0].w), bf16_hi(v[0].w));
         }
     }
 };
 
-template <int N>
-__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[N])
+__device__ __forceinline__ void load8(const float* p, uint64_t (&x)[kRun / 2])
 {
-    if constexpr (N == 1)
-        *static_cast<uint32_t*>(p) = w[0];
-    else if constexpr (N == 2)
-        *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else
-        *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = pack(a.x, a.y);
+    x[1] = pack(a.z, a.w);
+    x[2] = pack(b.x, b.y);
+    x[3] = pack(b.z, b.w);
 }
 
-template <int E>
-__device__ __forceinline__ void store_bf16(uint16_t* p, const float (&y)[E])
+__device__ __forceinline__ uint32_t bf16x2(uint64_t v)
 {
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    store_words(p, w);
+    float x, y;
+    unpack(v, x, y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void store_bf16(uint16_t* p, const uint64_t (&y)[kRun / 2])
+{
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(y[0]), bf16x2(y[1]), bf16x2(y[2]), bf16x2(y[3]));
 }
 
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
+__device__ __forceinline__ uint32_t e4m3x2(uint64_t v, uint64_t inv)
 {
+    float x, y;
+    unpack(mul2(v, inv), x, y);
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
     return r;
 }
-
-template <int E>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&y)[E], float inv)
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const uint64_t (&y)[kRun / 2], float inv)
 {
-    uint16_t h[E / 2];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) h[i] = e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv);
-    if constexpr (E == 2) {
-        *reinterpret_cast<uint16_t*>(p) = h[0];
-    } else {
-        uint32_t w[E / 4];
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i) w[i] = h[2 * i] | (static_cast<uint32_t>(h[2 * i + 1]) << 16);
-        store_words(p, w);
-    }
+    const uint64_t i2 = pack(inv, inv);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(e4m3x2(y[0], i2) | (e4m3x2(y[1], i2) << 16), e4m3x2(y[2], i2) | (e4m3x2(y[3], i2) << 16));
 }
 
-template <typename T, int D, bool F8>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const QkRopeArgs a, uint32_t groups)
+template <typename T, int D, bool F8, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, 3) qk_rope_kernel(const QkRopeArgs a, uint32_t groups, int run)
 {
-    constexpr int E = D / kWarp;
-    const int lane = threadIdx.x % kWarp;
+    constexpr int L = D / 16, HW = kWarp / L;  // lanes of a head, heads of a step
+    constexpr int N = kRun / 2;
+    const int lane = threadIdx.x % kWarp, l = lane % L;
     const int Hkv = a.cache.heads, heads = a.Hq + 2 * Hkv;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / kWarp) + threadIdx.x / kWarp;
     int64_t t;
-    int h0;
+    int g;
     if (a.T * groups < 0xFFFFFF00ll) {  // a 32-bit division where it will do
         const uint32_t tt = static_cast<uint32_t>(item) / groups;
         t = tt;
-        h0 = static_cast<int>(static_cast<uint32_t>(item) - tt * groups) * kHeads;
+        g = static_cast<int>(static_cast<uint32_t>(item) - tt * groups);
     } else {
         t = item / groups;
-        h0 = static_cast<int>(item % groups) * kHeads;
+        g = static_cast<int>(item % groups);
     }
     if (t >= a.T) return;
-    const int e0 = lane * E;
+    const int h0 = g * run + lane / L, h1 = min((g + 1) * run, heads);  // this lane's heads: h0, h0 + HW, ...
+    const int s = l * kRun, half = a.rot / 2;                            // the lane's first pair
+    const int e0 = PAIRS ? 2 * s : s < half ? s : half + s;
+    const int e1 = PAIRS ? 2 * s + kRun : s < half ? s + half : e0 + (D - a.rot) / 2;
 
-    Raw<T, E> raw[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i;
-        if (h < heads) {
-            const T* src = h < a.Hq         ? static_cast<const T*>(a.q) + t * a.q_pitch + static_cast<int64_t>(h) * D
-                           : h < a.Hq + Hkv ? static_cast<const T*>(a.k) + t * a.k_pitch + static_cast<int64_t>(h - a.Hq) * D
-                                            : static_cast<const T*>(a.v) + t * a.v_pitch +
-                                                  static_cast<int64_t>(h - a.Hq - Hkv) * D;
-            raw[i].load(src + e0);
+    // rows of q, k and v, each so that head h is h D further
+    const T* qb = static_cast<const T*>(a.q) + t * a.q_pitch;
+    const T* kb = static_cast<const T*>(a.k) + t * a.k_pitch - static_cast<int64_t>(a.Hq) * D;
+    const T* vb = static_cast<const T*>(a.v) + t * a.v_pitch - static_cast<int64_t>(a.Hq + Hkv) * D;
+    Raw<T> lo, hi;
+    auto fetch = [&](int h) {
+        if (h < h1) {
+            const T* src = (h < a.Hq ? qb : h < a.Hq + Hkv ? kb : vb) + static_cast<int64_t>(h) * D;
+            lo.load(src + e0);
+            hi.load(src + e1);
         }
-    }
+    };
+    fetch(h0);
     const int pos = a.rot ? a.positions[t] : 0;
     const bool pos_ok = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
-    const int64_t slot = h0 + kHeads > a.Hq ? a.slots[t] : -1;
+    const int64_t slot = h1 > a.Hq ? a.slots[t] : -1;
     const bool stored = pos_ok && slot >= 0 && slot < a.cache.num_pages * a.cache.page_size;
-    const int64_t at0 = stored ? (slot / a.cache.page_size) * a.cache.page_stride +
+    const int shift = 31 - __clz(a.cache.page_size);
+    const int64_t at0 = stored ? (slot >> shift) * a.cache.page_stride +
                                      (slot & (a.cache.page_size - 1)) * a.cache.token_stride
                                : 0;
-
-    // this lane's cosines and sines, signed so that y' = y c + other s
-    const int half = a.rot / 2;
-    const bool turns = pos_ok && e0 < a.rot;
-    const bool upper = e0 >= half;  // halves: which end of its pairs the lane holds
-    const int other = turns && !a.pairs ? (upper ? lane - half / E : lane + half / E) : lane;
-    float cs[E], sn[E];
+    const bool turns = pos_ok && s < half;
+    uint64_t cs[N] = {}, sn[N] = {};  // one angle per pair
     if (turns) {
-        const float* p = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
-        if (a.pairs) {
-            float c2[E / 2], s2[E / 2];
-            load_f32(p + e0 / 2, c2);
-            load_f32(p + half + e0 / 2, s2);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                cs[i] = c2[i / 2];
-                sn[i] = (i & 1) ? s2[i / 2] : -s2[i / 2];
-            }
-        } else {
-            const int i0 = upper ? e0 - half : e0;
-            load_f32(p + i0, cs);
-            load_f32(p + half + i0, sn);
-            if (!upper)
-#pragma unroll
-                for (int i = 0; i < E; ++i) sn[i] = -sn[i];
-        }
+        const float* p = a.cos_sin + static_cast<int64_t>(pos) * a.rot + s;
+        load8(p, cs);
+        load8(p + half, sn);
     }
+    const float* held = nullptr;  // whose weights the lane holds
+    uint64_t w0[N], w1[N];
 
+    for (int h = h0; h - lane / L < h1; h += HW) {  // as often for every lane of the warp
+        uint64_t y0[N], y1[N];
+        lo.get(y0);
+        hi.get(y1);
+        fetch(h + HW);
+        const bool live = h < h1, is_q = live && h < a.Hq, is_k = live && !is_q && h < a.Hq + Hkv;
+        const float* w = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+        uint64_t ss2 = 0;
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i;
-        if (h >= heads) break;
-        const int kind = h < a.Hq ? 0 : h < a.Hq + Hkv ? 1 : 2;  // q, k, v
-        float y[E];
-        raw[i].get(y);
-        if (kind != 2) {
-            const float* w = kind == 0 ? a.q_weight : a.k_weight;
-            if (w) {
-                float ss = 0.f;
+        for (int i = 0; i < N; ++i) ss2 = fma2(y1[i], y1[i], fma2(y0[i], y0[i], ss2));
+        float ss, st;
+        unpack(ss2, ss, st);
+        ss += st;
 #pragma unroll
-                for (int j = 0; j < E; ++j) ss += y[j] * y[j];
-                const float r = rsqrtf(warp_sum(ss) / D + a.eps);
-                float g[E];
-                load_f32(w + e0, g);
-#pragma unroll
-                for (int j = 0; j < E; ++j) y[j] *= r * g[j];
+        for (int d = L / 2; d; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+        if (w) {
+            if (w != held) {
+                load8(w + e0, w0);
+                load8(w + e1, w1);
+                held = w;
             }
-            if (a.rot) {
-                float z[E];
+            const float r = rsqrtf(ss * (1.f / D) + a.eps);
+            const uint64_t rr = pack(r, r);
 #pragma unroll
-                for (int j = 0; j < E; ++j) z[j] = a.pairs ? y[j ^ 1] : __shfl_sync(0xFFFFFFFFu, y[j], other);
-                if (turns)
-#pragma unroll
-                    for (int j = 0; j < E; ++j) y[j] = y[j] * cs[j] + z[j] * sn[j];
+            for (int i = 0; i < N; ++i) {
+                y0[i] = mul2(mul2(y0[i], rr), w0[i]);
+                y1[i] = mul2(mul2(y1[i], rr), w1[i]);
             }
         }
-        if (kind == 0) {
+        if (turns && (is_q || is_k)) {
+            if (PAIRS) {
+                // pairs 0 .. 3 in y0, 4 .. 7 in y1, each one register pair
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    float p, q, c0, c1, s0, s1;
+                    unpack(cs[i / 2], c0, c1);
+                    unpack(sn[i / 2], s0, s1);
+                    unpack(y0[i], p, q);
+                    const float ca = i % 2 ? c1 : c0, sa = i % 2 ? s1 : s0;
+                    y0[i] = pack(p * ca - q * sa, q * ca + p * sa);
+                    unpack(cs[2 + i / 2], c0, c1);
+                    unpack(sn[2 + i / 2], s0, s1);
+                    unpack(y1[i], p, q);
+                    const float cb = i % 2 ? c1 : c0, sb = i % 2 ? s1 : s0;
+                    y1[i] = pack(p * cb - q * sb, q * cb + p * sb);
+                }
+            } else {
+                const uint64_t minus = pack(-1.f, -1.f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const uint64_t p = y0[i], q = y1[i];
+                    y0[i] = fma2(p, cs[i], mul2(mul2(q, sn[i]), minus));
+                    y1[i] = fma2(q, cs[i], mul2(p, sn[i]));
+                }
+            }
+        }
+        if (is_q) {
             if (!pos_ok)
 #pragma unroll
-                for (int j = 0; j < E; ++j) y[j] = 0.f;
-            store_bf16(a.q_out + (t * a.Hq + h) * D + e0, y);
-        } else if (stored) {
-            const int hh = kind == 1 ? h - a.Hq : h - a.Hq - Hkv;
-            const int64_t at = at0 + static_cast<int64_t>(hh) * a.cache.head_stride + e0;
-            void* base = kind == 1 ? a.cache.k : a.cache.v;
+                for (int i = 0; i < N; ++i) y0[i] = y1[i] = 0;
+            uint16_t* out = a.q_out + (t * a.Hq + h) * D;
+            store_bf16(out + e0, y0);
+            store_bf16(out + e1, y1);
+        } else if (live && stored) {
+            const int hc = is_k ? h - a.Hq : h - a.Hq - Hkv;
+            const int64_t at = at0 + static_cast<int64_t>(hc) * a.cache.head_stride;
+            void* base = is_k ? a.cache.k : a.cache.v;
             if constexpr (F8) {
-                const float* sc = kind == 1 ? a.cache.k_scale : a.cache.v_scale;
-                store_e4m3(static_cast<uint8_t*>(base) + at, y, sc ? 1.f / sc[hh] : 1.f);
+                const float* sc = is_k ? a.cache.k_scale : a.cache.v_scale;
+                const float inv = sc ? 1.f / sc[hc] : 1.f;
+                store_e4m3(static_cast<uint8_t*>(base) + at + e0, y0, inv);
+                store_e4m3(static_cast<uint8_t*>(base) + at + e1, y1, inv);
             } else {
-                store_bf16(static_cast<uint16_t*>(base) + at, y);
+                store_bf16(static_cast<uint16_t*>(base) + at + e0, y0);
+                store_bf16(static_cast<uint16_t*>(base) + at + e1, y1);
             }
         }
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool F8, bool PAIRS>
 void launch(const QkRopeArgs& a, cudaStream_t s)
 {
-    const uint32_t groups = static_cast<uint32_t>((a.Hq + 2 * a.cache.heads + kHeads - 1) / kHeads);
+    // Heads per warp: one step's, doubled while the warps still fill the GPU
+    // four times over (the angles and weights are then read less often).
+    const int heads = a.Hq + 2 * a.cache.heads;
+    int run = 512 / D;
+    while (run < heads && a.T * ((heads + 2 * run - 1) / (2 * run)) >= 152 * 24 * 4) run *= 2;
+    const uint32_t groups = static_cast<uint32_t>((heads + run - 1) / run);
     const int64_t blocks = (a.T * groups + kThreads / kWarp - 1) / (kThreads / kWarp);
+    qk_rope_kernel<T, D, F8, PAIRS><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, groups, run);
+}
+
+template <typename T, int D>
+void launch_t(const QkRopeArgs& a, cudaStream_t s)
+{
     if (a.cache.type == BQD_E4M3)
-        qk_rope_kernel<T, D, true><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, groups);
+        a.pairs ? launch<T, D, true, true>(a, s) : launch<T, D, true, false>(a, s);
     else
-        qk_rope_kernel<T, D, false><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, groups);
+        a.pairs ? launch<T, D, false, true>(a, s) : launch<T, D, false, false>(a, s);
 }
 
 template <typename T>
 void launch_d(const QkRopeArgs& a, cudaStream_t s)
 {
     switch (a.cache.head_dim) {
-        case 64: return launch<T, 64>(a, s);
-        case 128: return launch<T, 128>(a, s);
-        default: return launch<T, 256>(a, s);
+        case 64: return launch_t<T, 64>(a, s);
+        case 128: return launch_t<T, 128>(a, s);
+        default: return launch_t<T, 256>(a, s);
     }
 }
 

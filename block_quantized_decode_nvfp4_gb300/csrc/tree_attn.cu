@@ -15,7 +15,7 @@
 //
 // Split. Lengths are known to the device only, and a batch is ragged, so the
 // work of all items is laid out in units of kUnit tokens, and each of the
-// grid's CTAs (two per SM) takes an equal share of the line, at most two
+// grid's CTAs (three per SM; two for D = 256) takes an equal share of the line, at most two
 // items' ends among them being partial. A CTA writes the items that lie within its share; of an item
 // that crosses a boundary each CTA writes its part to the workspace, and a
 // second kernel joins them in ascending order (results do not depend on
@@ -52,7 +52,7 @@ namespace bqd {
 
 namespace {
 
-constexpr int kGrid = 2 * 152;     // two CTAs per SM
+constexpr int kMaxGrid = 3 * 152;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kBlock = 16;         // tokens a token group takes at a time
@@ -65,7 +65,7 @@ struct Meta {  // of a CTA's unfinished last item: whose it is and the last CTA 
     int32_t r, h, tile, last;  // r = -1: none
 };
 
-__host__ __device__ constexpr size_t meta_bytes() { return (kGrid * sizeof(Meta) + 255) / 256 * 256; }
+__host__ __device__ constexpr size_t meta_bytes() { return (kMaxGrid * sizeof(Meta) + 255) / 256 * 256; }
 __host__ __device__ constexpr size_t part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
 
 template <int D, int RG, bool F8>
@@ -74,13 +74,14 @@ struct Shape {
     static constexpr int kGroups = kWarps / RG;            // token groups
     static constexpr int kRowBytes = D * (F8 ? 1 : 2);
     static constexpr int kStage = 2 * kBlock * kRowBytes;  // K and V of one block
-    static constexpr int kMost = (F8 ? 64 : 96) * 1024 / (kGroups * kStage);
-    static constexpr int kStages = kMost < 3 ? 3 : kMost > 8 ? 8 : kMost;
+    static constexpr int kCtas = D <= 128 ? 3 : 2;         // per SM: 64 of o and 40 more registers, or 128 of o
+    static constexpr int kGrid = kCtas * 152;
+    static constexpr int kMost = (D <= 128 ? 64 : 96) * 1024 / (kGroups * kStage);
+    static constexpr int kStages = kMost < 2 ? 2 : kMost > 8 ? 8 : kMost;
     static constexpr int kRing = kGroups * kStages * kStage;
     static constexpr int kJoin = kWarps * kRows16 * D * 4;
     static constexpr int kMain = kRing > kJoin ? kRing : kJoin;
-    static constexpr bool kQReg = D <= 128;                // q in registers (beside 64 of o)
-    static constexpr int kQBytes = kQReg ? 0 : RG * (D / 16) * 512;
+    static constexpr int kQBytes = RG * (D / 16) * 512;    // q as mma fragments
     static constexpr int kSmem = kMain + kQBytes;
 };
 
@@ -252,7 +253,7 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int64_t t, int i, int64_
 }
 
 template <int D, int RG, bool F8>
-__global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_kernel(const AttnArgs a)
 {
     using S = Shape<D, RG, F8>;
     constexpr int NT = D / 8;     // n tiles of the output; d of column n of tile j:
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a
     const int G = a.Hq / a.cache.heads;
     const uint32_t ring = smem_u32(smem) + tg * (S::kStages * S::kStage);
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     int64_t u, end, total, r, base;
     find_share(a, S::kRows, s_find, u, end, total, r, base);
     Meta* meta = static_cast<Meta*>(a.ws);
@@ -292,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a
         float c0 = a.scale * kLog2e, c1 = c0;  // score to log2 units, per row
 
         // ---- q fragments
-        uint32_t qf[S::kQReg ? KS : 1][4];
         const uint32_t qsm = smem_u32(smem) + S::kMain + (rg * KS * 32 + lane) * 16;
         {
             uint32_t f[KS][4];
@@ -341,19 +342,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a
                     f[s][3] = live1 ? *reinterpret_cast<const uint32_t*>(q1 + d + 8) : 0u;
                 }
             }
-            if (S::kQReg) {
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) qf[S::kQReg ? s : 0][e] = f[s][e];
-            } else if (tg == 0) {
+            if (tg == 0) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
                     *reinterpret_cast<uint4*>(smem + S::kMain + ((rg * KS + s) * 32 + lane) * 16) =
                         make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
             }
         }
-        if (!S::kQReg) __syncthreads();
+        __syncthreads();
 
         // ---- the token group's stream
         const int64_t first = l0 + tg * kBlock;
@@ -410,15 +406,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a
                 const int mrow = (lane & 7) + ((lane >> 4) << 3), mch = (lane >> 3) & 1;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4], qa[4];
+                    uint32_t b[4];
                     ldsm4(ks + chunk_at<S::kRowBytes, F8>(mrow, 2 * k + mch), b);
-                    if (S::kQReg) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) qa[e] = qf[S::kQReg ? k : 0][e];
-                    } else {
-                        const uint4 x = lds128(qsm + k * 512);
-                        qa[0] = x.x, qa[1] = x.y, qa[2] = x.z, qa[3] = x.w;
-                    }
+                    const uint4 x = lds128(qsm + k * 512);
+                    const uint32_t qa[4] = {x.x, x.y, x.z, x.w};
                     mma16816<F8>(s[0], qa, b[0], b[1]);
                     mma16816<F8>(s[1], qa, b[2], b[3]);
                 }
@@ -431,14 +422,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const AttnArgs a
 #pragma unroll
                     for (int e4 = 0; e4 < 4; ++e4) {
                         const int k = 4 * k4 + e4;
-                        uint32_t qa[4];
-                        if (S::kQReg) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) qa[e] = qf[S::kQReg ? k : 0][e];
-                        } else {
-                            const uint4 w = lds128(qsm + k * 512);
-                            qa[0] = w.x, qa[1] = w.y, qa[2] = w.z, qa[3] = w.w;
-                        }
+                        const uint4 w = lds128(qsm + k * 512);
+                        const uint32_t qa[4] = {w.x, w.y, w.z, w.w};
                         mma16816<F8>(s[0], qa, e4m3x2_to_f16x2(xs[e4] & 0xFFFFu), e4m3x2_to_f16x2(xs[e4] >> 16));
                         mma16816<F8>(s[1], qa, e4m3x2_to_f16x2(ys[e4] & 0xFFFFu), e4m3x2_to_f16x2(ys[e4] >> 16));
                     }
@@ -754,11 +739,11 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     blocks_per_sm(occ, reinterpret_cast<const void*>(&tree_attn_kernel<D, RG, F8>), dev, kThreads, S::kSmem);
-    tree_attn_kernel<D, RG, F8><<<kGrid, kThreads, S::kSmem, s>>>(a);
+    tree_attn_kernel<D, RG, F8><<<S::kGrid, kThreads, S::kSmem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kGrid, S::kRows / 4);
+    cfg.gridDim = dim3(S::kGrid, S::kRows / 4);
     cfg.blockDim = dim3(D);
     cfg.stream = s;
     cudaLaunchAttribute at{};
@@ -782,7 +767,7 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D)
 {
     const int rows = kRows16 * row_groups(R, T, Hq, Hkv);
-    return meta_bytes() + 2 * kGrid * part_floats(rows, D) * sizeof(float);
+    return meta_bytes() + 2 * kMaxGrid * part_floats(rows, D) * sizeof(float);
 }
 
 cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t s)
