@@ -50,6 +50,7 @@ struct AttnArgs {
 };
 size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D);
 cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t s);
+cudaError_t read_and_clear_attn_error(unsigned int* out);
 
 struct LogprobArgs {
     const void* x;

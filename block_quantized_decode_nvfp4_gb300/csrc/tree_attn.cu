@@ -47,26 +47,17 @@
 #include "common.cuh"
 #include "host_util.h"
 #include "stream.cuh"
+#include "tree_attn.cuh"
 
 namespace bqd {
 
 namespace {
 
-constexpr int kMaxGrid = 3 * 152;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kBlock = 16;         // tokens a token group takes at a time
 constexpr int kUnit = 64;          // tokens per unit of the split
 constexpr int kRows16 = 16;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kPShift = 12.f;    // E4M3: log2 of the scale p carries
-
-struct Meta {  // of a CTA's unfinished last item: whose it is and the last CTA with a part of it
-    int32_t r, h, tile, last;  // r = -1: none
-};
-
-__host__ __device__ constexpr size_t meta_bytes() { return (kMaxGrid * sizeof(Meta) + 255) / 256 * 256; }
-__host__ __device__ constexpr size_t part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
 
 template <int D, int RG, bool F8>
 struct Shape {
@@ -84,77 +75,6 @@ struct Shape {
     static constexpr int kQBytes = RG * (D / 16) * 512;    // q as mma fragments
     static constexpr int kSmem = kMain + kQBytes;
 };
-
-struct Req {
-    int o0, n;      // first token, new tokens
-    int64_t ctx;    // cached tokens
-    int64_t len;    // tokens to look at
-    int tiles;
-    int64_t nb;     // units per item
-};
-
-__device__ __forceinline__ Req request(const AttnArgs& a, int64_t r, int rows)
-{
-    Req q;
-    const int T = static_cast<int>(a.T);
-    q.o0 = min(max(a.offsets[r], 0), T);
-    q.n = min(max(a.offsets[r + 1], q.o0), T) - q.o0;
-    q.ctx = max(a.context[r], 0);
-    q.len = min(q.ctx + q.n, a.width * a.cache.page_size);
-    q.tiles = static_cast<int>((static_cast<int64_t>(q.n) * (a.Hq / a.cache.heads) + rows - 1) / rows);
-    q.nb = max(int64_t(1), (q.len + kUnit - 1) / kUnit);
-    return q;
-}
-
-__device__ __forceinline__ int64_t units_of(const AttnArgs& a, int64_t r, int rows)
-{
-    const Req q = request(a, r, rows);
-    return q.nb * q.tiles * a.cache.heads;
-}
-
-// Total units, and the request that holds unit `start` of CTA blockIdx.x's
-// share with the units before it. Each thread sums a run of requests.
-__device__ __forceinline__ void find_share(const AttnArgs& a, int rows, int64_t* sh, int64_t& start, int64_t& end,
-                                           int64_t& total, int64_t& r, int64_t& base)
-{
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    const int64_t per = (a.R + kThreads - 1) / kThreads;
-    const int64_t r0 = min(threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
-    int64_t mine = 0;
-    for (int64_t i = r0; i < r1; ++i) mine += units_of(a, i, rows);
-    int64_t incl = mine;
-#pragma unroll
-    for (int d = 1; d < kWarp; d <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += v;
-    }
-    if (lane == kWarp - 1) sh[warp] = incl;
-    __syncthreads();
-    total = 0;
-    int64_t before = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh[w];
-        total += sh[w];
-    }
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);  // each of them has a unit at least
-    start = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-    end = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
-    const int64_t first = before + incl - mine;
-    if (start < end && start >= first && start < first + mine) {
-        int64_t b = first, i = r0;
-        for (;; ++i) {
-            const int64_t u = units_of(a, i, rows);
-            if (start < b + u) break;
-            b += u;
-        }
-        sh[kWarps] = i;
-        sh[kWarps + 1] = b;
-    }
-    __syncthreads();
-    r = sh[kWarps];
-    base = sh[kWarps + 1];
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real)
 {
@@ -212,13 +132,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <bool F8>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -244,14 +157,6 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch)
     return static_cast<uint32_t>(row * RB + ((ch ^ f ^ ((row & 1) << 2)) << 4));
 }
 
-// Whether query token i of the request sees draft j (j < 0: a cached token).
-__device__ __forceinline__ bool sees(const AttnArgs& a, int64_t t, int i, int64_t j)
-{
-    if (j < 0) return true;
-    if (!a.mask) return j <= i;
-    return (j >> 6) < a.mask_words && ((a.mask[t * a.mask_words + (j >> 6)] >> (j & 63)) & 1);
-}
-
 template <int D, int RG, bool F8>
 __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_kernel(const AttnArgs a)
 {
@@ -269,19 +174,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     const uint32_t ring = smem_u32(smem) + tg * (S::kStages * S::kStage);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
-    int64_t u, end, total, r, base;
-    find_share(a, S::kRows, s_find, u, end, total, r, base);
-    Meta* meta = static_cast<Meta*>(a.ws);
-    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + meta_bytes());
+    AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kUnit, s_find);
+    int64_t u = sh.start;
+    AttnMeta* meta = static_cast<AttnMeta*>(a.ws);
+    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes());
     if (threadIdx.x == 0) meta[blockIdx.x].r = -1;
     int page_shift = 31 - __clz(a.cache.page_size);
 
-    while (u < end) {
-        const Req q = request(a, r, S::kRows);
-        const int64_t item = (u - base) / q.nb, b0 = (u - base) % q.nb, cnt = min(q.nb - b0, end - u);
+    while (u < sh.end) {
+        const AttnReq q = attn_request(a, sh.r, S::kRows, kUnit);
+        const int64_t item = (u - sh.base) / q.nb, b0 = (u - sh.base) % q.nb, cnt = min(q.nb - b0, sh.end - u);
         const int h = static_cast<int>(item / q.tiles), tile = static_cast<int>(item % q.tiles);
         const int64_t l0 = b0 * kUnit, l1 = min((b0 + cnt) * kUnit, q.len);
-        const int32_t* table = a.table + r * a.width;
+        const int32_t* table = a.table + sh.r * a.width;
         const int rows = static_cast<int>(min(static_cast<int64_t>(q.n) * G - static_cast<int64_t>(tile) * S::kRows,
                                               static_cast<int64_t>(S::kRows)));
         // this thread's two rows
@@ -291,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
         const int64_t t0 = q.o0 + (live0 ? i0 : 0), t1 = q.o0 + (live1 ? i1 : 0);
         const uint16_t* q0 = a.q + t0 * a.q_pitch + static_cast<int64_t>(h * G + row0 % G) * D;
         const uint16_t* q1 = a.q + t1 * a.q_pitch + static_cast<int64_t>(h * G + row1 % G) * D;
-        float c0 = a.scale * kLog2e, c1 = c0;  // score to log2 units, per row
+        float c0 = a.scale * kAttnLog2e, c1 = c0;  // score to log2 units, per row
 
         // ---- q fragments
         const uint32_t qsm = smem_u32(smem) + S::kMain + (rg * KS * 32 + lane) * 16;
@@ -446,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                         const int tok = 8 * nt + 2 * c + e;
                         const bool v = (vis >> tok) & 1;
                         const int64_t j = l + tok - q.ctx;
-                        if (!v || !sees(a, t0, i0, j)) s[nt][e] = -INFINITY;
-                        if (!v || !sees(a, t1, i1, j)) s[nt][2 + e] = -INFINITY;
+                        if (!v || !attn_sees(a, t0, i0, j)) s[nt][e] = -INFINITY;
+                        if (!v || !attn_sees(a, t1, i1, j)) s[nt][2 + e] = -INFINITY;
                     }
             }
             // running maximum
@@ -461,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             n0 = fmaxf(n0, m0);
             n1 = fmaxf(n1, m1);
             if (__any_sync(0xFFFFFFFFu, n0 != m0 || n1 != m1)) {
-                const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+                const float f0 = m0 == -INFINITY ? 0.f : attn_ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : attn_ex2(m1 - n1);
                 z0 *= f0;
                 z1 *= f1;
 #pragma unroll
@@ -474,13 +379,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 m0 = n0;
                 m1 = n1;
             }
-            const float sub0 = (m0 == -INFINITY ? 0.f : m0) - (F8 ? kPShift : 0.f);
-            const float sub1 = (m1 == -INFINITY ? 0.f : m1) - (F8 ? kPShift : 0.f);
+            const float sub0 = (m0 == -INFINITY ? 0.f : m0) - (F8 ? kAttnPShift : 0.f);
+            const float sub1 = (m1 == -INFINITY ? 0.f : m1) - (F8 ? kAttnPShift : 0.f);
             uint32_t pa[4];
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const float p0 = ex2(s[nt][0] - sub0), p1 = ex2(s[nt][1] - sub0);
-                const float p2 = ex2(s[nt][2] - sub1), p3 = ex2(s[nt][3] - sub1);
+                const float p0 = attn_ex2(s[nt][0] - sub0), p1 = attn_ex2(s[nt][1] - sub0);
+                const float p2 = attn_ex2(s[nt][2] - sub1), p3 = attn_ex2(s[nt][3] - sub1);
                 z0 += p0 + p1;
                 z1 += p2 + p3;
                 pa[2 * nt] = pack2<F8>(p0, p1);
@@ -506,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 if (__any_sync(0xFFFFFFFFu, odd)) {
                     for (int tok = 0; tok < kBlock; ++tok) {
                         if (!((vis >> tok) & 1)) continue;
-                        const bool see0 = sees(a, t0, i0, l + tok - q.ctx), see1 = sees(a, t1, i1, l + tok - q.ctx);
+                        const bool see0 = attn_sees(a, t0, i0, l + tok - q.ctx), see1 = attn_sees(a, t1, i1, l + tok - q.ctx);
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -619,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             }
         __syncthreads();
         const bool whole = b0 == 0 && cnt == q.nb;
-        float* part = parts + (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * part_floats(S::kRows, D);
+        float* part = parts + (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * attn_part_floats(S::kRows, D);
         const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[h] : 1.f;
         for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), d = x % (D / 4) * 4, rw = row / kRows16, rr = row % kRows16;
@@ -631,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
 #pragma unroll
             for (int w = 0; w < S::kGroups; ++w) {
                 const float mw = s_m[w * RG + rw][rr];
-                const float f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mw - m);
+                const float f = attn_weight(mw, m);
                 const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
                                                                   ((w * RG + rw) * kRows16 + rr) * D + d);
                 z += s_z[w * RG + rw][rr] * f;
@@ -643,13 +548,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             if (whole) {
                 const int grow = tile * S::kRows + row;
                 const int64_t at = (q.o0 + grow / G) * static_cast<int64_t>(a.Hq) + h * G + grow % G;
-                const float k = z == 0.f ? 0.f : vscale / z;
-                uint2 w;
-                w.x = pack2<false>(z == 0.f ? 0.f : v.x * k, z == 0.f ? 0.f : v.y * k);
-                w.y = pack2<false>(z == 0.f ? 0.f : v.z * k, z == 0.f ? 0.f : v.w * k);
-                *reinterpret_cast<uint2*>(a.out + at * D + d) = w;
-                if (d == 0 && a.lse)
-                    a.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z) - (F8 ? kPShift : 0.f)) * kLn2;
+                *reinterpret_cast<uint2*>(a.out + at * D + d) = attn_out4(v, z, vscale);
+                if (d == 0 && a.lse) a.lse[at] = attn_lse(m, z, F8 ? kAttnPShift : 0.f);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + d) = v;
                 if (d == 0) {
@@ -658,72 +558,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 }
             }
         }
-        if (b0 == 0 && !whole && threadIdx.x == 0) {
-            // the last CTA whose share begins before the item's end
-            const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), ends = u + q.nb;
-            Meta md;
-            md.r = static_cast<int32_t>(r);
-            md.h = h;
-            md.tile = tile;
-            md.last = static_cast<int32_t>((ends * ctas + total - 1) / total - 1);
-            meta[blockIdx.x] = md;
-        }
+        if (b0 == 0 && !whole && threadIdx.x == 0) meta[blockIdx.x] = attn_meta(sh, h, tile, u + q.nb);
         __syncthreads();
         u += cnt;
-        if (u < end) {
-            int64_t next = base + q.nb * q.tiles * a.cache.heads;
+        if (u < sh.end) {
+            int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
             while (u == next) {  // the next request with rows
-                ++r;
-                base = next;
-                next += units_of(a, r, S::kRows);
+                ++sh.r;
+                sh.base = next;
+                next += attn_units(a, sh.r, S::kRows, kUnit);
             }
         }
     }
-}
-
-// Joins the parts of the item that CTA blockIdx.x of the first kernel began
-// and did not finish: its own second part, then the first parts of the CTAs
-// after it, in order. blockIdx.y: four rows each, D / 4 threads a row.
-template <int D, int RG, bool F8>
-__global__ void __launch_bounds__(D) tree_attn_join_kernel(const AttnArgs a)
-{
-    using S = Shape<D, RG, F8>;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Meta md = static_cast<const Meta*>(a.ws)[blockIdx.x];
-    if (md.r < 0) return;
-    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + meta_bytes());
-    const int row = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
-    const Req q = request(a, md.r, S::kRows);
-    const int G = a.Hq / a.cache.heads;
-    const int64_t grow = static_cast<int64_t>(md.tile) * S::kRows + row;
-    if (grow >= static_cast<int64_t>(q.n) * G) return;
-    constexpr size_t P = part_floats(S::kRows, D);
-    const int b = blockIdx.x;
-    auto part = [&](int k) { return parts + (k == b ? 2 * k + 1 : 2 * k) * P; };
-    float m = -INFINITY;
-    for (int k = b; k <= md.last; ++k) m = fmaxf(m, part(k)[S::kRows * D + row]);
-    float z = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = b; k <= md.last; ++k) {
-        const float* p = part(k);
-        const float mw = p[S::kRows * D + row];
-        const float f = mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : ex2(mw - m);
-        const float4 y = *reinterpret_cast<const float4*>(p + row * D + d);
-        z += p[S::kRows * D + S::kRows + row] * f;
-        v.x += y.x * f;
-        v.y += y.y * f;
-        v.z += y.z * f;
-        v.w += y.w * f;
-    }
-    const int64_t at = (q.o0 + grow / G) * static_cast<int64_t>(a.Hq) + md.h * G + grow % G;
-    const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[md.h] : 1.f;
-    const float k = z == 0.f ? 0.f : vscale / z;
-    uint2 w;
-    w.x = pack2<false>(z == 0.f ? 0.f : v.x * k, z == 0.f ? 0.f : v.y * k);
-    w.y = pack2<false>(z == 0.f ? 0.f : v.z * k, z == 0.f ? 0.f : v.w * k);
-    *reinterpret_cast<uint2*>(a.out + at * D + d) = w;
-    if (d == 0 && a.lse) a.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z) - (F8 ? kPShift : 0.f)) * kLn2;
 }
 
 // Row groups: 16 rows unless the requests have more on average (two halve the
@@ -742,16 +588,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s)
     tree_attn_kernel<D, RG, F8><<<S::kGrid, kThreads, S::kSmem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(S::kGrid, S::kRows / 4);
-    cfg.blockDim = dim3(D);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, RG, F8>, a);
+    return launch_attn_join<D, S::kRows, kUnit, F8>(a, S::kGrid, s);
 }
 
 template <int D>
@@ -767,11 +604,14 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D)
 {
     const int rows = kRows16 * row_groups(R, T, Hq, Hkv);
-    return meta_bytes() + 2 * kMaxGrid * part_floats(rows, D) * sizeof(float);
+    const size_t narrow = attn_meta_bytes() + 2 * kAttnMaxGrid * attn_part_floats(rows, D) * sizeof(float);
+    const size_t wide = tree_attention_wide_ws(R, T, Hq, Hkv, D);
+    return narrow > wide ? narrow : wide;
 }
 
 cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t s)
 {
+    if (tree_attention_wide_fits(a)) return launch_tree_attention_wide(a, s);
     switch (a.cache.head_dim) {
         case 64: return launch_d<64>(a, s);
         case 128: return launch_d<128>(a, s);
