@@ -708,6 +708,8 @@ bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache
     a.scale = scale;
     a.mask_words = mask_words;
     a.Hq = Hq;
+    a.group = Hq / cache->heads;
+    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
     a.cache = *cache;
     return from_cuda(bqd::launch_tree_attention(a, stream));
 }

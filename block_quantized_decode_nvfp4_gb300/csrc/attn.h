@@ -46,6 +46,7 @@ struct AttnArgs {
     int64_t q_pitch, width, R, T;
     float scale;
     int mask_words, Hq;
+    int group, page_shift;  // query heads per kv head, log2 of the page size
     bqd_kv_cache cache;
 };
 size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D);

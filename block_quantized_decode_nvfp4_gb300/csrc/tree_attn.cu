@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int rg = warp % RG, tg = warp / RG;  // row group, token group
     const int g = lane >> 2, c = lane & 3;     // row (and column) and k positions in mma fragments
-    const int G = a.Hq / a.cache.heads;
+    const int G = a.group;
     const uint32_t ring = smem_u32(smem) + tg * (S::kStages * S::kStage);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
@@ -179,12 +179,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     AttnMeta* meta = static_cast<AttnMeta*>(a.ws);
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes());
     if (threadIdx.x == 0) meta[blockIdx.x].r = -1;
-    int page_shift = 31 - __clz(a.cache.page_size);
+    const int page_shift = a.page_shift;
 
     while (u < sh.end) {
         const AttnReq q = attn_request(a, sh.r, S::kRows, kUnit);
-        const int64_t item = (u - sh.base) / q.nb, b0 = (u - sh.base) % q.nb, cnt = min(q.nb - b0, sh.end - u);
-        const int h = static_cast<int>(item / q.tiles), tile = static_cast<int>(item % q.tiles);
+        int h, tile;
+        int64_t b0;
+        attn_place(sh, q, u, h, tile, b0);
+        const int64_t cnt = min(q.nb - b0, sh.end - u);
         const int64_t l0 = b0 * kUnit, l1 = min((b0 + cnt) * kUnit, q.len);
         const int32_t* table = a.table + sh.r * a.width;
         const int rows = static_cast<int>(min(static_cast<int64_t>(q.n) * G - static_cast<int64_t>(tile) * S::kRows,
@@ -588,7 +590,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s)
     tree_attn_kernel<D, RG, F8><<<S::kGrid, kThreads, S::kSmem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_attn_join<D, S::kRows, kUnit, F8>(a, S::kGrid, s);
+    return launch_attn_join(tree_attn_join_kernel<D, S::kRows, kUnit, F8>, dim3(S::kGrid, S::kRows / 4), D, a, s);
 }
 
 template <int D>

@@ -42,7 +42,7 @@ __device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int64_t r, in
     q.n = min(max(a.offsets[r + 1], q.o0), T) - q.o0;
     q.ctx = max(a.context[r], 0);
     q.len = min(q.ctx + q.n, a.width * a.cache.page_size);
-    q.tiles = static_cast<int>((static_cast<int64_t>(q.n) * (a.Hq / a.cache.heads) + rows - 1) / rows);
+    q.tiles = static_cast<int>((static_cast<int64_t>(q.n) * a.group + rows - 1) / rows);
     q.nb = max(int64_t(1), (q.len + unit - 1) / unit);
     return q;
 }
@@ -87,8 +87,15 @@ __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows
         s.total += sh[w];
     }
     s.ctas = min(static_cast<int64_t>(gridDim.x), s.total);
-    s.start = blockIdx.x < s.ctas ? s.total * blockIdx.x / s.ctas : s.total;
-    s.end = blockIdx.x < s.ctas ? s.total * (blockIdx.x + 1) / s.ctas : s.total;
+    if (blockIdx.x >= s.ctas) {
+        s.start = s.end = s.total;
+    } else if (s.total < (int64_t(1) << 22)) {  // 32-bit divisions (grids are below 2^10)
+        s.start = static_cast<uint32_t>(s.total) * blockIdx.x / static_cast<uint32_t>(s.ctas);
+        s.end = static_cast<uint32_t>(s.total) * (blockIdx.x + 1) / static_cast<uint32_t>(s.ctas);
+    } else {
+        s.start = s.total * blockIdx.x / s.ctas;
+        s.end = s.total * (blockIdx.x + 1) / s.ctas;
+    }
     const int64_t first = before + incl - mine;
     if (s.start < s.end && s.start >= first && s.start < first + mine) {
         int64_t b = first, i = r0;
@@ -104,6 +111,24 @@ __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows
     s.r = sh[W];
     s.base = sh[W + 1];
     return s;
+}
+
+// Unit u of the line: item (kv head, tile) of request s.r and its block.
+__device__ __forceinline__ void attn_place(const AttnShare& s, const AttnReq& q, int64_t u, int& h, int& tile,
+                                           int64_t& b0)
+{
+    const int64_t at = u - s.base;
+    if (at < (int64_t(1) << 32) && q.nb < (int64_t(1) << 32)) {
+        const uint32_t nb = static_cast<uint32_t>(q.nb), item = static_cast<uint32_t>(at) / nb;
+        b0 = static_cast<uint32_t>(at) - item * nb;
+        h = static_cast<int>(item / static_cast<uint32_t>(q.tiles));
+        tile = static_cast<int>(item) - h * q.tiles;
+    } else {
+        const int64_t item = at / q.nb;
+        b0 = at % q.nb;
+        h = static_cast<int>(item / q.tiles);
+        tile = static_cast<int>(item % q.tiles);
+    }
 }
 
 // The meta entry of a CTA whose item (units up to `ends` of the line) goes on
@@ -155,9 +180,10 @@ __device__ __forceinline__ float attn_weight(float mw, float m)
 
 // Joins the parts of the item that CTA blockIdx.x of the first kernel began
 // and did not finish: its own second part, then the first parts of the CTAs
-// after it, in order. blockIdx.y: four rows each, D / 4 threads a row.
+// after it, in order. blockIdx.y: four rows each, D / 4 threads a row. Parts
+// are row by row.
 template <int D, int ROWS, int UNIT, bool F8>
-__global__ void __launch_bounds__(D) tree_attn_join_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(D) tree_attn_join_kernel(AttnArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnMeta md = static_cast<const AttnMeta*>(a.ws)[blockIdx.x];
@@ -165,7 +191,7 @@ __global__ void __launch_bounds__(D) tree_attn_join_kernel(const AttnArgs a)
     const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
     const int row = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
     const AttnReq q = attn_request(a, md.r, ROWS, UNIT);
-    const int G = a.Hq / a.cache.heads;
+    const int G = a.group;
     const int64_t grow = static_cast<int64_t>(md.tile) * ROWS + row;
     if (grow >= static_cast<int64_t>(q.n) * G) return;
     constexpr size_t P = attn_part_floats(ROWS, D);
@@ -192,21 +218,72 @@ __global__ void __launch_bounds__(D) tree_attn_join_kernel(const AttnArgs a)
     if (d == 0 && a.lse) a.lse[at] = attn_lse(m, z, F8 ? kAttnPShift : 0.f);
 }
 
-// Launches the join after the first kernel (grid CTAs) in the same stream;
-// it may be set up while that one still runs, and waits for its end.
-template <int D, int ROWS, int UNIT, bool F8>
-cudaError_t launch_attn_join(const AttnArgs& a, int grid, cudaStream_t s)
+// The same for parts that lie column by column (o [D][rows]): blockIdx.y is
+// eight rows, a thread one of their D columns.
+template <int D, int ROWS, int UNIT>
+__global__ void __launch_bounds__(D) tree_attn_join_columns_kernel(AttnArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const AttnMeta md = static_cast<const AttnMeta*>(a.ws)[blockIdx.x];
+    if (md.r < 0) return;
+    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
+    const int row0 = blockIdx.y * 8, d = threadIdx.x, b = blockIdx.x;
+    const AttnReq q = attn_request(a, md.r, ROWS, UNIT);
+    const int64_t grow0 = static_cast<int64_t>(md.tile) * ROWS + row0;
+    const int live = static_cast<int>(min(static_cast<int64_t>(q.n) * a.group - grow0, int64_t(8)));
+    if (live <= 0) return;
+    constexpr size_t P = attn_part_floats(ROWS, D);
+    auto part = [&](int k) { return parts + (k == b ? 2 * k + 1 : 2 * k) * P; };
+    float m[8], z[8], v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = -INFINITY;
+        z[i] = v[i] = 0.f;
+    }
+    for (int k = b; k <= md.last; ++k) {
+        const float* p = part(k) + ROWS * D + row0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) m[i] = fmaxf(m[i], p[i]);
+    }
+#pragma unroll 2
+    for (int k = b; k <= md.last; ++k) {
+        const float* p = part(k);
+        const float4 lo = *reinterpret_cast<const float4*>(p + d * ROWS + row0);
+        const float4 hi = *reinterpret_cast<const float4*>(p + d * ROWS + row0 + 4);
+        const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) {
+                const float f = attn_weight(p[ROWS * D + row0 + i], m[i]);
+                z[i] += p[ROWS * D + ROWS + row0 + i] * f;
+                v[i] += y[i] * f;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < live) {
+            const uint32_t g = static_cast<uint32_t>(grow0 + i), tok = g / a.group;
+            const int64_t at = (q.o0 + static_cast<int64_t>(tok)) * a.Hq + md.h * a.group + (g - tok * a.group);
+            a.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(z[i] == 0.f ? 0.f : v[i] / z[i]));
+            if (d == 0 && a.lse) a.lse[at] = attn_lse(m[i], z[i], 0.f);
+        }
+}
+
+// Launches a join after the first kernel in the same stream; it may be set up
+// while that one still runs, and waits for its end.
+inline cudaError_t launch_attn_join(void (*kernel)(AttnArgs), dim3 grid, int threads, const AttnArgs& a, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, ROWS / 4);
-    cfg.blockDim = dim3(D);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, ROWS, UNIT, F8>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // The kernel for many rows a kv head (tree_attn_wide.cu), bf16 caches.

@@ -13,15 +13,18 @@
 //  - TWO: an item is 256 rows, a slot each 128 of them, over the same tokens;
 //  - else: an item is 128 rows; the slots take every other block of 128
 //    tokens, each with its own (m, z, o), and join at the item's end.
-// Warp 0 loads K and V blocks by 4-D tensor copies, one box per page and 64
-// elements of D (128-byte swizzle; pages outside the cache read as zero);
-// warp 1 issues, per block and slot, s = q k^T (both from shared memory,
-// K-major) and o += p v with p from tensor memory and v MN-major, the
-// previous block's o of a slot before its next s. Warps 4..7 and 8..11 are
-// the slots' softmax, a row per thread (tensor-memory lane): they read s,
-// write p in bf16 over the columns of s that they have read, and rescale o in
-// tensor memory only when a row's maximum has grown by more than 2^8 (p then
-// stays below 2^8, and nothing is lost: fp32 sums, bf16's range).
+// Warps 0 and 3 load K and V blocks by 4-D tensor copies, one box per page
+// and 64 elements of D (128-byte swizzle; pages outside the cache read as
+// zero). Warps 1 and 2, a thread each, issue one slot's products: per block s
+// = q k^T (both from shared memory, K-major) and o += p v with p from tensor
+// memory and v MN-major, a block's o before the next block's s. The slots take
+// turns block by block (left to themselves they fall into step, and both
+// softmaxes run while the tensor cores wait); an issuing thread keeps pace with
+// the tensor cores, so it does its waiting while the other issues. Warps 4..7 and 8..11 are the slots' softmax, a
+// row per thread (tensor-memory lane): they read s, write p in bf16 over the
+// columns of s that they have read, and rescale o in tensor memory only when
+// a row's maximum has grown by more than 2^8 (p then stays below 2^8, and
+// nothing is lost: fp32 sums, bf16's range).
 // Tensor memory: s0 | s1 (128 columns each) | o0 | o1 (D each).
 //
 // Blocks that reach past the cached tokens (drafts, the end), and all blocks
@@ -60,12 +63,12 @@ struct Wide {
     static constexpr int kRows = TWO ? 256 : 128;
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kBlk = kTok * D * 2;  // bytes of a K or V block
-    static constexpr int kKS = D == 64 ? 4 : TWO ? 2 : 3;
+    static constexpr int kKS = D == 64 ? 4 : 3;
     static constexpr int kVS = D == 64 ? 4 : 2;
     static constexpr int kQBytes = (TWO ? 2 : 1) * kQTile;
     static constexpr int kSmem = kQBytes + (kKS + kVS) * kBlk + 1024;  // + alignment slack
     static constexpr int kPitch = D + 4;  // floats of a row in the slots' join
-    static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of one CTA");
+    static_assert(kSmem <= 227 * 1024 - (TWO ? 1024 : 2048), "shared memory of one CTA, static beside it");
     static_assert(128 * kPitch * 4 <= (kKS + kVS) * kBlk, "the join lies over the ring");
 };
 
@@ -147,11 +150,25 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* r)
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 #undef BQD_R32
 
-__device__ __forceinline__ bool elect_one()
+// o of a slot's 32 rows of the warp times each row's f. Rare, so a call.
+template <int D>
+__device__ __noinline__ void rescale(uint32_t o_at, float f)
 {
-    uint32_t pred = 0;
-    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(pred));
-    return pred != 0;
+    const uint64_t ff = pack(f, f);
+    for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        tmem_ld(o_at + 32 * k, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float x, y;
+            unpack(mul2(pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ff), x, y);
+            o[e] = __float_as_uint(x);
+            o[e + 1] = __float_as_uint(y);
+        }
+        tmem_st(o_at + 32 * k, o);
+    }
+    tmem_st_wait();
 }
 
 // Bits e = 0 .. 31: whether token i of the request (t of the call) sees draft
@@ -175,42 +192,110 @@ __device__ __forceinline__ uint32_t sees32(const AttnArgs& a, int64_t t, int i, 
     return static_cast<uint32_t>(v);
 }
 
-struct Bars {
-    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[2], pready[2], odone[2];
+// The item (or part of one) that the CTA works on: written by one thread, read
+// by all, so that the softmax's registers hold scores and not bookkeeping.
+struct Seg {
+    int r, h, tile, n;      // request, kv head, tile of rows; blocks
+    int rows, o0, group;    // live rows of the tile, first token of the request, rows per token
+    int steps[2];           // softmax steps of the slots
+    int plain, ctx, len;    // tokens every row sees, cached tokens, tokens: from l0, kept within +-2^30
+    int64_t l0, table;      // first token; the request's row of the table
+    int64_t parts;          // where its part goes; -1: it is the whole item
+    int last;               // nothing of the CTA's share comes after it
 };
+
+struct Bars {
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[2], pready[2][2], odone[2], turn[2];
+};
+
+// A block that is not all tokens seen by every row: makes its V block fit for
+// the products (V row `row`, the thread's: cleared where it is no token, or
+// not finite; both slots of a TWO item do so, each before its own products,
+// and write the same) and returns the thread's row of visibility, 128 bits.
+// v_row: the V row in shared memory, after the block has landed.
+template <int D>
+__device__ __noinline__ uint4 special_block(const AttnArgs& a, const Seg& g, int j, int row, int64_t qt, int qi,
+                                            uint8_t* v_row, int* odd_flag)
+{
+    const int lane = threadIdx.x % kWarp;
+    const int br = min(a.cache.page_size, kTok), nbox = kTok / br;
+    const int rel = j * kTok;  // of the block's first token, from l0
+    const int lb = rel + lane * br;
+    const int e = lane < nbox && lb < g.len ? a.table[g.table + ((g.l0 + lb) >> a.page_shift)] : -1;
+    const uint32_t pages = __ballot_sync(0xFFFFFFFFu, e >= 0 && e < a.cache.num_pages);  // boxes that are tokens
+    const bool token = rel + row < g.len && ((pages >> (row / br)) & 1);
+    if (!token || rel + row >= g.ctx) {
+        for (int ch = 0; ch < D / 8; ++ch) {
+            uint4* p = reinterpret_cast<uint4*>(v_row + (ch / 8) * (kTok * 128) + (ch % 8) * 16);
+            const uint4 x = *p;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool odd = false;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const bool lo = (w[y] & 0x7F80u) == 0x7F80u, hi = (w[y] & 0x7F800000u) == 0x7F800000u;
+                odd |= lo || hi;
+                if (!token) w[y] = 0;
+                if (lo) w[y] &= 0xFFFF0000u;
+                if (hi) w[y] &= 0xFFFFu;
+            }
+            if (token && odd) {
+                *static_cast<volatile int*>(odd_flag) = 1;  // known before the element is gone
+                __threadfence_block();
+            }
+            if (!token || odd) *p = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    fence_async();
+    uint32_t see[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        see[k] = sees32(a, qt, qi, rel + 32 * k - g.ctx);
+        const int left = g.len - (rel + 32 * k);
+        if (left < 32) see[k] &= left <= 0 ? 0u : (1u << left) - 1u;
+        uint32_t real = 0;
+        if (br >= 32)
+            real = ((pages >> (32 * k / br)) & 1) ? 0xFFFFFFFFu : 0u;
+        else
+            for (int x = 0; x < 32; ++x) real |= ((pages >> ((32 * k + x) / br)) & 1) << x;
+        see[k] &= real;
+    }
+    return make_uint4(see[0], see[1], see[2], see[3]);
+}
 
 template <int D, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_attn_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+    tree_attn_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v)
 {
     using S = Wide<D, TWO>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) Bars bar;
     __shared__ int64_t s_find[kThreads / kWarp + 2];
+    __shared__ AttnShare s_share;
+    __shared__ int64_t s_u;
+    __shared__ Seg g;
     __shared__ uint32_t s_tmem;
     __shared__ int s_odd;
-    __shared__ float s_mz[128][2];
+    __shared__ float s_mz[TWO ? 1 : 128][2];  // slot 1's m and z, for the join
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const sm = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t q_at = base, k_at = base + S::kQBytes, v_at = k_at + S::kKS * S::kBlk;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    const int G = a.Hq / a.cache.heads;
-    const int shift = 31 - __clz(a.cache.page_size);
-    const int br = min(a.cache.page_size, kTok), nbox = kTok / br;  // tokens per box, boxes per block
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bar.kfull[i], 1);
-            mbar_init(&bar.kempty[i], 1);
+            mbar_init(&bar.kempty[i], TWO ? 2 : 1);  // slots that read a block
             mbar_init(&bar.vfull[i], 1);
-            mbar_init(&bar.vempty[i], 1);
+            mbar_init(&bar.vempty[i], TWO ? 2 : 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.sfull[i], 1);
-            mbar_init(&bar.pready[i], 4);
+            mbar_init(&bar.pready[i][0], 4);
+            mbar_init(&bar.pready[i][1], 4);
             mbar_init(&bar.odone[i], 1);
+            mbar_init(&bar.turn[i], 1);
         }
         fence_barrier_init();
         static_cast<AttnMeta*>(a.ws)[blockIdx.x].r = -1;
@@ -221,46 +306,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kTok, s_find);  // barriers inside
+    {
+        const AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kTok, s_find);  // barriers inside
+        if (threadIdx.x == 0) {
+            s_share = sh;
+            s_u = sh.start;
+        }
+    }
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes());
     // q takes the scale's sign; a scale of 0 stays one that keeps -inf apart
     const bool minus = a.scale < 0.f;
     const float c = fmaxf(fabsf(a.scale), 1e-30f) * kAttnLog2e;
 
-    bool ok = true;
-    uint32_t blocks = 0;            // K (and V) blocks before this item
+    bool ok = true, more = s_share.start < s_share.end;
+    uint32_t blocks = 0;              // K (and V) blocks before this item
     uint32_t steps_done[2] = {0, 0};  // softmax steps of the slots before this item
     uint32_t items_done[2] = {0, 0};  // items with a step, per slot
-    int64_t u = sh.start;
-    while (u < sh.end) {
-        const AttnReq q = attn_request(a, sh.r, S::kRows, kTok);
-        const int64_t item = (u - sh.base) / q.nb, b0 = (u - sh.base) % q.nb, cnt = min(q.nb - b0, sh.end - u);
-        const int h = static_cast<int>(item / q.tiles), tile = static_cast<int>(item % q.tiles);
-        const int64_t l0 = b0 * kTok, l1 = min((b0 + cnt) * kTok, q.len);
-        const int n = l1 > l0 ? static_cast<int>((l1 - l0 + kTok - 1) / kTok) : 0;
-        const int32_t* table = a.table + sh.r * a.width;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(q.n) * G - static_cast<int64_t>(tile) * S::kRows,
-                                              static_cast<int64_t>(S::kRows)));
-        const bool live1 = !TWO || rows > 128;
-        const int steps0 = TWO ? n : (n + 1) / 2, steps1 = TWO ? (live1 ? n : 0) : n / 2;
+    uint32_t turns[2] = {0, 0};       // turns that the slots have handed on
+    while (more) {
+        if (threadIdx.x == 0) {
+            AttnShare sh = s_share;
+            int64_t u = s_u, b0;
+            const AttnReq q = attn_request(a, sh.r, S::kRows, kTok);
+            attn_place(sh, q, u, g.h, g.tile, b0);
+            const int64_t cnt = min(q.nb - b0, sh.end - u);
+            const int64_t l0 = b0 * kTok, l1 = min((b0 + cnt) * kTok, q.len);
+            auto from_l0 = [&](int64_t l) {
+                return static_cast<int>(min(max(l - l0, -(int64_t(1) << 30)), int64_t(1) << 30));
+            };
+            g.r = static_cast<int>(sh.r);
+            g.n = l1 > l0 ? static_cast<int>((l1 - l0 + kTok - 1) / kTok) : 0;
+            g.group = a.group;
+            g.rows = static_cast<int>(min(static_cast<int64_t>(q.n) * a.group - static_cast<int64_t>(g.tile) * S::kRows,
+                                          static_cast<int64_t>(S::kRows)));
+            g.o0 = q.o0;
+            g.steps[0] = TWO ? g.n : (g.n + 1) / 2;
+            g.steps[1] = TWO ? (g.rows > 128 ? g.n : 0) : g.n / 2;
+            g.ctx = from_l0(q.ctx);
+            g.len = min(from_l0(q.len), static_cast<int>(l1 - l0));
+            g.plain = max(0, min(g.ctx, from_l0(q.len)));
+            g.l0 = l0;
+            g.table = sh.r * a.width;
+            const bool whole = b0 == 0 && cnt == q.nb;
+            g.parts = whole ? -1 : (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * static_cast<int64_t>(attn_part_floats(S::kRows, D));
+            if (b0 == 0 && !whole) static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(sh, g.h, g.tile, u + q.nb);
+            u += cnt;
+            g.last = u >= sh.end;
+            if (u < sh.end) {
+                int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
+                while (u == next) {  // the next request with rows
+                    ++sh.r;
+                    sh.base = next;
+                    next += attn_units(a, sh.r, S::kRows, kTok);
+                }
+                s_share.r = sh.r;
+                s_share.base = sh.base;
+            }
+            s_u = u;
+            s_odd = 0;
+        }
+        __syncthreads();
+        const int n = g.n, steps0 = g.steps[0], steps1 = g.steps[1];
         const int slot = warp >= 8 ? 1 : 0, quarter = warp % 4;  // of the softmax warps
         const int row = 32 * quarter + lane;                     // tensor-memory lane of the thread
-        const int rows_s = TWO ? min(max(rows - 128 * slot, 0), 128) : rows;
-        const int64_t grow = static_cast<int64_t>(tile) * S::kRows + (TWO ? 128 * slot : 0) + row;
+        const int rows_s = TWO ? min(max(g.rows - 128 * slot, 0), 128) : g.rows;
         const bool live = row < rows_s;
-        const int qi = live ? static_cast<int>(grow / G) : 0;
-        const int64_t qt = q.o0 + qi;
-        const int head = h * G + (live ? static_cast<int>(grow % G) : 0);
+        const uint32_t grow = live ? static_cast<uint32_t>(g.tile) * S::kRows + (TWO ? 128 * slot : 0) + row : 0u;
+        const int qi = static_cast<int>(grow / static_cast<uint32_t>(g.group));
+        const int head = g.h * g.group + static_cast<int>(grow) - qi * g.group;
 
         // pages all right? q into shared memory
         bool bad = false;
-        if (n > 0)
-            for (int64_t p = (l0 >> shift) + threadIdx.x; p <= (l1 - 1) >> shift; p += kThreads)
-                bad |= table[p] < 0 || table[p] >= a.cache.num_pages;
+        if (n > 0) {
+            const int64_t p1 = (g.l0 + g.len - 1) >> a.page_shift;
+            for (int64_t p = (g.l0 >> a.page_shift) + threadIdx.x; p <= p1; p += kThreads) {
+                const int32_t e = a.table[g.table + p];
+                bad |= e < 0 || e >= a.cache.num_pages;
+            }
+        }
         if (warp >= 4 && (TWO || slot == 0)) {
-            const uint16_t* src = a.q + qt * a.q_pitch + static_cast<int64_t>(head) * D;
+            const uint16_t* src = a.q + (g.o0 + static_cast<int64_t>(qi)) * a.q_pitch + static_cast<int64_t>(head) * D;
             uint8_t* dst = sm + (TWO ? slot : 0) * S::kQTile + row * 128;
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch) {
@@ -270,236 +397,192 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_async();
         }
-        if (threadIdx.x == 0) s_odd = 0;
         bad = __syncthreads_or(bad);
 
-        if (warp == 0) {
-            // ------------------------------------------------ loads
-            auto entry = [&](int64_t l) -> int { return lane < nbox && l < l1 ? table[l >> shift] : -1; };
-            int64_t l = l0 + lane * br;
-            int next = entry(l);
-            for (int j = 0; j < n && ok; ++j, l += kTok) {
-                const int e = next;
-                next = entry(l + kTok);
-                const int page = e >= 0 && e < a.cache.num_pages ? e : -1;
-                const int at = static_cast<int>(l & (a.cache.page_size - 1));
-                const uint32_t b = blocks + j;
+        if (warp == 0 || warp == 3) {
+            // ------------------------------------------------ loads of K (warp 0) or V (warp 3)
+            const bool is_v = warp == 3;
+            const uint32_t stages = is_v ? S::kVS : S::kKS, ring = is_v ? v_at : k_at;
+            const CUtensorMap* map = is_v ? &map_v : &map_k;
+            const int br = min(a.cache.page_size, kTok), nbox = kTok / br;  // tokens per box, boxes per block
+            const int32_t* table = a.table + g.table;
+            auto entry = [&](int rel) -> int {
+                return lane < nbox && rel < g.len ? table[(g.l0 + rel) >> a.page_shift] : -1;
+            };
+            int rel = lane * br, next = entry(rel);
+            for (int j = 0; j < n; ++j, rel += kTok) {
+                const int page = next >= 0 && next < a.cache.num_pages ? next : -1;
+                const int at = static_cast<int>((g.l0 + rel) & (a.cache.page_size - 1));
+                next = entry(rel + kTok);
+                const uint32_t b = blocks + j, st = b % stages;
+                uint64_t* full = is_v ? &bar.vfull[st] : &bar.kfull[st];
+                uint64_t* empty = is_v ? &bar.vempty[st] : &bar.kempty[st];
+                if (b >= stages) ok = ok && mbar_wait_warp(empty, (b / stages - 1) & 1, &g_attn_error);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full, S::kBlk);
+                __syncwarp();
+                if (lane < nbox) {
+                    const uint32_t dst = ring + st * S::kBlk + lane * br * 128;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t stages = kv ? S::kVS : S::kKS, st = b % stages;
-                    uint64_t* full = kv ? &bar.vfull[st] : &bar.kfull[st];
-                    uint64_t* empty = kv ? &bar.vempty[st] : &bar.kempty[st];
-                    if (b >= stages) ok = ok && mbar_wait_warp(empty, (b / stages - 1) & 1, &g_attn_error);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full, S::kBlk);
-                    __syncwarp();
-                    if (lane < nbox) {
-                        const uint32_t dst = (kv ? v_at : k_at) + st * S::kBlk + lane * br * 128;
-#pragma unroll
-                        for (int d = 0; d < D / 64; ++d)
-                            tma_load_4d(dst + d * (kTok * 128), kv ? &map_v : &map_k, 64 * d, at, h, page, full);
-                    }
-                    __syncwarp();
-                }
-            }
-        } else if (warp == 1) {
-            // ------------------------------------------------ products
-            const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // f32 D, bf16 A and B, M = 128
-            const uint32_t id_s = id | (static_cast<uint32_t>(kTok >> 3) << 17);
-            const uint32_t id_o = id | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);  // B MN-major
-            int pend[2] = {-1, -1};
-            uint32_t used[2] = {steps_done[0], steps_done[1]};  // p blocks taken
-            auto values = [&](int t) {  // o of slot t += p v of its pending block
-                const uint32_t b = blocks + pend[t], st = b % S::kVS;
-                ok = ok && mbar_wait_warp(&bar.pready[t], used[t] & 1, &g_attn_error) &&
-                     mbar_wait_warp(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error);
-                ++used[t];
-                if (!ok) return;
-                tc_fence_after();
-                if (elect_one()) {
-                    const bool first = TWO ? pend[t] == 0 : pend[t] == t;
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(tmem + 256 + t * D, tmem + 128 * t + 8 * k,
-                               desc_sw128(v_at + st * S::kBlk + k * 2048, kTok * 128), id_o, first && k == 0 ? 0u : 1u);
-                    if (!TWO || t == (live1 ? 1 : 0)) mma_commit(&bar.vempty[st]);
+                    for (int d = 0; d < D / 64; ++d) tma_load_4d(dst + d * (kTok * 128), map, 64 * d, at, g.h, page, full);
                 }
                 __syncwarp();
-            };
-            for (int j = 0; j < n && ok; ++j) {
-                const uint32_t b = blocks + j, st = b % S::kKS;
-                ok = ok && mbar_wait_warp(&bar.kfull[st], (b / S::kKS) & 1, &g_attn_error);
+            }
+        } else if (warp < 3) {
+            // ------------------------------------------------ products of slot warp - 1, by one thread
+            const int t = warp - 1, steps = t ? steps1 : steps0;
+            if (lane == 0 && steps > 0) {
+                const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // f32 D, bf16 A and B, M = 128
+                const uint32_t id_s = id | (static_cast<uint32_t>(kTok >> 3) << 17);
+                const uint32_t id_o = id | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);  // B MN-major
+                // descriptors advance by addresses / 16, all below 2^14
+                const uint64_t q_desc = desc_sw128(q_at + (TWO ? t : 0) * S::kQTile, 16), k_desc = desc_sw128(k_at, 16);
+                const uint64_t v_desc = desc_sw128(v_at, kTok * 128);
+                const uint32_t s_col = tmem + 128 * t, o_col = tmem + 256 + t * D;
+                const bool alone = TWO && steps1 == 0;  // the other slot's arrivals are this one's
+                // turn u of slot 0 follows turn u - 1 of slot 1, which follows turn u - 1 of slot 0
+                auto my_turn = [&](int u) {
+                    if (steps1 > 0 && (t == 1 || u > 0))
+                        ok = ok && mbar_wait(&bar.turn[t], (turns[1 - t] + (t ? u : u - 1)) & 1, &g_attn_error);
+                };
+                auto values = [&](int i) {  // o += p v of step i
+                    const uint32_t b = blocks + (TWO ? i : 2 * i + t), st = b % S::kVS, ph = (steps_done[t] + i) & 1;
+                    const uint64_t vd = v_desc + st * (S::kBlk >> 4);
+                    ok = ok && mbar_wait(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (TWO ? (t == 1 && !live1) : (j & 1) != t) continue;
-                    if (pend[t] >= 0) values(t);
+                    for (int f = 1; f >= 0; --f) {  // p's second half comes first
+                        ok = ok && mbar_wait(&bar.pready[t][f], ph, &g_attn_error);
+                        if (f == 1) my_turn(i + 1);
+                        if (!ok) return;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 4 * f; k < 4 * f + 4; ++k)
+                            mma_ts(o_col, s_col + 64 * f + 8 * (k & 3), vd + (k * 2048 >> 4), id_o,
+                                   i == 0 && k == 4 ? 0u : 1u);
+                    }
+                    mma_commit(&bar.vempty[st]);
+                    if (alone) mma_commit(&bar.vempty[st]);
+                };
+                for (int i = 0; i < steps; ++i) {
+                    const uint32_t b = blocks + (TWO ? i : 2 * i + t), st = b % S::kKS;
+                    ok = ok && mbar_wait(&bar.kfull[st], (b / S::kKS) & 1, &g_attn_error);
+                    if (i > 0)
+                        values(i - 1);
+                    else
+                        my_turn(0);
                     if (!ok) break;
                     tc_fence_after();
-                    if (elect_one()) {
+                    const uint64_t kd = k_desc + st * (S::kBlk >> 4);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
-                            mma_ss(tmem + 128 * t, desc_sw128(q_at + (TWO ? t : 0) * S::kQTile + off, 16),
-                                   desc_sw128(k_at + st * S::kBlk + off, 16), id_s, k ? 1u : 0u);
-                        }
-                        mma_commit(&bar.sfull[t]);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+                        mma_ss(s_col, q_desc + off, kd + off, id_s, k ? 1u : 0u);
                     }
-                    __syncwarp();
-                    pend[t] = j;
+                    mma_commit(&bar.sfull[t]);
+                    mbar_arrive(&bar.turn[1 - t]);
+                    mma_commit(&bar.kempty[st]);
+                    if (alone) mma_commit(&bar.kempty[st]);
                 }
-                if (ok && elect_one()) mma_commit(&bar.kempty[st]);
-                __syncwarp();
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = TWO ? i : (n & 1) ^ i;  // the older block first
-                if (pend[t] < 0) continue;
+                if (ok) values(steps - 1);
                 if (ok) {
-                    if (t == 0)
-                        values(0);
-                    else
-                        values(1);
+                    mma_commit(&bar.odone[t]);
+                    mbar_arrive(&bar.turn[1 - t]);
                 }
-                if (ok && elect_one()) mma_commit(&bar.odone[t]);
-                __syncwarp();
             }
-        } else if (warp >= 4) {
+            __syncwarp();
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        } else {
             // ------------------------------------------------ softmax
             const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
             const uint32_t s_at = tmem + lanes + 128 * slot, o_at = tmem + lanes + 256 + slot * D;
-            const int steps = slot ? steps1 : steps0;
             const bool busy = 32 * quarter < rows_s;  // the warp has a live row
-            const int64_t plain = min(q.ctx, q.len);  // tokens that every row sees
             float m = -INFINITY, z = 0.f;
-            for (int i = 0; i < steps; ++i) {
-                const int j = TWO ? i : 2 * i + slot;
-                const int64_t l = l0 + static_cast<int64_t>(j) * kTok;
-                ok = ok && mbar_wait_warp(&bar.sfull[slot], (steps_done[slot] + i) & 1, &g_attn_error);
-                if (!ok) break;
-                tc_fence_after();
-                const bool special = bad || l + kTok > plain;
-                uint32_t pages = 0;  // which boxes are tokens
-                if (special) {
-                    const int64_t lb = l + lane * br;
-                    const int e = lane < nbox && lb < l1 ? table[lb >> shift] : -1;
-                    pages = __ballot_sync(0xFFFFFFFFu, e >= 0 && e < a.cache.num_pages);
-                    if (!TWO || slot == 0) {
-                        // V row `row` of the block: cleared where it is no token, or not finite
-                        const uint32_t b = blocks + j, st = b % S::kVS;
-                        ok = ok && mbar_wait_warp(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error);
-                        uint8_t* v = sm + (v_at - base) + st * S::kBlk + row * 128;
-                        const bool token = l + row < q.len && ((pages >> (row / br)) & 1);
-                        if (!token || l + row >= q.ctx) {
-                            for (int ch = 0; ch < D / 8; ++ch) {
-                                uint4* p = reinterpret_cast<uint4*>(v + (ch / 8) * (kTok * 128) + (ch % 8) * 16);
-                                uint4 x = *p;
-                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                                bool change = !token;
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    const bool lo = (w[y] & 0x7F80u) == 0x7F80u, hi = (w[y] & 0x7F800000u) == 0x7F800000u;
-                                    change |= lo || hi;
-                                    if (!token) w[y] = 0;
-                                    if (lo) w[y] &= 0xFFFF0000u;
-                                    if (hi) w[y] &= 0xFFFFu;
-                                }
-                                if (change) {
-                                    *p = make_uint4(w[0], w[1], w[2], w[3]);
-                                    if (token) s_odd = 1;
-                                }
-                            }
-                        }
-                        fence_async();
-                    }
-                }
-                if (busy) {
-                    uint32_t see[4];  // a special block's visible tokens
+            {
+                const int steps = slot ? steps1 : steps0;
+                const int all_seen = bad ? 0 : g.plain / kTok;  // blocks that every row sees whole
+                const uint32_t phase0 = steps_done[slot];
+                for (int i = 0; i < steps; ++i) {
+                    const int j = TWO ? i : 2 * i + slot;
+                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&bar.sfull[slot], (phase0 + i) & 1, &g_attn_error));
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);
+                    const bool special = j >= all_seen;
                     if (special) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            see[k] = sees32(a, qt, qi, l + 32 * k - q.ctx);
-                            const int64_t left = q.len - (l + 32 * k);
-                            if (left < 32) see[k] &= left <= 0 ? 0u : (1u << left) - 1u;
-                            uint32_t real = 0;
-                            if (br >= 32)
-                                real = ((pages >> (32 * k / br)) & 1) ? 0xFFFFFFFFu : 0u;
-                            else
-                                for (int e = 0; e < 32; ++e) real |= ((pages >> ((32 * k + e) / br)) & 1) << e;
-                            see[k] &= real;
-                        }
+                        const uint32_t b = blocks + j, st = b % S::kVS;
+                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error));
+                        if (!ok) break;
+                        see = special_block<D>(a, g, j, row, g.o0 + static_cast<int64_t>(qi), qi,
+                                               sm + (v_at - base) + st * S::kBlk + row * 128, &s_odd);
                     }
-                    // the scores are read twice, 64 at a time: all 128 would not fit beside the rest
-                    auto scores = [&](int half, uint32_t (&s)[64]) {
-                        tmem_ld(s_at + 64 * half, s);
-                        tmem_ld(s_at + 64 * half + 32, s + 32);
-                        tmem_ld_wait();
-                        if (special)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!((see[2 * half + k] >> e) & 1)) s[32 * k + e] = 0xFF800000u;
-                    };
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    if (busy) {
+                        // 64 scores at a time: all 128 would not fit beside the rest. The second half is still held
+                        // when the maximum is known, so its p comes first; p of a half lies over its own scores.
                         uint32_t s[64];
-                        scores(k, s);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
-                    }
-                    const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                    const bool grown = m != -INFINITY && mn > m + kGrow;
-                    if (__any_sync(0xFFFFFFFFu, grown)) {
-                        const float f = grown ? attn_ex2(m - mn) : 1.f;
-                        z *= f;
-                        const uint64_t ff = pack(f, f);
-                        for (int k = 0; k < D / 32; ++k) {
-                            uint32_t o[32];
-                            tmem_ld(o_at + 32 * k, o);
+                        auto scores = [&](int half) {
+                            tmem_ld(s_at + 64 * half, s);
+                            tmem_ld(s_at + 64 * half + 32, s + 32);
                             tmem_ld_wait();
+                            if (special) {
+                                const uint32_t lo = half ? see.z : see.x, hi = half ? see.w : see.y;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float x, y;
-                                unpack(mul2(pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ff), x, y);
-                                o[e] = __float_as_uint(x);
-                                o[e + 1] = __float_as_uint(y);
+                                for (int e = 0; e < 32; ++e) {
+                                    if (!((lo >> e) & 1)) s[e] = 0xFF800000u;
+                                    if (!((hi >> e) & 1)) s[32 + e] = 0xFF800000u;
+                                }
                             }
-                            tmem_st(o_at + 32 * k, o);
-                        }
-                        tmem_st_wait();
-                    }
-                    if (grown || m == -INFINITY) m = mn;
-                    const float sub = m == -INFINITY ? 0.f : -m;
-                    const uint64_t cc = pack(c, c), ss = pack(sub, sub);
-                    uint64_t z0 = 0, z1 = 0;
+                        };
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t s[64], p[32];
-                        scores(k, s);
+                        for (int k = 0; k < 2; ++k) {
+                            scores(k);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float x, y;
-                            unpack(fma2(pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss),
-                                   x, y);
-                            x = attn_ex2(x);
-                            y = attn_ex2(y);
-                            if (e & 1)
-                                z1 = add2(z1, pack(x, y));
-                            else
-                                z0 = add2(z0, pack(x, y));
-                            p[e] = attn_bf16x2(x, y);
+                            for (int e = 0; e < 64; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
                         }
-                        tmem_st(s_at + 32 * k, p);
+                        const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                        const bool grown = m != -INFINITY && mn > m + kGrow;
+                        if (__any_sync(0xFFFFFFFFu, grown)) {
+                            const float f = grown ? attn_ex2(m - mn) : 1.f;
+                            z *= f;
+                            rescale<D>(o_at, f);
+                        }
+                        if (grown || m == -INFINITY) m = mn;
+                        const float sub = m == -INFINITY ? 0.f : -m;
+                        const uint64_t cc = pack(c, c), ss = pack(sub, sub);
+                        uint64_t z0 = 0, z1 = 0;
+#pragma unroll
+                        for (int k = 1; k >= 0; --k) {
+                            uint32_t p[32];
+                            if (k == 0) scores(0);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float x, y;
+                                unpack(fma2(pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss), x, y);
+                                x = attn_ex2(x);
+                                y = attn_ex2(y);
+                                if (e & 1)
+                                    z1 = add2(z1, pack(x, y));
+                                else
+                                    z0 = add2(z0, pack(x, y));
+                                p[e] = attn_bf16x2(x, y);
+                            }
+                            tmem_st(s_at + 64 * k, p);
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.pready[slot][k]);
+                        }
+                        float x, y;
+                        unpack(add2(z0, z1), x, y);
+                        z += x + y;
+                    } else {
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar.pready[slot][1]);
+                            mbar_arrive(&bar.pready[slot][0]);
+                        }
                     }
-                    float x, y;
-                    unpack(add2(z0, z1), x, y);
-                    z += x + y;
-                    tmem_st_wait();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.pready[slot]);
             }
 
             // ---- the item's end
@@ -522,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (slot == 1) {
-                    s_mz[row][0] = m;
-                    s_mz[row][1] = z;
+                    s_mz[TWO ? 0 : row][0] = m;
+                    s_mz[TWO ? 0 : row][1] = z;
                 }
                 named_sync(1, 256);
             }
@@ -531,17 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool other = !TWO && steps1 > 0;
                 float f0 = 1.f, f1 = 0.f;
                 if (other) {
-                    const float m1 = s_mz[row][0], mm = fmaxf(m, m1);
+                    const float m1 = s_mz[TWO ? 0 : row][0], mm = fmaxf(m, m1);
                     f0 = attn_weight(m, mm);
                     f1 = attn_weight(m1, mm);
-                    z = z * f0 + s_mz[row][1] * f1;
+                    z = z * f0 + s_mz[TWO ? 0 : row][1] * f1;
                     m = mm;
                 }
-                const bool whole = b0 == 0 && cnt == q.nb;
-                const int64_t at = qt * a.Hq + head;
+                const bool whole = g.parts < 0;
+                const int64_t qt = g.o0 + static_cast<int64_t>(qi), at = qt * a.Hq + head;
                 const int prow = (TWO ? 128 * slot : 0) + row;
-                float* part = parts + (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * attn_part_floats(S::kRows, D);
-                const bool odd = s_odd != 0;
+                float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes()) + g.parts;
+                const bool odd = *static_cast<volatile int*>(&s_odd) != 0;
                 for (int k = 0; k < D / 32; ++k) {
                     uint32_t o[32];
                     if (steps0 > 0) {  // a slot that is busy has steps if the other has
@@ -563,12 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!live) continue;
                     if (odd) {  // the drafts' elements that are not finite, for the rows that see them
-                        for (int64_t l = max(l0, q.ctx); l < l1; ++l) {
-                            const int32_t e = table[l >> shift];
-                            if (e < 0 || e >= a.cache.num_pages || !attn_sees(a, qt, qi, l - q.ctx)) continue;
+                        for (int rel = max(0, g.ctx); rel < g.len; ++rel) {
+                            const int64_t l = g.l0 + rel;
+                            const int32_t e = a.table[g.table + (l >> a.page_shift)];
+                            if (e < 0 || e >= a.cache.num_pages || !attn_sees(a, qt, qi, rel - g.ctx)) continue;
                             const uint16_t* v = static_cast<const uint16_t*>(a.cache.v) + e * a.cache.page_stride +
                                                 (l & (a.cache.page_size - 1)) * a.cache.token_stride +
-                                                h * a.cache.head_stride + 32 * k;
+                                                g.h * a.cache.head_stride + 32 * k;
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
                                 if ((v[x] & 0x7F80u) == 0x7F80u)
@@ -578,16 +662,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        const float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                     __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                        const float4 y = make_float4(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]),
-                                                     __uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
                         if (whole) {
-                            const uint2 lo = attn_out4(x, z, 1.f), hi = attn_out4(y, z, 1.f);
+                            const uint2 lo = attn_out4(make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                   __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                                                       z, 1.f);
+                            const uint2 hi = attn_out4(make_float4(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]),
+                                                                   __uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])),
+                                                       z, 1.f);
                             *reinterpret_cast<uint4*>(a.out + at * D + 32 * k + e) = make_uint4(lo.x, lo.y, hi.x, hi.y);
                         } else {
-                            *reinterpret_cast<float4*>(part + prow * D + 32 * k + e) = x;
-                            *reinterpret_cast<float4*>(part + prow * D + 32 * k + e + 4) = y;
+                            // column by column: the rows of a warp are adjacent
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) part[(32 * k + e + i) * S::kRows + prow] = __uint_as_float(o[e + i]);
                         }
                     }
                 }
@@ -596,29 +682,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[S::kRows * D + prow] = m;
                     part[S::kRows * D + S::kRows + prow] = z;
                 }
-                if (b0 == 0 && !whole && row == 0 && slot == 0)
-                    static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(sh, h, tile, u + q.nb);
             }
             tc_fence_before();
             fence_async();  // the join's memory goes back to the copies
         }
-        __syncthreads();
         blocks += n;
         steps_done[0] += steps0;
         steps_done[1] += steps1;
         items_done[0] += steps0 > 0;
         items_done[1] += steps1 > 0;
-        u += cnt;
-        if (u < sh.end) {
-            int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
-            while (u == next) {  // the next request with rows
-                ++sh.r;
-                sh.base = next;
-                next += attn_units(a, sh.r, S::kRows, kTok);
-            }
-        }
+        turns[0] += steps0 > 0 ? steps0 + 1 : 0;
+        turns[1] += steps1 > 0 ? steps1 + 1 : 0;
+        more = !g.last;
+        __syncthreads();  // all have read g and their own of the item
     }
-    if (warp == 0 && !ok) {  // a wait ran out: time for the copies in flight to land before the block ends
+    if ((warp == 0 || warp == 3) && !ok) {  // a wait ran out: time for the copies in flight to land before the block ends
         const long long t0 = clock64();
         while (clock64() - t0 < (1ll << 27)) {
         }
@@ -684,7 +762,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
     tree_attn_wide_kernel<D, TWO><<<kGrid, kThreads, S::kSmem, s>>>(a, mk, mv);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_attn_join<D, S::kRows, kTok, false>(a, kGrid, s);
+    return launch_attn_join(tree_attn_join_columns_kernel<D, S::kRows, kTok>, dim3(kGrid, S::kRows / 8), D, a, s);
 }
 
 }  // namespace
