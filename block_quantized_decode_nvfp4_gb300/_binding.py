@@ -126,10 +126,26 @@ def _ptr(a):
     return a.data_ptr()
 
 
+_current_raw_stream = None  # handle of torch's current stream on the current device
+
+
+def _find_current_raw_stream():
+    """torch's own shortcut to the handle where it has one (0.2 us a call), else through a Stream object (2.9 us)."""
+    global _current_raw_stream
+    import torch
+    torch.cuda.current_stream()  # initialises CUDA, or raises
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or dev is None:
+        _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        _current_raw_stream = lambda: raw(dev())  # noqa: E731
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_raw_stream is None:
+            _find_current_raw_stream()
+        return _current_raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -57,6 +57,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kBlock = 16;         // tokens a token group takes at a time
 constexpr int kUnit = 64;          // tokens per unit of the split
+constexpr int kOver = 1;           // units that an item's beginning and end cost
 constexpr int kRows16 = 16;
 
 template <int D, int RG, bool F8>
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     const uint32_t ring = smem_u32(smem) + tg * (S::kStages * S::kStage);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
-    AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kUnit, s_find);
+    AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kUnit, kOver, s_find);
     int64_t u = sh.start;
     AttnMeta* meta = static_cast<AttnMeta*>(a.ws);
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes());
@@ -182,11 +183,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     const int page_shift = a.page_shift;
 
     while (u < sh.end) {
-        const AttnReq q = attn_request(a, sh.r, S::kRows, kUnit);
+        const AttnReq q = attn_request(a, sh.r, S::kRows, kUnit, kOver);
         int h, tile;
         int64_t b0;
         attn_place(sh, q, u, h, tile, b0);
-        const int64_t cnt = min(q.nb - b0, sh.end - u);
+        int64_t cnt = min(q.nb - b0, sh.end - u);
+        const int64_t u_next = u + cnt, item_end = u + q.nb - b0;
+        // the item's first kOver units stand for what it costs beside its tokens
+        cnt = max(b0 + cnt - kOver, int64_t(0));
+        b0 = max(b0 - kOver, int64_t(0));
+        cnt -= b0;
+        if (cnt <= 0) {
+            u = u_next;
+            continue;
+        }
         const int64_t l0 = b0 * kUnit, l1 = min((b0 + cnt) * kUnit, q.len);
         const int32_t* table = a.table + sh.r * a.width;
         const int rows = static_cast<int>(min(static_cast<int64_t>(q.n) * G - static_cast<int64_t>(tile) * S::kRows,
@@ -525,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 join[(g + 8) * D + d] = o[j][2 + e];
             }
         __syncthreads();
-        const bool whole = b0 == 0 && cnt == q.nb;
+        const bool whole = b0 == 0 && cnt == q.nb - kOver;
         float* part = parts + (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * attn_part_floats(S::kRows, D);
         const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[h] : 1.f;
         for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
@@ -560,15 +570,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 }
             }
         }
-        if (b0 == 0 && !whole && threadIdx.x == 0) meta[blockIdx.x] = attn_meta(sh, h, tile, u + q.nb);
+        if (b0 == 0 && !whole && threadIdx.x == 0) meta[blockIdx.x] = attn_meta(sh, h, tile, item_end);
         __syncthreads();
-        u += cnt;
+        u = u_next;
         if (u < sh.end) {
             int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
             while (u == next) {  // the next request with rows
                 ++sh.r;
                 sh.base = next;
-                next += attn_units(a, sh.r, S::kRows, kUnit);
+                next += attn_units(a, sh.r, S::kRows, kUnit, kOver);
             }
         }
     }
@@ -590,7 +600,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s)
     tree_attn_kernel<D, RG, F8><<<S::kGrid, kThreads, S::kSmem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_attn_join(tree_attn_join_kernel<D, S::kRows, kUnit, F8>, dim3(S::kGrid, S::kRows / 4), D, a, s);
+    return launch_attn_join(tree_attn_join_kernel<D, S::kRows, F8>, dim3(S::kGrid, S::kRows / 4), D, a, s);
 }
 
 template <int D>

@@ -31,10 +31,10 @@ struct AttnReq {
     int64_t ctx;  // cached tokens
     int64_t len;  // tokens to look at
     int tiles;    // of `rows` rows
-    int64_t nb;   // units of `unit` tokens per item
+    int64_t nb;   // units per item: `over` for its beginning and end, then one per `unit` tokens
 };
 
-__device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int64_t r, int rows, int unit)
+__device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int64_t r, int rows, int unit, int over)
 {
     AttnReq q;
     const int T = static_cast<int>(a.T);
@@ -43,13 +43,13 @@ __device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int64_t r, in
     q.ctx = max(a.context[r], 0);
     q.len = min(q.ctx + q.n, a.width * a.cache.page_size);
     q.tiles = static_cast<int>((static_cast<int64_t>(q.n) * a.group + rows - 1) / rows);
-    q.nb = max(int64_t(1), (q.len + unit - 1) / unit);
+    q.nb = over + max(int64_t(1), (q.len + unit - 1) / unit);
     return q;
 }
 
-__device__ __forceinline__ int64_t attn_units(const AttnArgs& a, int64_t r, int rows, int unit)
+__device__ __forceinline__ int64_t attn_units(const AttnArgs& a, int64_t r, int rows, int unit, int over)
 {
-    const AttnReq q = attn_request(a, r, rows, unit);
+    const AttnReq q = attn_request(a, r, rows, unit, over);
     return q.nb * q.tiles * a.cache.heads;
 }
 
@@ -63,14 +63,14 @@ struct AttnShare {
 // Each thread sums a run of requests, one scan places them. sh: THREADS / 32
 // + 2 entries of shared memory; called by the whole CTA.
 template <int THREADS>
-__device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows, int unit, int64_t* sh)
+__device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows, int unit, int over, int64_t* sh)
 {
     constexpr int W = THREADS / kWarp;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int64_t per = (a.R + THREADS - 1) / THREADS;
     const int64_t r0 = min(threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
     int64_t mine = 0;
-    for (int64_t i = r0; i < r1; ++i) mine += attn_units(a, i, rows, unit);
+    for (int64_t i = r0; i < r1; ++i) mine += attn_units(a, i, rows, unit, over);
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < kWarp; d <<= 1) {
@@ -100,7 +100,7 @@ __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows
     if (s.start < s.end && s.start >= first && s.start < first + mine) {
         int64_t b = first, i = r0;
         for (;; ++i) {
-            const int64_t u = attn_units(a, i, rows, unit);
+            const int64_t u = attn_units(a, i, rows, unit, over);
             if (s.start < b + u) break;
             b += u;
         }
@@ -113,7 +113,7 @@ __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows
     return s;
 }
 
-// Unit u of the line: item (kv head, tile) of request s.r and its block.
+// Unit u of the line: item (kv head, tile) of request s.r and the unit in it.
 __device__ __forceinline__ void attn_place(const AttnShare& s, const AttnReq& q, int64_t u, int& h, int& tile,
                                            int64_t& b0)
 {
@@ -182,7 +182,7 @@ __device__ __forceinline__ float attn_weight(float mw, float m)
 // and did not finish: its own second part, then the first parts of the CTAs
 // after it, in order. blockIdx.y: four rows each, D / 4 threads a row. Parts
 // are row by row.
-template <int D, int ROWS, int UNIT, bool F8>
+template <int D, int ROWS, bool F8>
 __global__ void __launch_bounds__(D) tree_attn_join_kernel(AttnArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(D) tree_attn_join_kernel(AttnArgs a)
     if (md.r < 0) return;
     const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
     const int row = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
-    const AttnReq q = attn_request(a, md.r, ROWS, UNIT);
+    const AttnReq q = attn_request(a, md.r, ROWS, 1, 0);
     const int G = a.group;
     const int64_t grow = static_cast<int64_t>(md.tile) * ROWS + row;
     if (grow >= static_cast<int64_t>(q.n) * G) return;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(D) tree_attn_join_kernel(AttnArgs a)
 
 // The same for parts that lie column by column (o [D][rows]): blockIdx.y is
 // eight rows, a thread one of their D columns.
-template <int D, int ROWS, int UNIT>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(D) tree_attn_join_columns_kernel(AttnArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(D) tree_attn_join_columns_kernel(AttnArgs a)
     if (md.r < 0) return;
     const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
     const int row0 = blockIdx.y * 8, d = threadIdx.x, b = blockIdx.x;
-    const AttnReq q = attn_request(a, md.r, ROWS, UNIT);
+    const AttnReq q = attn_request(a, md.r, ROWS, 1, 0);
     const int64_t grow0 = static_cast<int64_t>(md.tile) * ROWS + row0;
     const int live = static_cast<int>(min(static_cast<int64_t>(q.n) * a.group - grow0, int64_t(8)));
     if (live <= 0) return;

@@ -56,6 +56,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTok = 128;  // tokens per block (and unit of the split)
 constexpr int kGrid = 152;
+constexpr int kOver = 4;  // units that an item's beginning and end cost
 constexpr float kGrow = 8.f;
 
 template <int D, bool TWO>
@@ -201,7 +202,7 @@ struct Seg {
     int plain, ctx, len;    // tokens every row sees, cached tokens, tokens: from l0, kept within +-2^30
     int64_t l0, table;      // first token; the request's row of the table
     int64_t parts;          // where its part goes; -1: it is the whole item
-    int last;               // nothing of the CTA's share comes after it
+    int last, skip;         // nothing of the CTA's share comes after it; no token of it is in the share
 };
 
 struct Bars {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int64_t s_u;
     __shared__ Seg g;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_odd;
+    __shared__ int s_odd, s_bad;
     __shared__ float s_mz[TWO ? 1 : 128][2];  // slot 1's m and z, for the join
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const sm = smem_raw + (base - smem_u32(smem_raw));
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     {
-        const AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kTok, s_find);  // barriers inside
+        const AttnShare sh = attn_find_share<kThreads>(a, S::kRows, kTok, kOver, s_find);  // barriers inside
         if (threadIdx.x == 0) {
             s_share = sh;
             s_u = sh.start;
@@ -329,10 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) {
             AttnShare sh = s_share;
             int64_t u = s_u, b0;
-            const AttnReq q = attn_request(a, sh.r, S::kRows, kTok);
+            const AttnReq q = attn_request(a, sh.r, S::kRows, kTok, kOver);
             attn_place(sh, q, u, g.h, g.tile, b0);
-            const int64_t cnt = min(q.nb - b0, sh.end - u);
-            const int64_t l0 = b0 * kTok, l1 = min((b0 + cnt) * kTok, q.len);
+            int64_t cnt = min(q.nb - b0, sh.end - u);
+            const int64_t item_end = u + q.nb - b0;
+            u += cnt;
+            // the item's first kOver units stand for what it costs beside its tokens
+            cnt = max(b0 + cnt - kOver, int64_t(0));
+            b0 = max(b0 - kOver, int64_t(0));
+            cnt -= b0;
+            g.skip = cnt <= 0;
+            const int64_t l0 = b0 * kTok, l1 = min((b0 + max(cnt, int64_t(0))) * kTok, q.len);
             auto from_l0 = [&](int64_t l) {
                 return static_cast<int>(min(max(l - l0, -(int64_t(1) << 30)), int64_t(1) << 30));
             };
@@ -349,25 +357,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             g.plain = max(0, min(g.ctx, from_l0(q.len)));
             g.l0 = l0;
             g.table = sh.r * a.width;
-            const bool whole = b0 == 0 && cnt == q.nb;
+            const bool whole = b0 == 0 && cnt == q.nb - kOver;
             g.parts = whole ? -1 : (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * static_cast<int64_t>(attn_part_floats(S::kRows, D));
-            if (b0 == 0 && !whole) static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(sh, g.h, g.tile, u + q.nb);
-            u += cnt;
+            if (b0 == 0 && !whole && !g.skip) static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(sh, g.h, g.tile, item_end);
             g.last = u >= sh.end;
             if (u < sh.end) {
                 int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
                 while (u == next) {  // the next request with rows
                     ++sh.r;
                     sh.base = next;
-                    next += attn_units(a, sh.r, S::kRows, kTok);
+                    next += attn_units(a, sh.r, S::kRows, kTok, kOver);
                 }
                 s_share.r = sh.r;
                 s_share.base = sh.base;
             }
             s_u = u;
-            s_odd = 0;
+            s_odd = s_bad = 0;
         }
         __syncthreads();
+        more = !g.last;
+        if (g.skip) {
+            __syncthreads();
+            continue;
+        }
         const int n = g.n, steps0 = g.steps[0], steps1 = g.steps[1];
         const int slot = warp >= 8 ? 1 : 0, quarter = warp % 4;  // of the softmax warps
         const int row = 32 * quarter + lane;                     // tensor-memory lane of the thread
@@ -377,27 +389,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qi = static_cast<int>(grow / static_cast<uint32_t>(g.group));
         const int head = g.h * g.group + static_cast<int>(grow) - qi * g.group;
 
-        // pages all right? q into shared memory
-        bool bad = false;
-        if (n > 0) {
-            const int64_t p1 = (g.l0 + g.len - 1) >> a.page_shift;
-            for (int64_t p = (g.l0 >> a.page_shift) + threadIdx.x; p <= p1; p += kThreads) {
-                const int32_t e = a.table[g.table + p];
-                bad |= e < 0 || e >= a.cache.num_pages;
-            }
-        }
-        if (warp >= 4 && (TWO || slot == 0)) {
-            const uint16_t* src = a.q + (g.o0 + static_cast<int64_t>(qi)) * a.q_pitch + static_cast<int64_t>(head) * D;
-            uint8_t* dst = sm + (TWO ? slot : 0) * S::kQTile + row * 128;
+        if (warp >= 4) {
+            // q into shared memory; pages all right?
+            if (TWO || slot == 0) {
+                const uint16_t* src = a.q + (g.o0 + static_cast<int64_t>(qi)) * a.q_pitch + static_cast<int64_t>(head) * D;
+                uint8_t* dst = sm + (TWO ? slot : 0) * S::kQTile + row * 128;
 #pragma unroll
-            for (int ch = 0; ch < D / 8; ++ch) {
-                uint4 x = live ? *reinterpret_cast<const uint4*>(src + 8 * ch) : make_uint4(0, 0, 0, 0);
-                if (minus) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
-                *reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + (((ch % 8) ^ (row & 7)) << 4)) = x;
+                for (int ch = 0; ch < D / 8; ++ch) {
+                    uint4 x = live ? *reinterpret_cast<const uint4*>(src + 8 * ch) : make_uint4(0, 0, 0, 0);
+                    if (minus) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+                    *reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + (((ch % 8) ^ (row & 7)) << 4)) = x;
+                }
+                fence_async();
             }
-            fence_async();
+            if (n > 0) {
+                const int64_t p1 = (g.l0 + g.len - 1) >> a.page_shift;
+                for (int64_t p = (g.l0 >> a.page_shift) + (threadIdx.x - 128); p <= p1; p += 256) {
+                    const int32_t e = a.table[g.table + p];
+                    if (e < 0 || e >= a.cache.num_pages) s_bad = 1;
+                }
+            }
         }
-        bad = __syncthreads_or(bad);
+        if (warp != 0 && warp != 3) named_sync(2, kThreads - 64);  // the loads need not wait for q
 
         if (warp == 0 || warp == 3) {
             // ------------------------------------------------ loads of K (warp 0) or V (warp 3)
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, z = 0.f;
             {
                 const int steps = slot ? steps1 : steps0;
-                const int all_seen = bad ? 0 : g.plain / kTok;  // blocks that every row sees whole
+                const int all_seen = s_bad ? 0 : g.plain / kTok;  // blocks that every row sees whole
                 const uint32_t phase0 = steps_done[slot];
                 for (int i = 0; i < steps; ++i) {
                     const int j = TWO ? i : 2 * i + slot;
@@ -693,7 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         items_done[1] += steps1 > 0;
         turns[0] += steps0 > 0 ? steps0 + 1 : 0;
         turns[1] += steps1 > 0 ? steps1 + 1 : 0;
-        more = !g.last;
         __syncthreads();  // all have read g and their own of the item
     }
     if ((warp == 0 || warp == 3) && !ok) {  // a wait ran out: time for the copies in flight to land before the block ends
@@ -762,7 +774,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
     tree_attn_wide_kernel<D, TWO><<<kGrid, kThreads, S::kSmem, s>>>(a, mk, mv);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_attn_join(tree_attn_join_columns_kernel<D, S::kRows, kTok>, dim3(kGrid, S::kRows / 8), D, a, s);
+    return launch_attn_join(tree_attn_join_columns_kernel<D, S::kRows>, dim3(kGrid, S::kRows / 8), D, a, s);
 }
 
 }  // namespace
