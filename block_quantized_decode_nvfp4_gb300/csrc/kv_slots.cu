@@ -26,8 +26,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 4;  // requests per thread and chunk
 constexpr int kChunk = kThreads * kPer;
-constexpr int kTokens = 1024;  // tokens per CTA at least (four per thread)
-constexpr int kMaxCtas = 152;
+constexpr int kTokens = kThreads;  // tokens per CTA at least (one per thread)
+constexpr int kMaxCtas = 2 * 152;
 
 struct Need {
     int64_t c, n;        // cached and new tokens
@@ -48,6 +48,7 @@ __device__ __forceinline__ Need need_of(const SlotsArgs& a, int64_t r)
 __global__ void __launch_bounds__(kThreads) paged_slots_kernel(const SlotsArgs a)
 {
     __shared__ int64_t s_tok[kChunk + 1], s_page[kChunk + 1];  // exclusive sums of the chunk's requests
+    __shared__ int32_t s_ctx[kChunk];
     __shared__ int64_t s_warp[kThreads / kWarp][2];
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int64_t share = (a.capacity + gridDim.x - 1) / gridDim.x;
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(kThreads) paged_slots_kernel(const SlotsArgs a
             tk[i] = pg[i] = 0;
             if (k < count) {
                 const Need x = need_of(a, r0 + k);
+                s_ctx[k] = static_cast<int32_t>(x.c);
                 tk[i] = x.n;
                 pg[i] = x.want - x.have;
                 full |= x.n > 0 && ((x.c + x.n - 1) >> a.page_shift) >= a.width;
@@ -130,17 +132,17 @@ __global__ void __launch_bounds__(kThreads) paged_slots_kernel(const SlotsArgs a
                 else
                     hi = mid;
             }
-            const Need x = need_of(a, r0 + lo);
-            const int64_t j = t - s_tok[lo], b = (x.c + j) >> a.page_shift;
+            const int64_t ctx = s_ctx[lo], j = t - s_tok[lo], b = (ctx + j) >> a.page_shift;
+            const int64_t have = min((ctx + (int64_t(1) << a.page_shift) - 1) >> a.page_shift, a.width);
             int64_t slot = -1;
             if (b < a.width) {
-                const int64_t f = s_page[lo] + b - x.have;
-                const int32_t page = b < x.have ? a.table[(r0 + lo) * a.width + b] : f < a.num_free ? a.free_pages[f] : -1;
+                const int64_t f = s_page[lo] + b - have;
+                const int32_t page = b < have ? a.table[(r0 + lo) * a.width + b] : f < a.num_free ? a.free_pages[f] : -1;
                 if (page >= 0)
-                    slot = (static_cast<int64_t>(page) << a.page_shift) + ((x.c + j) & ((1 << a.page_shift) - 1));
+                    slot = (static_cast<int64_t>(page) << a.page_shift) + ((ctx + j) & ((1 << a.page_shift) - 1));
             }
             a.slots[t] = slot;
-            a.positions[t] = static_cast<int32_t>(x.c + (a.depths ? a.depths[t] : j));
+            a.positions[t] = static_cast<int32_t>(ctx + (a.depths ? a.depths[t] : j));
         }
         __syncthreads();  // the next chunk overwrites the sums
     }
