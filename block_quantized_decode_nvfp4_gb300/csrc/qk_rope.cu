@@ -13,9 +13,9 @@
 // then the rest two by two) go to its lanes in order, eight each: both ends
 // of a pair are in one lane, the rotation needs no exchange, and a lane's
 // elements are two runs of eight (rot / 2 is a multiple of 8). Arithmetic is
-// two elements an instruction. A lane keeps the weights of its places from
-// step to step; a step's loads are issued before the step before it is
-// worked on.
+// two elements an instruction. Weights and angles come from L1 at every step,
+// which leaves the registers to loads in flight: two steps of bf16 or one of
+// fp32 ahead of the work, 2 KiB a warp and 64 KiB an SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -96,7 +96,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const uint64_t (&y)[kRun 
 }
 
 template <typename T, int D, bool F8, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 3) qk_rope_kernel(const QkRopeArgs a, uint32_t groups, int run)
+__global__ void __launch_bounds__(kThreads, 4) qk_rope_kernel(const QkRopeArgs a, uint32_t groups, int run)
 {
     constexpr int L = D / 16, HW = kWarp / L;  // lanes of a head, heads of a step
     constexpr int N = kRun / 2;
@@ -123,15 +123,17 @@ __global__ void __launch_bounds__(kThreads, 3) qk_rope_kernel(const QkRopeArgs a
     const T* qb = static_cast<const T*>(a.q) + t * a.q_pitch;
     const T* kb = static_cast<const T*>(a.k) + t * a.k_pitch - static_cast<int64_t>(a.Hq) * D;
     const T* vb = static_cast<const T*>(a.v) + t * a.v_pitch - static_cast<int64_t>(a.Hq + Hkv) * D;
-    Raw<T> lo, hi;
-    auto fetch = [&](int h) {
+    constexpr int kFar = sizeof(T) == 2 ? 2 : 1;  // steps in flight
+    Raw<T> lo[kFar], hi[kFar];
+    auto fetch = [&](int i, int h) {
         if (h < h1) {
             const T* src = (h < a.Hq ? qb : h < a.Hq + Hkv ? kb : vb) + static_cast<int64_t>(h) * D;
-            lo.load(src + e0);
-            hi.load(src + e1);
+            lo[i].load(src + e0);
+            hi[i].load(src + e1);
         }
     };
-    fetch(h0);
+#pragma unroll
+    for (int i = 0; i < kFar; ++i) fetch(i, h0 + i * HW);
     const int pos = a.rot ? a.positions[t] : 0;
     const bool pos_ok = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
     const int64_t slot = h1 > a.Hq ? a.slots[t] : -1;
@@ -141,45 +143,42 @@ __global__ void __launch_bounds__(kThreads, 3) qk_rope_kernel(const QkRopeArgs a
                                      (slot & (a.cache.page_size - 1)) * a.cache.token_stride
                                : 0;
     const bool turns = pos_ok && s < half;
-    uint64_t cs[N] = {}, sn[N] = {};  // one angle per pair
-    if (turns) {
-        const float* p = a.cos_sin + static_cast<int64_t>(pos) * a.rot + s;
-        load8(p, cs);
-        load8(p + half, sn);
-    }
-    const float* held = nullptr;  // whose weights the lane holds
-    uint64_t w0[N], w1[N];
+    const float* angles = a.cos_sin + static_cast<int64_t>(turns ? pos : 0) * a.rot + s;  // one per pair
 
-    for (int h = h0; h - lane / L < h1; h += HW) {  // as often for every lane of the warp
+    for (int hb = h0; hb - lane / L < h1; hb += kFar * HW)  // as often for every lane of the warp
+#pragma unroll
+    for (int i = 0; i < kFar; ++i) {
+        const int h = hb + i * HW;
+        if (h - lane / L >= h1) break;
         uint64_t y0[N], y1[N];
-        lo.get(y0);
-        hi.get(y1);
-        fetch(h + HW);
+        lo[i].get(y0);
+        hi[i].get(y1);
+        fetch(i, h + kFar * HW);
         const bool live = h < h1, is_q = live && h < a.Hq, is_k = live && !is_q && h < a.Hq + Hkv;
         const float* w = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
         uint64_t ss2 = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss2 = fma2(y1[i], y1[i], fma2(y0[i], y0[i], ss2));
+        for (int x = 0; x < N; ++x) ss2 = fma2(y1[x], y1[x], fma2(y0[x], y0[x], ss2));
         float ss, st;
         unpack(ss2, ss, st);
         ss += st;
 #pragma unroll
         for (int d = L / 2; d; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
         if (w) {
-            if (w != held) {
-                load8(w + e0, w0);
-                load8(w + e1, w1);
-                held = w;
-            }
             const float r = rsqrtf(ss * (1.f / D) + a.eps);
             const uint64_t rr = pack(r, r);
+            uint64_t g[N];
+            load8(w + e0, g);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                y0[i] = mul2(mul2(y0[i], rr), w0[i]);
-                y1[i] = mul2(mul2(y1[i], rr), w1[i]);
-            }
+            for (int x = 0; x < N; ++x) y0[x] = mul2(mul2(y0[x], rr), g[x]);
+            load8(w + e1, g);
+#pragma unroll
+            for (int x = 0; x < N; ++x) y1[x] = mul2(mul2(y1[x], rr), g[x]);
         }
         if (turns && (is_q || is_k)) {
+            uint64_t cs[N], sn[N];
+            load8(angles, cs);
+            load8(angles + half, sn);
             if (PAIRS) {
                 // pairs 0 .. 3 in y0, 4 .. 7 in y1, each one register pair
 #pragma unroll
