@@ -1,26 +1,33 @@
 // logprobs.cu -- log probability of given tokens, entropy and the top
 // alternatives of logits rows, in one pass over the logits.
 //
-// With m = max x, z = sum e^(x - m), u = sum e^(x - m) (x - m):
-//   lse = m + log z, logprob = x_tok - lse, entropy = log z - u / z,
+// With m = max x, t = (x - m) log2(e), z = sum 2^t and u = sum 2^t t:
+//   lse = m + log2(z) ln 2, logprob = x_tok - lse, entropy = (log2 z - u / z)
+//   ln 2,
 // and two partial results join as m = max(m1, m2), f = e^(m1 - m), z1' = f z1,
-// u1' = f (u1 + z1 (m1 - m)), likewise the other, and sums. The alternatives
-// are ordered by one 64-bit key per logit: the value's bits made monotonic
-// (NaN lowest, -0 as +0) above the complemented index, so equal values go to
+// u1' = f (u1 + z1 log2 f), likewise the other, and sums. t is one multiply-add,
+// x log2(e) - r with r = m log2(e) rounded (what the rounding moved goes back
+// into lse; the fp32 log2(e) is 1.3e-8 off, which moves lse by as much of
+// itself). The alternatives are ordered by one
+// 64-bit key per logit: the value's bits made monotonic (NaN lowest, -0 as
+// +0) above the complemented index, so equal values go to
 // the lower index; the k largest keys of a row are the k largest of the k
 // largest of its parts.
 //
-// A row is shared by a cluster of C CTAs (1 to 16: one for many rows, 16 for
-// a decode step's few), which join through distributed shared memory, so the
-// call is one launch and needs no workspace. The row's whole 16-byte windows
-// come through a ring of 32 KiB bulk copies (three stages, two CTAs per SM:
-// 128 KiB and more in flight per SM); its ragged ends, at most 14 logits, are
-// read one by one. The warps run through the ring without a barrier of the
-// CTA. A tile costs its maximum, the sums (two logits an instruction where
-// there is a packed form) and a compare of the thread's maximum with tau.
+// Few rows: a row is shared by a cluster of C CTAs (16 for a decode step's one
+// row), which join through distributed shared memory; of many rows each has a
+// CTA. Either way the call is one launch and needs no workspace.
+// A row's whole 16-byte windows come through a ring of 32 KiB bulk copies
+// (two stages, three CTAs per SM: 96 KiB and more in flight per SM); its
+// ragged ends, at most 14 logits, are read one by one. The warps run through
+// the ring without a barrier of the CTA. A tile costs its maximum, the sums
+// (two logits an instruction where there is a packed form) and a compare of
+// the thread's maximum with tau; what a tile costs beside its logits (waits,
+// addresses) made 32 KiB better than 16 or 8 KiB (the sums of 2047 bf16 rows of
+// 151936: 128, 147 and 215 us).
 //
-// Alternatives. The k-th largest of the maxima that the CTA's 32 half-warps
-// have seen has k logits at or above it: that is tau, published in shared
+// Alternatives. The k-th largest of the maxima that the CTA's 32 groups of
+// lanes (8 or 16) have seen has k logits at or above it: that is tau, published in shared
 // memory after the first tile and again by every warp that meets a logit at
 // or above it (the maxima only grow, so an older one is a bound too). What
 // passes goes to the warp's own list of up to 64 keys; one that has grown past
@@ -50,19 +57,14 @@ __device__ unsigned int g_logprobs_error = 0;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / kWarp;
-constexpr int kPer = 4;                             // windows per thread and tile
-constexpr int kTileWindows = kThreads * kPer;
+constexpr int kPer = 4;                             // windows per thread and pass over a tile
+constexpr int kTileWindows = 2048;
 constexpr int kTileBytes = kTileWindows * 16;
-constexpr int kStages = 3;
 constexpr int kList = 64;                           // entries of a warp's list
 constexpr int kMaxK = 32;
 constexpr int kMaxCluster = 16;
-static_assert(kMaxCluster * kMaxK <= kThreads, "the leader takes one key per thread");
-static_assert(2 * kWarps == kWarp, "a warp ranks the half-warps' maxima, one per lane");
 static_assert(kList == 2 * kWarp && kMaxK <= kWarp, "a cut handles two keys per lane, and leaves room for a ballot");
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
 {
@@ -95,21 +97,31 @@ struct Sums {
     float m, z, u;
 };
 
+// Beyond this size a maximum's product with log2(e) may overflow (a row masked
+// throughout by the type's lowest value): differences are taken first there.
+constexpr float kHuge = 1e38f;
+
 __device__ __forceinline__ void raise(Sums& s, float m)  // s relative to m >= s.m
 {
     if (s.m != -INFINITY) {
-        const float d = s.m - m, f = ex2(d * kLog2e);
+        const bool plain = fabsf(s.m) < kHuge && fabsf(m) < kHuge;
+        // rounded products, as add() takes them: equal maxima must give 0
+        const float d = plain ? __fmul_rn(s.m, kLog2e) - __fmul_rn(m, kLog2e) : (s.m - m) * kLog2e, f = ex2(d);
         s.u = d < -150.f ? 0.f : (s.u + s.z * d) * f;
         s.z *= f;
     }
     s.m = m;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b)
+// The join of a warp's 32, the same in every lane.
+__device__ __forceinline__ Sums join_warp(Sums s)
 {
-    const float m = max_nan(a.m, b.m);
-    raise(a, m);
-    raise(b, m);
-    return {m, a.z + b.z, a.u + b.u};
+    float m = s.m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    raise(s, m);
+    s.z = warp_sum(s.z);
+    s.u = warp_sum(s.u);
+    return s;
 }
 
 // A thread's kPer 16-byte windows of a tile.
@@ -158,68 +170,84 @@ struct Chunk {
             return max_nan(__low2float(m), __high2float(m));
         }
     }
-    // z += sum e^(x - m), u += sum e^(x - m) (x - m). Between -1e29 and 1e29
-    // of m, logits below -1e30 (-inf, and masks by the type's lowest value)
-    // count as -1e30: their e^(x - m) is 0 either way, and x - m stays finite.
-    __device__ __forceinline__ void add(float m, float& z, float& u) const
+    // Windows of it that are padding, when there are numbers above -1e29 in it:
+    // a value that adds nothing and keeps t finite.
+    __device__ __forceinline__ void pad(int j)
     {
-        if (fabsf(m) < 1e29f) {
-            const uint64_t mm = pack(-m, -m), l2 = pack(kLog2e, kLog2e);
-            uint64_t zz = 0, uu = 0;
-            const __nv_bfloat162 low = __float2bfloat162_rn(-1e30f);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
+        for (int i = 0; i < 4; ++i) w[j][i] = sizeof(T) == 4 ? 0xF149F2CAu : 0xF14AF14Au;  // -1e30
+    }
+    // z += sum 2^t, u += sum 2^t t; false, and nothing added, where a t is -inf
+    // (a logit of -inf or of the type's lowest value: 0 * -inf), or m is huge.
+    __device__ __forceinline__ bool add(float m, float& z, float& u) const
+    {
+        const float r = -__fmul_rn(m, kLog2e);
+        const uint64_t r2 = pack(r, r), l2 = pack(kLog2e, kLog2e);
+        uint64_t zz = 0, uu = 0;
 #pragma unroll
-                for (int e = 0; e < kN; e += 2) {
-                    uint64_t x;
-                    if constexpr (sizeof(T) == 4) {
-                        x = pack(fmaxf(__uint_as_float(w[j][e]), -1e30f), fmaxf(__uint_as_float(w[j][e + 1]), -1e30f));
-                    } else {
-                        const __nv_bfloat162 b = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[j][e / 2]), low);
-                        const uint32_t v = *reinterpret_cast<const uint32_t*>(&b);
-                        x = pack(bf16_lo(v), bf16_hi(v));
-                    }
-                    const uint64_t d = add2(x, mm);
-                    float a, b;
-                    unpack(mul2(d, l2), a, b);
-                    const uint64_t p = pack(ex2(a), ex2(b));
-                    zz = add2(zz, p);
-                    uu = fma2(p, d, uu);
-                }
-            float a, b;
-            unpack(zz, a, b);
-            z += a + b;
-            unpack(uu, a, b);
-            u += a + b;
-        } else {
-            const float mm = m == -INFINITY ? 0.f : m;
+        for (int j = 0; j < kPer; ++j)
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-#pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    // -150: e^-150 is 0 in fp32, and 0 * -inf is not
-                    const float d = fmaxf(get(j, e) - mm, -150.f), p = ex2(d * kLog2e);
-                    z += p;
-                    u += p * d;
-                }
-        }
+            for (int e = 0; e < kN; e += 2) {
+                const uint64_t t = fma2(pack(get(j, e), get(j, e + 1)), l2, r2);
+                float v, w;
+                unpack(t, v, w);
+                const uint64_t p = pack(ex2(v), ex2(w));
+                zz = add2(zz, p);
+                uu = fma2(p, t, uu);
+            }
+        float a, b, c, d;
+        unpack(zz, a, b);
+        unpack(uu, c, d);
+        if (c + d != c + d || !(fabsf(m) < kHuge)) return false;
+        z += a + b;
+        u += c + d;
+        return true;
     }
 };
 
+// The same for any logits, from the tile in shared memory: t kept above -150
+// (2^-150 is 0 in fp32), and differences first where m is huge.
+template <typename T>
+__device__ __noinline__ float2 add_slowly(const uint8_t* at, int stride, int windows, float m)
+{
+    constexpr int N = 16 / static_cast<int>(sizeof(T));
+    const bool plain = fabsf(m) < kHuge;
+    const float mm = m == -INFINITY ? 0.f : m, r = -__fmul_rn(m, kLog2e);
+    float2 s = make_float2(0.f, 0.f);
+    for (int j = 0; j < windows; ++j, at += stride)
+        for (int e = 0; e < N; ++e) {
+            float x;
+            if constexpr (sizeof(T) == 4)
+                x = reinterpret_cast<const float*>(at)[e];
+            else
+                x = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[e]) << 16);
+            const float t = fmaxf(plain ? fmaf(x, kLog2e, r) : (x - mm) * kLog2e, -150.f), p = ex2(t);
+            s.x += p;
+            s.y += p * t;
+        }
+    return s;
+}
+
+template <int WARPS, int STAGES>
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
-    alignas(16) uint64_t list[kWarps][kList];  // a warp's candidates, read 16 bytes at a time
-    uint64_t top[kMaxK];                       // this CTA's best, descending
-    Sums sums[kWarps];
-    uint32_t bound[kWarp];                     // the half-warps' maxima, as ordered bits; 0: none above -inf
-    uint32_t tau;                              // the k-th largest of them; 0: fewer than k
+    uint64_t full[STAGES], empty[STAGES];
+    union {
+        alignas(16) uint64_t list[WARPS][kList];  // a warp's candidates, read 16 bytes at a time
+        uint64_t all_top[kMaxCluster][kMaxK];     // of a cluster's leader: every CTA's best, once its lists are cut
+    };
+    // keys to be cut to the k best: at most kMaxK of each warp, or of each CTA; +16: padding
+    alignas(16) uint64_t cand[kMaxCluster * kMaxK + 16];
+    uint64_t top[kMaxK];                      // this CTA's best, descending
+    Sums sums[WARPS];
+    alignas(16) uint32_t bound[kWarp];        // the lane groups' maxima, as ordered bits; 0: none above -inf
+    uint32_t tau;                             // the k-th largest of them; 0: fewer than k
     int count;
-    int all_n[kMaxCluster];                    // of the leader: every CTA's number of best, sums and best
+    int all_n[kMaxCluster];                   // of the leader: every CTA's number of best, and sums
     Sums all_sums[kMaxCluster];
-    uint64_t all_top[kMaxCluster][kMaxK];
-    uint64_t all_tau;
 };
-static_assert(offsetof(Shared, list) % 16 == 0 && kList % 2 == 0, "16-byte reads of the lists");
+using Shared8 = Shared<8, 2>;
+static_assert(offsetof(Shared8, list) % 16 == 0 && offsetof(Shared8, cand) % 16 == 0 && kList % 2 == 0,
+              "16-byte reads of the lists");
 
 // A bound's value: everything for none.
 __device__ __forceinline__ float bits_value(uint32_t b) { return b == 0 ? -INFINITY : ordered_value(b); }
@@ -227,17 +255,17 @@ __device__ __forceinline__ float bits_value(uint32_t b) { return b == 0 ? -INFIN
 // The ordered bits of a value: the upper half of its key.
 __device__ __forceinline__ uint32_t order_bits(float x) { return static_cast<uint32_t>(order_key(x, 0) >> 32); }
 
-// The k-th largest of the 32 lanes' values.
-__device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k)
+// The k-th largest of 32 values, at least: the values are cut to their upper
+// 27 bits and the lane's number, which makes them distinct. The same for every
+// lane.
+__device__ __forceinline__ uint32_t kth_of_32(const volatile uint32_t* v, int k)
 {
     const int lane = threadIdx.x % kWarp;
-    int r = 0;  // how many are ahead of this lane's
-#pragma unroll
-    for (int l = 0; l < kWarp; ++l) {
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, v, l);
-        r += o > v || (o == v && l < lane);
-    }
-    return __shfl_sync(0xFFFFFFFFu, v, __ffs(__ballot_sync(0xFFFFFFFFu, r == k - 1)) - 1);
+    const uint32_t mine = (v[lane] & ~31u) | lane;
+    int r = 0;  // how many are ahead
+#pragma unroll 8
+    for (int l = 0; l < kWarp; ++l) r += __shfl_sync(0xFFFFFFFFu, mine, l) > mine;
+    return __shfl_sync(0xFFFFFFFFu, mine, __ffs(__ballot_sync(0xFFFFFFFFu, r == k - 1)) - 1) & ~31u;
 }
 
 // Cuts a warp's list of n <= kList keys back to its k best, descending.
@@ -258,20 +286,39 @@ __device__ __noinline__ void cut_list(uint64_t* list, int n, int k)
     __syncwarp();
 }
 
-// The k best of c keys at cand (16-byte aligned, room for c + 1) in
-// descending order to top. Called by the whole CTA, with a barrier before.
+// Adds the warp's keys that are `in` to a list of the CTA's.
+__device__ __forceinline__ void collect(uint64_t* cand, int* count, uint64_t key, bool in)
+{
+    const int lane = threadIdx.x % kWarp;
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, in);
+    int at = 0;
+    if (lane == 0 && b) at = atomicAdd(count, __popc(b));
+    at = __shfl_sync(0xFFFFFFFFu, at, 0);
+    if (in) cand[at + __popc(b & ((1u << lane) - 1))] = key;
+}
+
+// The k best of c keys at cand (room for 16 more) in descending order to top:
+// eight lanes count a key's larger ones. Called by the whole CTA, with a
+// barrier before.
+template <int WARPS>
 __device__ __forceinline__ void cut_all(uint64_t* cand, int c, uint64_t* top, int k)
 {
-    if (threadIdx.x == 0) cand[c] = 0;
+    if (threadIdx.x < 16) cand[c + threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < c; i += kThreads) {
-        const uint64_t mine = cand[i];
+    const int sub = threadIdx.x % 8, group = threadIdx.x / 8;
+#pragma unroll 1
+    for (int i = group; i - group < c; i += WARPS * 4) {  // whole warps
+        const uint64_t mine = i < c ? cand[i] : 0;
         int r = 0;
-        for (int j = 0; j < c; j += 2) {
+#pragma unroll 2
+        for (int j = 2 * sub; j < c; j += 16) {
             const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&cand[j]);
             r += (v.x > mine) + (v.y > mine);
         }
-        if (r < k) top[r] = mine;
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, 1);
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, 2);
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, 4);
+        if (sub == 0 && mine && r < k) top[r] = mine;
     }
     __syncthreads();
 }
@@ -283,63 +330,83 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, int rank)  // its coun
     return r;
 }
 
+// A CTA's part of a row. 16-byte windows are counted from the one that holds
+// the row's first logit; `pre` elements of it lie before the row. The CTA has
+// the whole windows [w0, w1).
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs a, int C)
+struct Part {
+    const T* x;
+    int pre, tiles;
+    int whole0, whole1, w0, w1;  // below 2^30: V is below 2^31
+    __device__ __forceinline__ Part(const LogprobArgs& a, int64_t t, int rank, int C)
+    {
+        constexpr int N = 16 / static_cast<int>(sizeof(T));
+        x = static_cast<const T*>(a.x) + t * a.pitch;
+        pre = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+        whole0 = pre ? 1 : 0;
+        whole1 = max(whole0, static_cast<int>((static_cast<uint32_t>(pre) + static_cast<uint32_t>(a.V)) / N));
+        const uint32_t whole = whole1 - whole0, share = (whole + C - 1) / static_cast<uint32_t>(C);
+        w0 = whole0 + static_cast<int>(min(share * rank, whole));
+        w1 = whole0 + static_cast<int>(min(share * (rank + 1), whole));
+        tiles = (w1 - w0 + kTileWindows - 1) / kTileWindows;
+    }
+};
+
+// CLUSTER: C CTAs a row; else one.
+template <typename T, int WARPS, int STAGES, int CTAS, bool CLUSTER>
+__global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(const LogprobArgs a, int C)
 {
     using K = Chunk<T>;
-    constexpr int N = K::kN;
+    constexpr int kStages = STAGES, N = K::kN, kThreads = WARPS * kWarp, kGroup = WARPS;  // lanes per group: 32 groups
+    constexpr int kPasses = kTileWindows / (kThreads * kPer);
+    static_assert(kPasses * kThreads * kPer == kTileWindows && (WARPS == 8 || WARPS == 16), "tile shape");
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ __align__(16) Shared s;
+    __shared__ __align__(16) Shared<WARPS, STAGES> s;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    const int64_t t = blockIdx.x / C;
-    const int rank = static_cast<int>(blockIdx.x % C), k = a.topk, V = a.V;
-    const T* x = static_cast<const T*>(a.x) + t * a.pitch;
-    // 16-byte windows, counted from the one that holds the row's first logit:
-    // `pre` elements of it lie before the row. Whole ones: [whole0, whole1).
-    const int pre = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-    const int64_t whole0 = pre ? 1 : 0, whole1 = (static_cast<int64_t>(pre) + V) / N;
-    const int64_t whole = whole1 > whole0 ? whole1 - whole0 : 0, share = (whole + C - 1) / C;
-    const int64_t w0 = whole0 + min(share * rank, whole), w1 = whole0 + min(share * (rank + 1), whole);
-    const int tiles = static_cast<int>((w1 - w0 + kTileWindows - 1) / kTileWindows);
-
-    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int rank = CLUSTER ? static_cast<int>(blockIdx.x % C) : 0, k = a.topk, V = a.V;
+    const int64_t t = CLUSTER ? blockIdx.x / C : blockIdx.x;
+    uint64_t* list = s.list[warp % WARPS];
+    volatile uint32_t* bound = s.bound;
+    const Part<T> p(a, t, rank, C);
     auto copy = [&](int i) {  // tile i into its stage
-        const int64_t w = w0 + static_cast<int64_t>(i) * kTileWindows;
-        const uint32_t bytes = static_cast<uint32_t>(min(w1 - w, static_cast<int64_t>(kTileWindows))) * 16;
+        const int w = p.w0 + i * kTileWindows;
+        const uint32_t bytes = static_cast<uint32_t>(min(p.w1 - w, kTileWindows)) * 16;
         mbar_arrive_expect_tx(&s.full[i % kStages], bytes);
-        bulk_g2s(ring + (i % kStages) * kTileBytes, x + (w * N - pre), bytes, &s.full[i % kStages]);
+        bulk_g2s(ring + (i % kStages) * kTileBytes, p.x + (static_cast<int64_t>(w) * N - p.pre), bytes,
+                 &s.full[i % kStages]);
     };
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kThreads) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], kWarps);
+            mbar_init(&s.empty[i], WARPS);
         }
         fence_barrier_init();
-        for (int i = 0; i < min(kStages, tiles); ++i) copy(i);
-        s.count = 0;
-        s.tau = 0;
-        s.all_tau = 0;
+#pragma unroll 1
+        for (int i = 0; i < min(kStages, p.tiles); ++i) copy(i);
     }
+    bool ok = true;
     Sums sum{-INFINITY, 0.f, 0.f};
-    uint64_t* list = s.list[warp];
     uint32_t kth = 0;        // of the own list, as ordered bits; 0: not cut yet, or NaN
     float seen = -INFINITY;  // largest so far, of the tiles that mattered
-    bool ok = true;
-    int have = 0;  // entries of the own list
-    if (lane % 16 == 0) s.bound[2 * warp + lane / 16] = 0;
-
+    int have = 0;            // entries of the own list
+    if (threadIdx.x < kWarp) s.bound[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        s.count = 0;
+        s.tau = 0;
+    }
     // the row's ends, by the first CTA's first warp, a logit per lane
     if (rank == 0 && warp == 0) {
-        const int head = whole ? static_cast<int>(whole0 * N - pre) : 0;
-        const int64_t tail0 = whole ? whole1 * N - pre : 0;
+        const bool whole = p.whole1 > p.whole0;
+        const int head = whole ? p.whole0 * N - p.pre : 0;
+        const int64_t tail0 = whole ? static_cast<int64_t>(p.whole1) * N - p.pre : 0;
         const int64_t i = lane < head ? lane : tail0 + (lane - head);
         have = head + static_cast<int>(V - tail0);
         if (i < V) {
             float v;
             if constexpr (sizeof(T) == 4)
-                v = x[i];
+                v = p.x[i];
             else
-                v = __bfloat162float(x[i]);
+                v = __bfloat162float(p.x[i]);
             raise(sum, v);
             sum.z = v == -INFINITY ? 0.f : v - v + 1.f;  // NaN for NaN (and for +inf)
             seen = v;
@@ -347,51 +414,75 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
         }
     }
     __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-        const int64_t w = w0 + static_cast<int64_t>(i) * kTileWindows + threadIdx.x;
-        if (warp == 0 && i > 0 && i - 1 + kStages < tiles) {  // tile i - 1 has been read by all: its stage again
-            ok = ok && mbar_wait_warp(&s.empty[(i - 1) % kStages], static_cast<uint32_t>(((i - 1) / kStages) & 1),
-                                      &g_logprobs_error);
-            if (ok && lane == 0) copy(i - 1 + kStages);
-        }
-        ok = ok && mbar_wait_warp(&s.full[i % kStages], static_cast<uint32_t>((i / kStages) & 1), &g_logprobs_error);
-        K c;
-        const uint32_t at = smem_u32(ring) + (i % kStages) * kTileBytes + threadIdx.x * 16;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            if (w + j * kThreads < w1)
-                c.load(j, at + j * kThreads * 16);
-            else
-                c.clear(j);
-        }
-        const float top = c.top();
-        if (!(top <= sum.m)) raise(sum, top);
-        c.add(sum.m, sum.z, sum.u);
-
-        bool hit = k > 0;
-        uint32_t tau = 0;
-        volatile uint32_t* bound = s.bound;
-        // the half-warps' maxima so far, and the CTA's k-th of them
-        auto publish = [&] {
-            seen = fmaxf(seen, top);
-            const uint32_t bits = seen == -INFINITY ? 0u : order_bits(seen);  // -inf may be padding, or NaN passed over
-            const uint32_t best = lane < 16 ? __reduce_max_sync(0x0000FFFFu, bits) : __reduce_max_sync(0xFFFF0000u, bits);
-            if (lane % 16 == 0) bound[2 * warp + lane / 16] = best;
+    if (warp == WARPS) {
+        // the rest of the copies; and tau, after the first pass and whenever there is a copy to issue
+        auto update = [&] {
+            const uint32_t tau = kth_of_32(bound, k);
+            if (lane == 0) *static_cast<volatile uint32_t*>(&s.tau) = tau;  // the maxima only grow, and so does it
         };
-        if (k > 0) {
-            if (i == 0) {
+        if (k > 0 && p.tiles > 0) {
+            __syncthreads();
+            update();
+            __syncthreads();
+        }
+#pragma unroll 1
+        for (int i = kStages; i < p.tiles; ++i) {
+            if (k > 0) update();
+            ok = ok && mbar_wait_warp(&s.empty[i % kStages], (i / kStages - 1) & 1, &g_logprobs_error);
+            if (ok && lane == 0) copy(i);
+        }
+    }
+    for (int i = 0; i < p.tiles && warp < WARPS; ++i) {
+        const int st = i % kStages;
+        ok = ok && mbar_wait_warp(&s.full[st], (i / kStages) & 1, &g_logprobs_error);
+        const int wt = p.w0 + i * kTileWindows, left = min(p.w1 - wt, kTileWindows);  // the tile's first window, windows
+#pragma unroll
+        for (int pass = 0; pass < kPasses; ++pass) {
+            const int w = pass * (kThreads * kPer) + threadIdx.x;  // of the tile
+            K c;
+            const uint32_t at = smem_u32(ring) + st * kTileBytes + w * 16;
+            if (left == kTileWindows) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) c.load(j, at + j * kThreads * 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    if (w + j * kThreads < left)
+                        c.load(j, at + j * kThreads * 16);
+                    else
+                        c.clear(j);
+                }
+            }
+            const float top = c.top();
+            if (!(top <= sum.m)) raise(sum, top);
+            if (left != kTileWindows && top > -1e29f)
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (w + j * kThreads >= left) c.pad(j);
+            if (!c.add(sum.m, sum.z, sum.u)) {
+                const int mine = min(kPer, (left - w + kThreads - 1) / kThreads);
+                const float2 o = add_slowly<T>(ring + st * kTileBytes + w * 16, kThreads * 16, mine, sum.m);
+                sum.z += o.x;
+                sum.u += o.y;
+            }
+            if (k == 0) continue;
+
+            // the lane groups' maxima so far
+            auto publish = [&] {
+                seen = fmaxf(seen, top);
+                uint32_t best = seen == -INFINITY ? 0u : order_bits(seen);  // -inf may be padding, or NaN passed over
+#pragma unroll
+                for (int d = kGroup / 2; d; d >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, d));
+                if (lane % kGroup == 0) bound[threadIdx.x / kGroup] = best;
+            };
+            if (i == 0 && pass == 0) {  // the CTA's k-th of them, for the first time
                 publish();
                 __syncthreads();
-                if (warp == 0) {
-                    tau = kth_of_lanes(bound[lane], k);
-                    if (lane == 0) s.tau = tau;
-                }
                 __syncthreads();
             }
-            tau = *static_cast<volatile uint32_t*>(&s.tau);
-            hit = __any_sync(0xFFFFFFFFu, !(top < bits_value(tau)));
-        }
-        if (hit) {
+            const uint32_t tau = *static_cast<volatile uint32_t*>(&s.tau);
+            if (!__any_sync(0xFFFFFFFFu, !(top < bits_value(tau)))) continue;
+
             // at or above tau, above the own k-th
             const float low = kth >= tau && kth ? bits_value(kth + 1) : bits_value(tau);
             uint32_t mask = 0;
@@ -403,19 +494,19 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
                 if (tau == 0 && kth == 0)  // fewer than k numbers so far: NaN too
 #pragma unroll
                     for (int e = 0; e < N; ++e) m |= (c.get(j, e) != c.get(j, e) ? 1u : 0u) << e;
-                if (w + j * kThreads < w1) mask |= m << (j * N);
+                if (w + j * kThreads < left) mask |= m << (j * N);
             }
             bool cut = false;
             while (const uint32_t b = __ballot_sync(0xFFFFFFFFu, mask != 0)) {
                 if (mask) {
                     const int q = __ffs(mask) - 1, j = q / N, e = q % N;
                     mask &= mask - 1;
-                    const uint8_t* src = ring + (i % kStages) * kTileBytes + (j * kThreads + threadIdx.x) * 16;
+                    const uint8_t* src = ring + st * kTileBytes + (w + j * kThreads) * 16;
                     const float v = sizeof(T) == 4 ? reinterpret_cast<const float*>(src)[e]
                                                    : __uint_as_float(static_cast<uint32_t>(
                                                          reinterpret_cast<const uint16_t*>(src)[e]) << 16);
                     list[have + __popc(b & ((1u << lane) - 1))] =
-                        order_key(v, static_cast<uint32_t>((w + j * kThreads) * N - pre) + e);
+                        order_key(v, static_cast<uint32_t>(wt + w + j * kThreads) * N - p.pre + e);
                 }
                 have += __popc(b);
                 if (have > kList - kWarp) {
@@ -425,52 +516,44 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
                 }
             }
             if (cut && have >= k) kth = static_cast<uint32_t>(list[k - 1] >> 32);
-            if (i > 0) {
-                publish();
-                __syncwarp();
-                tau = kth_of_lanes(bound[lane], k);
-                if (lane == 0) atomicMax(&s.tau, tau);
-            }
+            if (i + pass > 0) publish();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.empty[i % kStages]);
-    }
-    int n = 0;
-    if (k > 0) {
-        // the CTA's lists into one (the ring is free), less what the last tau rules out
-        __syncthreads();
-        const uint32_t tau = s.tau;
-        uint64_t* cand = reinterpret_cast<uint64_t*>(ring);
-        for (int q = lane; q < have; q += kWarp) {
-            const uint64_t key = list[q];
-            if (static_cast<uint32_t>(key >> 32) >= tau) cand[atomicAdd(&s.count, 1)] = key;
-        }
-        __syncthreads();
-        n = s.count;
-        cut_all(cand, n, s.top, k);
-        n = min(n, k);
+        if (lane == 0) mbar_arrive(&s.empty[st]);
     }
     // the block's sums
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const Sums o{__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.z, d),
-                     __shfl_xor_sync(0xFFFFFFFFu, sum.u, d)};
-        sum = (lane & d) ? join(o, sum) : join(sum, o);
-    }
-    if (lane == 0) s.sums[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        sum = s.sums[lane % kWarps];
-#pragma unroll
-        for (int d = kWarps / 2; d; d >>= 1) {
-            const Sums o{__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.z, d),
-                         __shfl_xor_sync(0xFFFFFFFFu, sum.u, d)};
-            sum = (lane & d) ? join(o, sum) : join(sum, o);
+    sum = join_warp(sum);
+    if (lane == 0 && warp < WARPS) s.sums[warp] = sum;
+    int n = 0;
+    if (k > 0) {
+        // the CTA's lists into one, less what the last tau rules out
+        if (have > k) {
+            cut_list(list, have, k);
+            have = k;
         }
+        __syncthreads();
+        const uint32_t tau = kth_of_32(bound, k);
+        const uint64_t key = lane < have ? list[lane] : 0;
+        collect(s.cand, &s.count, key, key && static_cast<uint32_t>(key >> 32) >= tau);
+        __syncthreads();  // the lists are read
+        if (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        n = s.count;
+        cut_all<WARPS + 1>(s.cand, n, s.top, k);
+        n = min(n, k);
+    } else {
+        __syncthreads();
+        if (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    if (warp == 0) {
+        sum = Sums{-INFINITY, 0.f, 0.f};
+        if (lane < WARPS) sum = s.sums[lane];
+        __syncwarp();
+        sum = join_warp(sum);
     }
     // the cluster's: every CTA hands its sums and its best to the first
-    if (C > 1) {
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all of them have started
+    if (CLUSTER) {
+        // all of them have read their lists: the leader's may be written over
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (static_cast<int>(threadIdx.x) < n)
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cta(&s.all_top[rank][threadIdx.x], 0)),
                          "l"(s.top[threadIdx.x])
@@ -486,72 +569,76 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (rank != 0) return;
         if (k > 0) {
-            // no key below any CTA's k-th can be among the k best
-            const int r = threadIdx.x / kMaxK, l = threadIdx.x % kMaxK;
-            const uint64_t key = r < C && l < s.all_n[r] ? s.all_top[r][l] : 0;
-            if (l == k - 1 && key) atomicMax(reinterpret_cast<unsigned long long*>(&s.all_tau), key);
-            uint64_t* cand = reinterpret_cast<uint64_t*>(ring);
+            // the k-th largest of some 32 of the CTAs' first ones has k keys at or above it
+            const int each = kWarp / C, r0 = lane / each, l0 = lane % each;
+            const uint64_t some = r0 < C && l0 < s.all_n[r0] ? s.all_top[r0][l0] : 0;
+            int ahead = 0;
+#pragma unroll 8
+            for (int l = 0; l < kWarp; ++l) ahead += __shfl_sync(0xFFFFFFFFu, some, l) > some;
+            const uint32_t at = __ballot_sync(0xFFFFFFFFu, some != 0 && ahead == k - 1);
+            const uint64_t least = at ? __shfl_sync(0xFFFFFFFFu, some, __ffs(at) - 1) : 0;
+            for (int r = warp; r < C; r += WARPS + 1) {
+                const uint64_t key = lane < s.all_n[r] ? s.all_top[r][lane] : 0;
+                collect(s.cand, &s.count, key, key && key >= least);
+            }
             __syncthreads();
-            if (key && key >= s.all_tau) cand[atomicAdd(&s.count, 1)] = key;
-            __syncthreads();
-            cut_all(cand, s.count, s.top, k);
+            cut_all<WARPS + 1>(s.cand, s.count, s.top, k);
         }
         if (warp == 0) {
-            sum = lane < C ? s.all_sums[lane] : Sums{-INFINITY, 0.f, 0.f};
-#pragma unroll
-            for (int d = kMaxCluster / 2; d; d >>= 1) {
-                const Sums o{__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.z, d),
-                             __shfl_xor_sync(0xFFFFFFFFu, sum.u, d)};
-                sum = (lane & d) ? join(o, sum) : join(sum, o);
-            }
+            sum = Sums{-INFINITY, 0.f, 0.f};
+            if (lane < C) sum = s.all_sums[lane];
+            __syncwarp();
+            sum = join_warp(sum);
         }
     }
-    if (warp != 0) return;
-    sum.m = __shfl_sync(0xFFFFFFFFu, sum.m, 0);
-    sum.z = __shfl_sync(0xFFFFFFFFu, sum.z, 0);
-    sum.u = __shfl_sync(0xFFFFFFFFu, sum.u, 0);
-    if (sum.m == INFINITY) sum.z = sum.m - sum.m;  // +inf among the logits: NaN
-    const float lse = sum.z == 0.f ? INFINITY : sum.m + logf(sum.z);  // an empty row: every log probability is -inf
-    if (lane == 0) {
-        if (a.logprob) {
-            const int tok = a.tokens[t];
-            float v = -INFINITY;
-            if (tok >= 0 && tok < V) {
-                if constexpr (sizeof(T) == 4)
-                    v = x[tok] - lse;
-                else
-                    v = __bfloat162float(x[tok]) - lse;
+    if (warp == 0) {
+        if (sum.m == INFINITY) sum.z = sum.m - sum.m;  // +inf among the logits: NaN
+        // an empty row: every log probability is -inf
+        const float moved = fabsf(sum.m) < kHuge ? fmaf(sum.m, kLog2e, -__fmul_rn(sum.m, kLog2e)) : 0.f;
+        const float lse = sum.z == 0.f ? INFINITY : sum.m + (log2f(sum.z) - moved) * kLn2;
+        if (lane == 0) {
+            if (a.logprob) {
+                const int tok = a.tokens[t];
+                float v = -INFINITY;
+                if (tok >= 0 && tok < V) {
+                    if constexpr (sizeof(T) == 4)
+                        v = p.x[tok] - lse;
+                    else
+                        v = __bfloat162float(p.x[tok]) - lse;
+                }
+                a.logprob[t] = v;
             }
-            a.logprob[t] = v;
+            if (a.entropy) a.entropy[t] = sum.z == 0.f ? 0.f : (log2f(sum.z) - sum.u / sum.z) * kLn2;
         }
-        if (a.entropy) a.entropy[t] = sum.z == 0.f ? 0.f : logf(sum.z) - sum.u / sum.z;
-    }
-    if (lane < k) {
-        const uint64_t key = s.top[lane];
-        a.top_ids[t * k + lane] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
-        a.top_logprobs[t * k + lane] = ordered_value(static_cast<uint32_t>(key >> 32)) - lse;
+        if (lane < k) {
+            const uint64_t key = s.top[lane];
+            a.top_ids[t * k + lane] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+            a.top_logprobs[t * k + lane] = ordered_value(static_cast<uint32_t>(key >> 32)) - lse;
+        }
     }
 }
 
-template <typename T>
-cudaError_t launch(const LogprobArgs& a, cudaStream_t s)
+template <typename T, int WARPS, int STAGES, int CTAS, bool CLUSTER>
+cudaError_t launch_as(const LogprobArgs& a, int C, cudaStream_t s)
 {
-    constexpr size_t kSmem = kStages * kTileBytes;
+    constexpr size_t kSmem = STAGES * kTileBytes;
+    static_assert(CTAS * (kSmem + sizeof(Shared<WARPS, STAGES>) + 1024) <= 228 * 1024, "shared memory of an SM");
+    auto kern = logprobs_kernel<T, WARPS, STAGES, CTAS, CLUSTER>;
+    const unsigned grid = static_cast<unsigned>(a.T * C);
     static OccCache occ;
-    static const cudaError_t wide =
-        cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (wide != cudaSuccess) return wide;
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    blocks_per_sm(occ, reinterpret_cast<const void*>(&logprobs_kernel<T>), dev, kThreads, kSmem);  // opts in to kSmem
-    // CTAs per row: as many as fill the GPU once (two CTAs per SM), while
-    // each still has 16 logits a thread.
-    int C = 1;
-    while (C < kMaxCluster && a.T * C * 2 <= 2 * 152 && a.V / (C * 2) >= kThreads * 16) C *= 2;
+    blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, (WARPS + 1) * kWarp, kSmem);  // opts in to kSmem
+    if (!CLUSTER) {
+        kern<<<grid, (WARPS + 1) * kWarp, kSmem, s>>>(a, 1);
+        return cudaGetLastError();
+    }
+    static const cudaError_t wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (wide != cudaSuccess) return wide;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T * C));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((WARPS + 1) * kWarp);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute at{};
@@ -560,7 +647,20 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t s)
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a, C);
+    return cudaLaunchKernelEx(&cfg, kern, a, C);
+}
+
+template <typename T>
+cudaError_t launch(const LogprobArgs& a, cudaStream_t s)
+{
+    // CTAs per row: as many as the GPU holds at once (three per SM, less what
+    // clusters leave free where they do not fit a GPC: 456 CTAs in clusters of
+    // three took 35 us, 384 of them 24), while each has 32 logits a thread.
+    const int64_t room = 384 / a.T, most = a.V / (256 * 32);
+    int64_t C = room < most ? room : most;
+    C = C < 1 ? 1 : C > kMaxCluster ? kMaxCluster : C;
+    if (C > 1) return launch_as<T, 8, 2, 3, true>(a, static_cast<int>(C), s);
+    return launch_as<T, 8, 2, 3, false>(a, 1, s);
 }
 
 }  // namespace
