@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     int64_t u = sh.start;
     AttnMeta* meta = static_cast<AttnMeta*>(a.ws);
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes());
-    if (threadIdx.x == 0) meta[blockIdx.x].r = -1;
+    if (threadIdx.x == 0) meta[blockIdx.x].rows = 0;
     const int page_shift = a.page_shift;
 
     while (u < sh.end) {
@@ -210,7 +210,39 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
         const uint16_t* q1 = a.q + t1 * a.q_pitch + static_cast<int64_t>(h * G + row1 % G) * D;
         float c0 = a.scale * kAttnLog2e, c1 = c0;  // score to log2 units, per row
 
-        // ---- q fragments
+        // ---- the token group's stream
+        const int64_t first = l0 + tg * kBlock;
+        const int nblk = first < l1 ? static_cast<int>((l1 - first + S::kGroups * kBlock - 1) / (S::kGroups * kBlock)) : 0;
+        auto entry = [&](int64_t l) -> int32_t { return l < l1 ? table[l >> page_shift] : -1; };
+        int32_t ent = entry(first + (lane & 15));  // table entry of the next block to fetch, a token per lane
+        auto fetch = [&](int i) {  // block i into its stage
+            if (i < nblk) {
+                const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock) + (lane & 15);
+                const bool ok = ent >= 0 && ent < a.cache.num_pages;
+                const int64_t off = ok ? (ent * a.cache.page_stride + (l & (a.cache.page_size - 1)) * a.cache.token_stride +
+                                          h * a.cache.head_stride) * (F8 ? 1 : 2)
+                                       : 0;
+                const uint32_t vis = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+                ent = entry(l + S::kGroups * kBlock);
+                if (rg == 0 && lane == 0) s_vis[tg][i % S::kStages] = vis;
+                const uint32_t st = ring + (i % S::kStages) * S::kStage;
+                constexpr int CPR = S::kRowBytes / 16;  // chunks per row
+#pragma unroll
+                for (int it = 0; it < kBlock * CPR / (kWarp * RG); ++it) {
+                    const int ch = (it * RG + rg) * kWarp + lane, row = ch / CPR, cc = ch % CPR;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row) + cc * 16;
+                    const bool real = (vis >> row) & 1;
+                    const uint32_t at = st + chunk_at<S::kRowBytes, F8>(row, cc);
+                    cp_async16(at, static_cast<const uint8_t*>(a.cache.k) + o, real);
+                    cp_async16(at + S::kStage / 2, static_cast<const uint8_t*>(a.cache.v) + o, real);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
+
+        // ---- q fragments, while the first blocks are on their way
         const uint32_t qsm = smem_u32(smem) + S::kMain + (rg * KS * 32 + lane) * 16;
         {
             uint32_t f[KS][4];
@@ -267,38 +299,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             }
         }
         __syncthreads();
-
-        // ---- the token group's stream
-        const int64_t first = l0 + tg * kBlock;
-        const int nblk = first < l1 ? static_cast<int>((l1 - first + S::kGroups * kBlock - 1) / (S::kGroups * kBlock)) : 0;
-        auto entry = [&](int64_t l) -> int32_t { return l < l1 ? table[l >> page_shift] : -1; };
-        int32_t ent = entry(first + (lane & 15));  // table entry of the next block to fetch, a token per lane
-        auto fetch = [&](int i) {  // block i into its stage
-            if (i < nblk) {
-                const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock) + (lane & 15);
-                const bool ok = ent >= 0 && ent < a.cache.num_pages;
-                const int64_t off = ok ? (ent * a.cache.page_stride + (l & (a.cache.page_size - 1)) * a.cache.token_stride +
-                                          h * a.cache.head_stride) * (F8 ? 1 : 2)
-                                       : 0;
-                const uint32_t vis = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
-                ent = entry(l + S::kGroups * kBlock);
-                if (rg == 0 && lane == 0) s_vis[tg][i % S::kStages] = vis;
-                const uint32_t st = ring + (i % S::kStages) * S::kStage;
-                constexpr int CPR = S::kRowBytes / 16;  // chunks per row
-#pragma unroll
-                for (int it = 0; it < kBlock * CPR / (kWarp * RG); ++it) {
-                    const int ch = (it * RG + rg) * kWarp + lane, row = ch / CPR, cc = ch % CPR;
-                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row) + cc * 16;
-                    const bool real = (vis >> row) & 1;
-                    const uint32_t at = st + chunk_at<S::kRowBytes, F8>(row, cc);
-                    cp_async16(at, static_cast<const uint8_t*>(a.cache.k) + o, real);
-                    cp_async16(at + S::kStage / 2, static_cast<const uint8_t*>(a.cache.v) + o, real);
-                }
-            }
-            cp_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
 
         float o[NT][4];
 #pragma unroll
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 }
             }
         }
-        if (b0 == 0 && !whole && threadIdx.x == 0) meta[blockIdx.x] = attn_meta(sh, h, tile, item_end);
+        if (b0 == 0 && !whole && threadIdx.x == 0) meta[blockIdx.x] = attn_meta(a, sh, q, h, tile, S::kRows, item_end);
         __syncthreads();
         u = u_next;
         if (u < sh.end) {
@@ -600,7 +600,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s)
     tree_attn_kernel<D, RG, F8><<<S::kGrid, kThreads, S::kSmem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_attn_join(tree_attn_join_kernel<D, S::kRows, F8>, dim3(S::kGrid, S::kRows / 4), D, a, s);
+    return launch_attn_join(tree_attn_join_kernel<D, S::kRows, F8>, a, S::kGrid, s);
 }
 
 template <int D>

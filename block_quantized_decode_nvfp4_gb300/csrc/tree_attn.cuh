@@ -18,8 +18,10 @@ constexpr int kAttnMaxGrid = 3 * 152;
 constexpr float kAttnLog2e = 1.4426950408889634f, kAttnLn2 = 0.6931471805599453f;
 constexpr float kAttnPShift = 12.f;  // E4M3: log2 of the scale p carries
 
-struct AttnMeta {  // of a CTA's unfinished last item: whose it is and the last CTA with a part of it
-    int32_t r, h, tile, last;  // r = -1: none
+// Of a CTA's unfinished last item: the last CTA with a part of it, its first
+// row's token and head (of all query heads), live rows (0: there is none such).
+struct alignas(16) AttnMeta {
+    int32_t last, rows, o0, row0, h0;  // row0: of the request, in rows of the group; h0: the group's first head
 };
 
 __host__ __device__ constexpr size_t attn_meta_bytes() { return (kAttnMaxGrid * sizeof(AttnMeta) + 255) / 256 * 256; }
@@ -99,7 +101,7 @@ __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows
     const int64_t first = before + incl - mine;
     if (s.start < s.end && s.start >= first && s.start < first + mine) {
         int64_t b = first, i = r0;
-        for (;; ++i) {
+        for (; i + 1 < r1; ++i) {
             const int64_t u = attn_units(a, i, rows, unit, over);
             if (s.start < b + u) break;
             b += u;
@@ -133,9 +135,12 @@ __device__ __forceinline__ void attn_place(const AttnShare& s, const AttnReq& q,
 
 // The meta entry of a CTA whose item (units up to `ends` of the line) goes on
 // in other CTAs: the last CTA whose share begins before the item's end.
-__device__ __forceinline__ AttnMeta attn_meta(const AttnShare& s, int h, int tile, int64_t ends)
+__device__ __forceinline__ AttnMeta attn_meta(const AttnArgs& a, const AttnShare& s, const AttnReq& q, int h, int tile,
+                                              int rows, int64_t ends)
 {
-    return {static_cast<int32_t>(s.r), h, tile, static_cast<int32_t>((ends * s.ctas + s.total - 1) / s.total - 1)};
+    const int64_t left = static_cast<int64_t>(q.n) * a.group - static_cast<int64_t>(tile) * rows;
+    return {static_cast<int32_t>((ends * s.ctas + s.total - 1) / s.total - 1),
+            static_cast<int32_t>(left < rows ? left : rows), q.o0, tile * rows, h * a.group};
 }
 
 // Whether query token i of the request (token t of the call) sees draft j
@@ -178,112 +183,218 @@ __device__ __forceinline__ float attn_weight(float mw, float m)
     return mw == -INFINITY ? (m == -INFINITY ? 1.f : 0.f) : attn_ex2(mw - m);
 }
 
-// Joins the parts of the item that CTA blockIdx.x of the first kernel began
-// and did not finish: its own second part, then the first parts of the CTAs
-// after it, in order. blockIdx.y: four rows each, D / 4 threads a row. Parts
-// are row by row.
-template <int D, int ROWS, bool F8>
-__global__ void __launch_bounds__(D) tree_attn_join_kernel(AttnArgs a)
+constexpr int kJoinThreads = 256;
+constexpr int kJoinGrid = 6 * 152;
+constexpr int kAttnDeep = 8;  // CTAs an item reaches on for: from here its parts are shared by more threads
+
+// The items that the first kernel's CTAs left unfinished, as a list in shared
+// memory (list: kAttnMaxGrid entries, counts: two per warp); returns their
+// number, and whether one is deep. Every block of a
+// join makes it for itself: one read of the metas, and no idle blocks.
+__device__ __forceinline__ int attn_unfinished(const AttnArgs& a, int grid, int16_t* list, int* counts, bool& deep)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const AttnMeta md = static_cast<const AttnMeta*>(a.ws)[blockIdx.x];
-    if (md.r < 0) return;
-    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
-    const int row = blockIdx.y * 4 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
-    const AttnReq q = attn_request(a, md.r, ROWS, 1, 0);
-    const int G = a.group;
-    const int64_t grow = static_cast<int64_t>(md.tile) * ROWS + row;
-    if (grow >= static_cast<int64_t>(q.n) * G) return;
-    constexpr size_t P = attn_part_floats(ROWS, D);
-    const int b = blockIdx.x;
-    auto part = [&](int k) { return parts + (k == b ? 2 * k + 1 : 2 * k) * P; };
-    float m = -INFINITY;
-    for (int k = b; k <= md.last; ++k) m = fmaxf(m, part(k)[ROWS * D + row]);
-    float z = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = b; k <= md.last; ++k) {
-        const float* p = part(k);
-        const float f = attn_weight(p[ROWS * D + row], m);
-        const float4 y = *reinterpret_cast<const float4*>(p + row * D + d);
-        z += p[ROWS * D + ROWS + row] * f;
-        v.x += y.x * f;
-        v.y += y.y * f;
-        v.z += y.z * f;
-        v.w += y.w * f;
+    const AttnMeta* meta = static_cast<const AttnMeta*>(a.ws);
+    constexpr int kPer = (kAttnMaxGrid + kJoinThreads - 1) / kJoinThreads;
+    const int lane = threadIdx.x % kWarp;
+    static_assert(kPer <= 2, "counts");
+    bool open[kPer], far = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = i * kJoinThreads + threadIdx.x;
+        const int2 x = b < grid ? *reinterpret_cast<const int2*>(&meta[b]) : make_int2(0, 0);  // last, rows
+        open[i] = x.y > 0;
+        far |= open[i] && x.x - b >= kAttnDeep;
     }
-    const int64_t at = (q.o0 + grow / G) * static_cast<int64_t>(a.Hq) + md.h * G + grow % G;
-    const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[md.h] : 1.f;
-    *reinterpret_cast<uint2*>(a.out + at * D + d) = attn_out4(v, z, vscale);
-    if (d == 0 && a.lse) a.lse[at] = attn_lse(m, z, F8 ? kAttnPShift : 0.f);
+    deep = __syncthreads_or(far);
+    // the same order in every block: by CTA, a warp's ballot at a time
+    constexpr int kWarps = kJoinThreads / kWarp;
+    uint32_t m[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        m[i] = __ballot_sync(0xFFFFFFFFu, open[i]);
+        if (lane == 0) counts[i * kWarps + threadIdx.x / kWarp] = __popc(m[i]);
+    }
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int x = 0; x < kPer * kWarps; ++x) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (open[i] && x == i * kWarps + static_cast<int>(threadIdx.x / kWarp))
+                list[total + __popc(m[i] & ((1u << lane) - 1))] = static_cast<int16_t>(i * kJoinThreads + threadIdx.x);
+        total += counts[x];
+    }
+    __syncthreads();
+    return total;
 }
 
-// The same for parts that lie column by column (o [D][rows]): blockIdx.y is
-// eight rows, a thread one of their D columns.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(D) tree_attn_join_columns_kernel(AttnArgs a)
+// (m, z, o) of N values with another such of maximum m2.
+template <int N>
+__device__ __forceinline__ void attn_join(float& m, float& z, float (&o)[N], float m2, float z2, const float (&o2)[N])
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const AttnMeta md = static_cast<const AttnMeta*>(a.ws)[blockIdx.x];
-    if (md.r < 0) return;
-    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
-    const int row0 = blockIdx.y * 8, d = threadIdx.x, b = blockIdx.x;
-    const AttnReq q = attn_request(a, md.r, ROWS, 1, 0);
-    const int64_t grow0 = static_cast<int64_t>(md.tile) * ROWS + row0;
-    const int live = static_cast<int>(min(static_cast<int64_t>(q.n) * a.group - grow0, int64_t(8)));
-    if (live <= 0) return;
+    const float mm = fmaxf(m, m2), f = attn_weight(m, mm), f2 = attn_weight(m2, mm);
+    z = z * f + z2 * f2;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = o[i] * f + o2[i] * f2;
+    m = mm;
+}
+
+// Joins the parts of every item that a CTA b of the first kernel began and did
+// not finish: b's own second part, then the first parts of the CTAs after it,
+// in order. Parts are row by row. D / 4 threads a row. Few parts: a row's
+// threads take them all, four loads in flight. Many (a long context's item is
+// shared by dozens of CTAs): they go round among GROUPS such sets of threads,
+// whose results join in order (8 for D = 128: 57 parts in two rounds of loads).
+template <int D, int ROWS, bool F8, int GROUPS>
+__device__ __forceinline__ void attn_join_rows(const AttnArgs& a, const AttnMeta& md, int b, int row,
+                                               float (*s_part)[6])
+{
+    constexpr int TPR = D / 4;
     constexpr size_t P = attn_part_floats(ROWS, D);
-    auto part = [&](int k) { return parts + (k == b ? 2 * k + 1 : 2 * k) * P; };
-    float m[8], z[8], v[8];
+    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
+    const int d = threadIdx.x % TPR * 4, group = threadIdx.x / TPR % GROUPS;
+    float m = -INFINITY, z = 0.f, o[4] = {};
+    if (row < md.rows) {
+        for (int k0 = b + group; k0 <= md.last; k0 += 4 * GROUPS) {
+            float pm[4], pz[4];
+            float4 po[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        m[i] = -INFINITY;
-        z[i] = v[i] = 0.f;
-    }
-    for (int k = b; k <= md.last; ++k) {
-        const float* p = part(k) + ROWS * D + row0;
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + i * GROUPS;
+                pm[i] = -INFINITY, pz[i] = 0.f, po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k <= md.last) {
+                    const float* p = parts + (k == b ? 2 * k + 1 : 2 * k) * P;
+                    pm[i] = p[ROWS * D + row];
+                    pz[i] = p[ROWS * D + ROWS + row];
+                    po[i] = *reinterpret_cast<const float4*>(p + row * D + d);
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) m[i] = fmaxf(m[i], p[i]);
+            for (int i = 0; i < 4; ++i) {
+                const float v[4] = {po[i].x, po[i].y, po[i].z, po[i].w};
+                attn_join(m, z, o, pm[i], pz[i], v);
+            }
+        }
     }
+    if (GROUPS > 1) {
+        float* mine = s_part[threadIdx.x];
+        mine[0] = m, mine[1] = z, mine[2] = o[0], mine[3] = o[1], mine[4] = o[2], mine[5] = o[3];
+        __syncthreads();
+        if (group == 0)
+#pragma unroll
+            for (int x = 1; x < GROUPS; ++x) {
+                const float* p = s_part[threadIdx.x + x * TPR];
+                const float v[4] = {p[2], p[3], p[4], p[5]};
+                attn_join(m, z, o, p[0], p[1], v);
+            }
+        __syncthreads();
+    }
+    if (group == 0 && row < md.rows) {
+        const int g = md.row0 + row, tok = g / a.group;
+        const int64_t at = (md.o0 + static_cast<int64_t>(tok)) * a.Hq + md.h0 + g - tok * a.group;
+        const float vscale = (F8 && a.cache.v_scale) ? a.cache.v_scale[md.h0 / a.group] : 1.f;
+        *reinterpret_cast<uint2*>(a.out + at * D + d) = attn_out4(make_float4(o[0], o[1], o[2], o[3]), z, vscale);
+        if (d == 0 && a.lse) a.lse[at] = attn_lse(m, z, F8 ? kAttnPShift : 0.f);
+    }
+}
+
+template <int D, int ROWS, bool F8>
+__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(AttnArgs a, int grid)
+{
+    constexpr int TPR = D / 4, kRowsAt = kJoinThreads / TPR;  // rows of a step
+    constexpr int kSteps = (ROWS + kRowsAt - 1) / kRowsAt, kGroups = kRowsAt;  // deep: a row a step
+    __shared__ int16_t list[kAttnMaxGrid];
+    __shared__ int s_counts[kJoinThreads / kWarp * 2];
+    __shared__ float s_part[kJoinThreads][6];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool deep;
+    const int count = attn_unfinished(a, grid, list, s_counts, deep);
+    const AttnMeta* meta = static_cast<const AttnMeta*>(a.ws);
+    for (int w = blockIdx.x; w < count * kSteps; w += gridDim.x) {
+        const int b = list[w / kSteps];
+        const AttnMeta md = meta[b];
+        if (md.last - b < kAttnDeep)
+            attn_join_rows<D, ROWS, F8, 1>(a, md, b, w % kSteps * kRowsAt + threadIdx.x / TPR, s_part);
+    }
+    if (deep)
+        for (int w = blockIdx.x; w < count * ROWS; w += gridDim.x) {
+            const int b = list[w / ROWS];
+            const AttnMeta md = meta[b];
+            if (md.last - b >= kAttnDeep && w % ROWS < md.rows)
+                attn_join_rows<D, ROWS, F8, kGroups>(a, md, b, w % ROWS, s_part);
+        }
+}
+
+// The same for parts that lie column by column (o [D][rows]): a thread has one
+// column of eight rows.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_columns_kernel(AttnArgs a, int grid)
+{
+    constexpr int kRowsAt = kJoinThreads / D * 8, kSteps = ROWS / kRowsAt;  // rows of a step
+    __shared__ int16_t list[kAttnMaxGrid];
+    __shared__ int s_counts[kJoinThreads / kWarp * 2];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool deep;
+    const int count = attn_unfinished(a, grid, list, s_counts, deep);
+    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attn_meta_bytes());
+    constexpr size_t P = attn_part_floats(ROWS, D);
+    const int d = threadIdx.x % D;
+    for (int w = blockIdx.x; w < count * kSteps; w += gridDim.x) {
+        const int b = list[w / kSteps], row = w % kSteps * kRowsAt + threadIdx.x / D * 8;
+        const AttnMeta md = static_cast<const AttnMeta*>(a.ws)[b];
+        if (row >= md.rows) continue;
+        float m[8], z[8], o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = -INFINITY;
+            z[i] = o[i] = 0.f;
+        }
 #pragma unroll 2
-    for (int k = b; k <= md.last; ++k) {
-        const float* p = part(k);
-        const float4 lo = *reinterpret_cast<const float4*>(p + d * ROWS + row0);
-        const float4 hi = *reinterpret_cast<const float4*>(p + d * ROWS + row0 + 4);
-        const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        for (int k = b; k <= md.last; ++k) {
+            const float* p = parts + (k == b ? 2 * k + 1 : 2 * k) * P;
+            // rows past the live ones of the tile are written by nobody: their values are not used
+            const float4 o0 = *reinterpret_cast<const float4*>(p + d * ROWS + row);
+            const float4 o1 = *reinterpret_cast<const float4*>(p + d * ROWS + row + 4);
+            const float4 m0 = *reinterpret_cast<const float4*>(p + ROWS * D + row);
+            const float4 m1 = *reinterpret_cast<const float4*>(p + ROWS * D + row + 4);
+            const float4 z0 = *reinterpret_cast<const float4*>(p + ROWS * D + ROWS + row);
+            const float4 z1 = *reinterpret_cast<const float4*>(p + ROWS * D + ROWS + row + 4);
+            const float po[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+            const float pm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+            const float pz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float x[1] = {o[i]};
+                const float y[1] = {po[i]};
+                attn_join(m[i], z[i], x, pm[i], pz[i], y);
+                o[i] = x[0];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < live) {
-                const float f = attn_weight(p[ROWS * D + row0 + i], m[i]);
-                z[i] += p[ROWS * D + ROWS + row0 + i] * f;
-                v[i] += y[i] * f;
+            if (row + i < md.rows) {
+                const int g = md.row0 + row + i, tok = g / a.group;
+                const int64_t at = (md.o0 + static_cast<int64_t>(tok)) * a.Hq + md.h0 + g - tok * a.group;
+                a.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(z[i] == 0.f ? 0.f : o[i] / z[i]));
+                if (d == 0 && a.lse) a.lse[at] = attn_lse(m[i], z[i], 0.f);
             }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < live) {
-            const uint32_t g = static_cast<uint32_t>(grow0 + i), tok = g / a.group;
-            const int64_t at = (q.o0 + static_cast<int64_t>(tok)) * a.Hq + md.h * a.group + (g - tok * a.group);
-            a.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(z[i] == 0.f ? 0.f : v[i] / z[i]));
-            if (d == 0 && a.lse) a.lse[at] = attn_lse(m[i], z[i], 0.f);
-        }
 }
 
 // Launches a join after the first kernel in the same stream; it may be set up
 // while that one still runs, and waits for its end.
-inline cudaError_t launch_attn_join(void (*kernel)(AttnArgs), dim3 grid, int threads, const AttnArgs& a, cudaStream_t s)
+inline cudaError_t launch_attn_join(void (*kernel)(AttnArgs, int), const AttnArgs& a, int grid, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3(kJoinGrid);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, grid);
 }
 
 // The kernel for many rows a kv head (tree_attn_wide.cu), bf16 caches.

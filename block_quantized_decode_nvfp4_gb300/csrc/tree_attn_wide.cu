@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.turn[i], 1);
         }
         fence_barrier_init();
-        static_cast<AttnMeta*>(a.ws)[blockIdx.x].r = -1;
+        static_cast<AttnMeta*>(a.ws)[blockIdx.x].rows = 0;
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             g.table = sh.r * a.width;
             const bool whole = b0 == 0 && cnt == q.nb - kOver;
             g.parts = whole ? -1 : (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * static_cast<int64_t>(attn_part_floats(S::kRows, D));
-            if (b0 == 0 && !whole && !g.skip) static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(sh, g.h, g.tile, item_end);
+            if (b0 == 0 && !whole && !g.skip) static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(a, sh, q, g.h, g.tile, S::kRows, item_end);
             g.last = u >= sh.end;
             if (u < sh.end) {
                 int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
@@ -774,7 +774,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
     tree_attn_wide_kernel<D, TWO><<<kGrid, kThreads, S::kSmem, s>>>(a, mk, mv);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_attn_join(tree_attn_join_columns_kernel<D, S::kRows>, dim3(kGrid, S::kRows / 8), D, a, s);
+    return launch_attn_join(tree_attn_join_columns_kernel<D, S::kRows>, a, kGrid, s);
 }
 
 }  // namespace
