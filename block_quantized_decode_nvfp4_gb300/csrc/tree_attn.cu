@@ -22,7 +22,7 @@
 // timing). A CTA finds its place by one scan of the requests' unit counts.
 //
 // A CTA's four warps are 4 / RG token groups of RG warps, a warp per 16 rows.
-// A token group streams blocks of 16 tokens through a shared-memory ring of
+// A token group streams blocks of 16 (or 32) tokens through a shared-memory ring of
 // its own (cp.async, 16 bytes a lane, waited for by the group alone: no
 // barrier of the whole CTA in the loop) and holds its own (m, z, o) in
 // registers; the groups join at the end of an item. Products run on
@@ -55,9 +55,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / kWarp;
-constexpr int kBlock = 16;         // tokens a token group takes at a time
 constexpr int kUnit = 64;          // tokens per unit of the split
-constexpr int kOver = 1;           // units that an item's beginning and end cost
+constexpr int kOver = 2;           // units that an item's beginning and end cost
 constexpr int kRows16 = 16;
 
 template <int D, int RG, bool F8>
@@ -65,6 +64,9 @@ struct Shape {
     static constexpr int kRows = kRows16 * RG;
     static constexpr int kGroups = kWarps / RG;            // token groups
     static constexpr int kRowBytes = D * (F8 ? 1 : 2);
+    // Tokens a token group takes at a time: E4M3 blocks of 16 are 4 KiB, and what
+    // a block costs beside its products would weigh more than they do.
+    static constexpr int kNB = F8 && D <= 128 ? 2 : 1, kBlock = 16 * kNB;
     static constexpr int kStage = 2 * kBlock * kRowBytes;  // K and V of one block
     static constexpr int kCtas = D <= 128 ? 3 : 2;         // per SM: 64 of o and 40 more registers, or 128 of o
     static constexpr int kGrid = kCtas * 152;
@@ -164,10 +166,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
     using S = Shape<D, RG, F8>;
     constexpr int NT = D / 8;     // n tiles of the output; d of column n of tile j:
     constexpr int KS = D / 16;    // k steps of the scores
+    constexpr int kBlock = S::kBlock, NB = S::kNB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_find[kWarps + 2];
     __shared__ uint32_t s_vis[kWarps][8];
     __shared__ float s_m[kWarps][kRows16], s_z[kWarps][kRows16];
+    constexpr uint32_t kAll = kBlock == 32 ? 0xFFFFFFFFu : 0xFFFFu;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int rg = warp % RG, tg = warp / RG;  // row group, token group
     const int g = lane >> 2, c = lane & 3;     // row (and column) and k positions in mma fragments
@@ -214,15 +218,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
         const int64_t first = l0 + tg * kBlock;
         const int nblk = first < l1 ? static_cast<int>((l1 - first + S::kGroups * kBlock - 1) / (S::kGroups * kBlock)) : 0;
         auto entry = [&](int64_t l) -> int32_t { return l < l1 ? table[l >> page_shift] : -1; };
-        int32_t ent = entry(first + (lane & 15));  // table entry of the next block to fetch, a token per lane
+        int32_t ent = entry(first + (lane & (kBlock - 1)));  // table entry of the next block to fetch, a token per lane
         auto fetch = [&](int i) {  // block i into its stage
             if (i < nblk) {
-                const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock) + (lane & 15);
+                const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock) + (lane & (kBlock - 1));
                 const bool ok = ent >= 0 && ent < a.cache.num_pages;
                 const int64_t off = ok ? (ent * a.cache.page_stride + (l & (a.cache.page_size - 1)) * a.cache.token_stride +
                                           h * a.cache.head_stride) * (F8 ? 1 : 2)
                                        : 0;
-                const uint32_t vis = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+                const uint32_t vis = __ballot_sync(0xFFFFFFFFu, ok) & kAll;
                 ent = entry(l + S::kGroups * kBlock);
                 if (rg == 0 && lane == 0) s_vis[tg][i % S::kStages] = vis;
                 const uint32_t st = ring + (i % S::kStages) * S::kStage;
@@ -315,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             const uint32_t ks = ring + (i % S::kStages) * S::kStage, vs = ks + S::kStage / 2;
             const uint32_t vis = s_vis[tg][i % S::kStages];
             const int64_t l = first + static_cast<int64_t>(i) * (S::kGroups * kBlock);
-            float s[2][4];
+            float s[2 * NB][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+            for (int nt = 0; nt < 2 * NB; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
             // scores
             if (!F8) {
                 const int mrow = (lane & 7) + ((lane >> 4) << 3), mch = (lane >> 3) & 1;
@@ -333,21 +337,25 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             } else {
 #pragma unroll
                 for (int k4 = 0; k4 < KS / 4; ++k4) {
-                    const uint4 x = lds128(ks + chunk_at<S::kRowBytes, F8>(g, 4 * k4 + c));
-                    const uint4 y = lds128(ks + chunk_at<S::kRowBytes, F8>(g + 8, 4 * k4 + c));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    uint32_t x[2 * NB][4];  // 16 d of token 8 nt + g
+#pragma unroll
+                    for (int nt = 0; nt < 2 * NB; ++nt) {
+                        const uint4 v = lds128(ks + chunk_at<S::kRowBytes, F8>(8 * nt + g, 4 * k4 + c));
+                        x[nt][0] = v.x, x[nt][1] = v.y, x[nt][2] = v.z, x[nt][3] = v.w;
+                    }
 #pragma unroll
                     for (int e4 = 0; e4 < 4; ++e4) {
                         const int k = 4 * k4 + e4;
                         const uint4 w = lds128(qsm + k * 512);
                         const uint32_t qa[4] = {w.x, w.y, w.z, w.w};
-                        mma16816<F8>(s[0], qa, e4m3x2_to_f16x2(xs[e4] & 0xFFFFu), e4m3x2_to_f16x2(xs[e4] >> 16));
-                        mma16816<F8>(s[1], qa, e4m3x2_to_f16x2(ys[e4] & 0xFFFFu), e4m3x2_to_f16x2(ys[e4] >> 16));
+#pragma unroll
+                        for (int nt = 0; nt < 2 * NB; ++nt)
+                            mma16816<F8>(s[nt], qa, e4m3x2_to_f16x2(x[nt][e4] & 0xFFFFu), e4m3x2_to_f16x2(x[nt][e4] >> 16));
                     }
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < 2 * NB; ++nt) {
                 s[nt][0] *= c0;
                 s[nt][1] *= c0;
                 s[nt][2] *= c1;
@@ -355,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             }
             // what is hidden
             const bool drafts = l + kBlock > q.ctx;
-            if (vis != 0xFFFFu || drafts) {
+            if (vis != kAll || drafts) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 2 * NB; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int tok = 8 * nt + 2 * c + e;
@@ -368,8 +376,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                     }
             }
             // running maximum
-            float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            float n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+            float n0 = -INFINITY, n1 = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < 2 * NB; ++nt) {
+                n0 = fmaxf(n0, fmaxf(s[nt][0], s[nt][1]));
+                n1 = fmaxf(n1, fmaxf(s[nt][2], s[nt][3]));
+            }
 #pragma unroll
             for (int x = 1; x < 4; x <<= 1) {
                 n0 = fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, x));
@@ -393,15 +405,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             }
             const float sub0 = (m0 == -INFINITY ? 0.f : m0) - (F8 ? kAttnPShift : 0.f);
             const float sub1 = (m1 == -INFINITY ? 0.f : m1) - (F8 ? kAttnPShift : 0.f);
-            uint32_t pa[4];
+            uint32_t pa[NB][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < 2 * NB; ++nt) {
                 const float p0 = attn_ex2(s[nt][0] - sub0), p1 = attn_ex2(s[nt][1] - sub0);
                 const float p2 = attn_ex2(s[nt][2] - sub1), p3 = attn_ex2(s[nt][3] - sub1);
                 z0 += p0 + p1;
                 z1 += p2 + p3;
-                pa[2 * nt] = pack2<F8>(p0, p1);
-                pa[2 * nt + 1] = pack2<F8>(p2, p3);
+                pa[nt / 2][2 * (nt % 2)] = pack2<F8>(p0, p1);
+                pa[nt / 2][2 * (nt % 2) + 1] = pack2<F8>(p2, p3);
             }
             // A draft's value may be infinite or NaN and hidden from some of
             // the rows, where 0 * v must count nothing: such elements leave
@@ -475,19 +487,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 for (int k = 0; k < KS; ++k) {
                     uint32_t b[4];
                     ldsm4t(vs + chunk_at<S::kRowBytes, F8>(mrow, 2 * k + mch), b);
-                    mma16816<F8>(o[2 * k], pa, b[0], b[1]);
-                    mma16816<F8>(o[2 * k + 1], pa, b[2], b[3]);
+                    mma16816<F8>(o[2 * k], pa[0], b[0], b[1]);
+                    mma16816<F8>(o[2 * k + 1], pa[0], b[2], b[3]);
                 }
             } else {
                 // tokens 2c, 2c + 1, 2c + 8, 2c + 9; the NT d from NT g
                 constexpr int W = NT / 4;       // words per token
                 constexpr int WL = W < 4 ? W : 4;  // words per load
 #pragma unroll
-                for (int w0 = 0; w0 < W; w0 += WL) {
+                for (int ww = 0; ww < W * NB; ww += WL) {
+                    const int w0 = ww % W, nb = ww / W;  // words, 16 tokens
                     uint32_t x[4][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int tok = 2 * c + (e & 1) + 8 * (e >> 1), byte = NT * g + 4 * w0;
+                        const int tok = 16 * nb + 2 * c + (e & 1) + 8 * (e >> 1), byte = NT * g + 4 * w0;
                         const uint32_t at = vs + chunk_at<S::kRowBytes, F8>(tok, byte / 16) + byte % 16;
                         if (WL == 4) {
                             const uint4 y = lds128(at);
@@ -502,10 +515,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                         const uint32_t lo0 = __byte_perm(x[0][w], x[1][w], 0x5140), hi0 = __byte_perm(x[0][w], x[1][w], 0x7362);
                         const uint32_t lo1 = __byte_perm(x[2][w], x[3][w], 0x5140), hi1 = __byte_perm(x[2][w], x[3][w], 0x7362);
                         const int j = 4 * (w0 + w);
-                        mma16816<F8>(o[j], pa, e4m3x2_to_f16x2(lo0 & 0xFFFFu), e4m3x2_to_f16x2(lo1 & 0xFFFFu));
-                        mma16816<F8>(o[j + 1], pa, e4m3x2_to_f16x2(lo0 >> 16), e4m3x2_to_f16x2(lo1 >> 16));
-                        mma16816<F8>(o[j + 2], pa, e4m3x2_to_f16x2(hi0 & 0xFFFFu), e4m3x2_to_f16x2(hi1 & 0xFFFFu));
-                        mma16816<F8>(o[j + 3], pa, e4m3x2_to_f16x2(hi0 >> 16), e4m3x2_to_f16x2(hi1 >> 16));
+                        mma16816<F8>(o[j], pa[nb], e4m3x2_to_f16x2(lo0 & 0xFFFFu), e4m3x2_to_f16x2(lo1 & 0xFFFFu));
+                        mma16816<F8>(o[j + 1], pa[nb], e4m3x2_to_f16x2(lo0 >> 16), e4m3x2_to_f16x2(lo1 >> 16));
+                        mma16816<F8>(o[j + 2], pa[nb], e4m3x2_to_f16x2(hi0 & 0xFFFFu), e4m3x2_to_f16x2(hi1 & 0xFFFFu));
+                        mma16816<F8>(o[j + 3], pa[nb], e4m3x2_to_f16x2(hi0 >> 16), e4m3x2_to_f16x2(hi1 >> 16));
                     }
                 }
             }
