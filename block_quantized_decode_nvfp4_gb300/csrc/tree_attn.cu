@@ -64,9 +64,10 @@ struct Shape {
     static constexpr int kRows = kRows16 * RG;
     static constexpr int kGroups = kWarps / RG;            // token groups
     static constexpr int kRowBytes = D * (F8 ? 1 : 2);
-    // Tokens a token group takes at a time: E4M3 blocks of 16 are 4 KiB, and what
-    // a block costs beside its products would weigh more than they do.
-    static constexpr int kNB = F8 && D <= 128 ? 2 : 1, kBlock = 16 * kNB;
+    // Tokens a token group takes at a time: 32 where two stages of them fit, so
+    // that what a block costs beside its products (maximum, addresses, waits)
+    // is shared by twice the tokens.
+    static constexpr int kNB = D <= 128 && kGroups * 128 * kRowBytes <= 64 * 1024 ? 2 : 1, kBlock = 16 * kNB;
     static constexpr int kStage = 2 * kBlock * kRowBytes;  // K and V of one block
     static constexpr int kCtas = D <= 128 ? 3 : 2;         // per SM: 64 of o and 40 more registers, or 128 of o
     static constexpr int kGrid = kCtas * 152;
@@ -327,12 +328,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 const int mrow = (lane & 7) + ((lane >> 4) << 3), mch = (lane >> 3) & 1;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4];
-                    ldsm4(ks + chunk_at<S::kRowBytes, F8>(mrow, 2 * k + mch), b);
                     const uint4 x = lds128(qsm + k * 512);
                     const uint32_t qa[4] = {x.x, x.y, x.z, x.w};
-                    mma16816<F8>(s[0], qa, b[0], b[1]);
-                    mma16816<F8>(s[1], qa, b[2], b[3]);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        uint32_t b[4];
+                        ldsm4(ks + chunk_at<S::kRowBytes, F8>(16 * nb + mrow, 2 * k + mch), b);
+                        mma16816<F8>(s[2 * nb], qa, b[0], b[1]);
+                        mma16816<F8>(s[2 * nb + 1], qa, b[2], b[3]);
+                    }
                 }
             } else {
 #pragma unroll
@@ -484,12 +488,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
             if (!F8) {
                 const int mrow = (lane & 7) + (((lane >> 3) & 1) << 3), mch = lane >> 4;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4];
-                    ldsm4t(vs + chunk_at<S::kRowBytes, F8>(mrow, 2 * k + mch), b);
-                    mma16816<F8>(o[2 * k], pa[0], b[0], b[1]);
-                    mma16816<F8>(o[2 * k + 1], pa[0], b[2], b[3]);
-                }
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        uint32_t b[4];
+                        ldsm4t(vs + chunk_at<S::kRowBytes, F8>(16 * nb + mrow, 2 * k + mch), b);
+                        mma16816<F8>(o[2 * k], pa[nb], b[0], b[1]);
+                        mma16816<F8>(o[2 * k + 1], pa[nb], b[2], b[3]);
+                    }
             } else {
                 // tokens 2c, 2c + 1, 2c + 8, 2c + 9; the NT d from NT g
                 constexpr int W = NT / 4;       // words per token
