@@ -62,13 +62,46 @@ struct AttnShare {
     int64_t r, base;
 };
 
-// Each thread sums a run of requests, one scan places them. sh: THREADS / 32
-// + 2 entries of shared memory; called by the whole CTA.
+__device__ __forceinline__ void attn_cut(AttnShare& s)  // the share from the total
+{
+    s.ctas = min(static_cast<int64_t>(gridDim.x), s.total);
+    if (blockIdx.x >= s.ctas) {
+        s.start = s.end = s.total;
+    } else if (s.total < (int64_t(1) << 22)) {  // 32-bit divisions (grids are below 2^10)
+        s.start = static_cast<uint32_t>(s.total) * blockIdx.x / static_cast<uint32_t>(s.ctas);
+        s.end = static_cast<uint32_t>(s.total) * (blockIdx.x + 1) / static_cast<uint32_t>(s.ctas);
+    } else {
+        s.start = s.total * blockIdx.x / s.ctas;
+        s.end = s.total * (blockIdx.x + 1) / s.ctas;
+    }
+}
+
+// Up to 32 requests: every warp for itself, a request per lane. More: each
+// thread sums a run of requests, one scan places them. sh: THREADS / 32 + 2
+// entries of shared memory; called by the whole CTA.
 template <int THREADS>
 __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows, int unit, int over, int64_t* sh)
 {
     constexpr int W = THREADS / kWarp;
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    AttnShare s{};
+    if (a.R <= kWarp) {
+        const int64_t mine = lane < a.R ? attn_units(a, lane, rows, unit, over) : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int d = 1; d < kWarp; d <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        s.total = __shfl_sync(0xFFFFFFFFu, incl, kWarp - 1);
+        attn_cut(s);
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, incl > s.start);
+        const int at = past ? __ffs(past) - 1 : 0;  // none: the CTA has no share
+        s.r = at;
+        s.base = __shfl_sync(0xFFFFFFFFu, incl - mine, at);
+        __syncthreads();  // as the other way does: what the CTA has set up is visible
+        return s;
+    }
     const int64_t per = (a.R + THREADS - 1) / THREADS;
     const int64_t r0 = min(threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
     int64_t mine = 0;
@@ -81,23 +114,13 @@ __device__ __forceinline__ AttnShare attn_find_share(const AttnArgs& a, int rows
     }
     if (lane == kWarp - 1) sh[warp] = incl;
     __syncthreads();
-    AttnShare s{};
     int64_t before = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         if (w < warp) before += sh[w];
         s.total += sh[w];
     }
-    s.ctas = min(static_cast<int64_t>(gridDim.x), s.total);
-    if (blockIdx.x >= s.ctas) {
-        s.start = s.end = s.total;
-    } else if (s.total < (int64_t(1) << 22)) {  // 32-bit divisions (grids are below 2^10)
-        s.start = static_cast<uint32_t>(s.total) * blockIdx.x / static_cast<uint32_t>(s.ctas);
-        s.end = static_cast<uint32_t>(s.total) * (blockIdx.x + 1) / static_cast<uint32_t>(s.ctas);
-    } else {
-        s.start = s.total * blockIdx.x / s.ctas;
-        s.end = s.total * (blockIdx.x + 1) / s.ctas;
-    }
+    attn_cut(s);
     const int64_t first = before + incl - mine;
     if (s.start < s.end && s.start >= first && s.start < first + mine) {
         int64_t b = first, i = r0;
