@@ -16,7 +16,7 @@
 //
 // Few rows: a row is shared by a cluster of C CTAs (16 for a decode step's one
 // row), which join through distributed shared memory; of many rows each has a
-// CTA. Either way the call is one launch and needs no workspace.
+// CTA. Either way the call is one launch, and nothing passes through memory.
 // A row's whole 16-byte windows come through a ring of 32 KiB bulk copies
 // (two stages, three CTAs per SM: 96 KiB and more in flight per SM); its
 // ragged ends, at most 14 logits, are read one by one. The warps run through
@@ -37,6 +37,11 @@
 // distinct logits; rows of equal ones cost a few cuts in their first tile. At
 // the end the lists are joined, first the CTA's, then the cluster's, by the
 // same count.
+//
+// Measured over 151936 logits: one fp32 row with 20 alternatives 9.8 us, 128 with
+// 8 25.4 us (18.5 without alternatives), 2047 bf16 rows with 5 130.6 us or 4.8
+// TB/s (103 us without). What bounds it: the instructions per logit (64 % of the
+// issue slots), a quarter of them the alternatives' bookkeeping.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -15,18 +15,20 @@
 //
 // Split. Lengths are known to the device only, and a batch is ragged, so the
 // work of all items is laid out in units of kUnit tokens, and each of the
-// grid's CTAs (three per SM; two for D = 256) takes an equal share of the line, at most two
-// items' ends among them being partial. A CTA writes the items that lie within its share; of an item
-// that crosses a boundary each CTA writes its part to the workspace, and a
-// second kernel joins them in ascending order (results do not depend on
-// timing). A CTA finds its place by one scan of the requests' unit counts.
+// grid's CTAs (three per SM; two for D = 256) takes an equal share of the line:
+// at most two of its items are partial, the first and the last. A CTA writes the
+// items that lie within its share; of an item that crosses a boundary each CTA
+// writes its part to the workspace, and a second kernel joins them in ascending
+// order (results do not depend on timing). A CTA finds its place by one scan of
+// the requests' unit counts, within a warp for up to 32 requests.
 //
 // A CTA's four warps are 4 / RG token groups of RG warps, a warp per 16 rows.
-// A token group streams blocks of 16 (or 32) tokens through a shared-memory ring of
-// its own (cp.async, 16 bytes a lane, waited for by the group alone: no
+// A token group streams blocks of 32 tokens (16 where two stages of 32 do not
+// fit) through a shared-memory ring of its own (cp.async, 16 bytes a lane, waited for by the group alone: no
 // barrier of the whole CTA in the loop) and holds its own (m, z, o) in
 // registers; the groups join at the end of an item. Products run on
-// mma.sync m16n8k16: scores from q (A, registers) and keys (B), then the
+// mma.sync m16n8k16: scores from q (A, as fragments in shared memory, a 16-byte read each: in
+// registers they left too few for three CTAs) and keys (B), then the
 // probabilities, rounded, are the A operand as they lie in the score
 // accumulators, and the values B.
 //  - bf16 cache: B operands by ldmatrix (transposed for the values); p is
@@ -37,6 +39,14 @@
 //    power of two per row that brings the row's largest element to 2^14
 //    (what that drops is below 2^-38 of it); p is scaled by 2^12 before its
 //    rounding to f16, so that p down to 2^-26 keeps 11 bits.
+//
+// Measured (8 kv heads, D = 128; 32 query heads over bf16, 64 over E4M3):
+//  - 16 requests of 8 drafts over 8192 tokens, bf16: 75.6 us for 395 MB, 5.2
+//    TB/s; the slope over longer contexts is 6.9 TB/s, the rest is start, the
+//    spread of the CTAs' ends (56 to 71 us) and the join;
+//  - 64 decodes over 8192 tokens, E4M3: 138 us, 5.8 TB/s, and in between the
+//    conversions' latency (16 tokens a step: 156 us);
+//  - one decode over 1024 tokens: 8.9 us, two launches and one chain of loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

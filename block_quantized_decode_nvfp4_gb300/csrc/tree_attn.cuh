@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(AttnArgs a
 // rows, a warp D / 8 columns of them, and a load is four whole lines of 32 rows
 // (eight lanes of four rows). The outputs turn into rows in shared memory.
 // A column a thread instead, 32 lines a load, took 75.3 -> 84.5 us of four
-// trees of 64 tokens over 8192 (32 query heads on 8).
+// trees of 64 tokens over 8192 (64 query heads on 8).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_columns_kernel(AttnArgs a, int grid)
 {

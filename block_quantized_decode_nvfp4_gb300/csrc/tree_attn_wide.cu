@@ -25,6 +25,12 @@
 // columns of s that they have read, and rescale o in tensor memory only when
 // a row's maximum has grown by more than 2^8 (p then stays below 2^8, and
 // nothing is lost: fp32 sums, bf16's range).
+//
+// Four trees of 64 tokens over 32768 (64 query heads on 8, D = 128): 203 us,
+// 1.06 PFLOP/s of products. A block of both slots takes about 3300 cycles, 2670
+// of them the tensor cores' (90 per M128 N128 K16); beside them the starts of
+// two segments per CTA, their parts and the join, 25 us together, and each of
+// the two tiles of 256 rows reads the keys and values for itself (906 MB).
 // Tensor memory: s0 | s1 (128 columns each) | o0 | o1 (D each).
 //
 // Blocks that reach past the cached tokens (drafts, the end), and all blocks
@@ -119,10 +125,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar)
                  : "memory");
 }
 
-#define BQD_R32(v)                                                                                                  \
-    v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15], v[16],    \
-        v[17], v[18], v[19], v[20], v[21], v[22], v[23], v[24], v[25], v[26], v[27], v[28], v[29], v[30], v[31]
-
 // 32 columns of this warp's 32 lanes; the loads of one wait may be several.
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r)
 {
@@ -149,8 +151,6 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* r)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-#undef BQD_R32
-
 // o of a slot's 32 rows of the warp times each row's f. Rare, so a call.
 template <int D>
 __device__ __noinline__ void rescale(uint32_t o_at, float f)
@@ -172,37 +172,53 @@ __device__ __noinline__ void rescale(uint32_t o_at, float f)
     tmem_st_wait();
 }
 
-// Bits e = 0 .. 31: whether token i of the request (t of the call) sees draft
-// j0 + e (negative: cached).
-__device__ __forceinline__ uint32_t sees32(const AttnArgs& a, int64_t t, int i, int64_t j0)
+// Bits 0 .. 127: whether token i of the request (t of the call) sees draft j0 +
+// e (negative: a cached token).
+__device__ __forceinline__ uint4 sees128(const AttnArgs& a, int64_t t, int i, int64_t j0)
 {
-    if (j0 <= -32) return 0xFFFFFFFFu;
+    uint32_t see[4];
     if (!a.mask) {
-        const int64_t last = i - j0;  // bits 0 .. last
-        return last < 0 ? 0u : last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t last = i - (j0 + 32 * k);  // bits 0 .. last
+            see[k] = last < 0 ? 0u : last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u;
+        }
+        return make_uint4(see[0], see[1], see[2], see[3]);
     }
-    const uint64_t* m = a.mask + t * a.mask_words;
-    if (j0 < 0) {
-        const int k = static_cast<int>(-j0);  // bits 0 .. k - 1 are cached tokens
-        return ((1u << k) - 1u) | static_cast<uint32_t>(m[0] << k);
+    const int64_t w = j0 > 0 ? j0 >> 6 : 0;
+    const uint64_t* m = a.mask + t * a.mask_words + w;
+    uint64_t x[3];  // 128 bits from any bit of the first
+#pragma unroll
+    for (int k = 0; k < 3; ++k) x[k] = j0 > -128 && w + k < a.mask_words ? m[k] : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t j = j0 + 32 * k;
+        if (j <= -32) {
+            see[k] = 0xFFFFFFFFu;
+        } else if (j < 0) {
+            const int c = static_cast<int>(-j);  // bits 0 .. c - 1 are cached tokens
+            see[k] = ((1u << c) - 1u) | static_cast<uint32_t>(x[0] << c);
+        } else {
+            const int at = static_cast<int>(j - 64 * w), b = at & 63;  // at: 0 .. 159
+            uint64_t v = (at < 64 ? x[0] : at < 128 ? x[1] : x[2]) >> b;
+            if (b > 32) v |= (at < 64 ? x[1] : x[2]) << (64 - b);  // at 128 .. 159: b <= 31
+            see[k] = static_cast<uint32_t>(v);
+        }
     }
-    const int64_t w = j0 >> 6;
-    const int b = static_cast<int>(j0 & 63);
-    uint64_t v = w < a.mask_words ? m[w] >> b : 0;
-    if (b > 32 && w + 1 < a.mask_words) v |= m[w + 1] << (64 - b);
-    return static_cast<uint32_t>(v);
+    return make_uint4(see[0], see[1], see[2], see[3]);
 }
 
 // The item (or part of one) that the CTA works on: written by one thread, read
 // by all, so that the softmax's registers hold scores and not bookkeeping.
 struct Seg {
-    int r, h, tile, n;      // request, kv head, tile of rows; blocks
+    int h, tile, n;         // kv head, tile of rows; blocks
     int rows, o0, group;    // live rows of the tile, first token of the request, rows per token
     int steps[2];           // softmax steps of the slots
     int plain, ctx, len;    // tokens every row sees, cached tokens, tokens: from l0, kept within +-2^30
     int64_t l0, table;      // first token; the request's row of the table
     int64_t parts;          // where its part goes; -1: it is the whole item
-    int last, skip;         // nothing of the CTA's share comes after it; no token of it is in the share
+    int skip;               // there is none
+    int odd, bad;           // drafts with values that are not finite, pages outside the cache: found while at it
 };
 
 struct Bars {
@@ -210,57 +226,126 @@ struct Bars {
 };
 
 // A block that is not all tokens seen by every row: makes its V block fit for
-// the products (V row `row`, the thread's: cleared where it is no token, or
-// not finite; both slots of a TWO item do so, each before its own products,
-// and write the same) and returns the thread's row of visibility, 128 bits.
-// v_row: the V row in shared memory, after the block has landed.
+// the products (the warp's 32 rows, from row0: cleared where they are no
+// tokens, or not finite; both slots of a TWO item do so, each before its own
+// products, and write the same) and returns the thread's row of visibility,
+// 128 bits. v: the V block in shared memory, after it has landed.
 template <int D>
-__device__ __noinline__ uint4 special_block(const AttnArgs& a, const Seg& g, int j, int row, int64_t qt, int qi,
-                                            uint8_t* v_row, int* odd_flag)
+__device__ __noinline__ uint4 special_block(const AttnArgs& a, const Seg& g, int j, int row0, int64_t qt, int qi,
+                                            uint8_t* v, int* odd_flag)
 {
     const int lane = threadIdx.x % kWarp;
-    const int br = min(a.cache.page_size, kTok), nbox = kTok / br;
+    const int sh = min(a.page_shift, 7), nbox = kTok >> sh;  // log2 of a box's tokens; kTok is 2^7
     const int rel = j * kTok;  // of the block's first token, from l0
-    const int lb = rel + lane * br;
+    const int lb = rel + (lane << sh);
     const int e = lane < nbox && lb < g.len ? a.table[g.table + ((g.l0 + lb) >> a.page_shift)] : -1;
+    const uint4 sees = sees128(a, qt, qi, rel - g.ctx);
     const uint32_t pages = __ballot_sync(0xFFFFFFFFu, e >= 0 && e < a.cache.num_pages);  // boxes that are tokens
-    const bool token = rel + row < g.len && ((pages >> (row / br)) & 1);
-    if (!token || rel + row >= g.ctx) {
-        for (int ch = 0; ch < D / 8; ++ch) {
-            uint4* p = reinterpret_cast<uint4*>(v_row + (ch / 8) * (kTok * 128) + (ch % 8) * 16);
-            const uint4 x = *p;
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            bool odd = false;
+    const int at = rel + row0 + lane;
+    const bool is_token = at < g.len && ((pages >> ((row0 + lane) >> sh)) & 1);
+    const uint32_t tokens = __ballot_sync(0xFFFFFFFFu, is_token);
+    const uint32_t drafts = __ballot_sync(0xFFFFFFFFu, is_token && at >= g.ctx);
+    if (tokens != 0xFFFFFFFFu || drafts) {
+        // a lane has 16 bytes of every fourth row, so that eight lanes read a whole line
+        uint8_t* mine = v + (row0 + lane / 8) * 128 + lane % 8 * 16;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const bool lo = (w[y] & 0x7F80u) == 0x7F80u, hi = (w[y] & 0x7F800000u) == 0x7F800000u;
-                odd |= lo || hi;
-                if (!token) w[y] = 0;
-                if (lo) w[y] &= 0xFFFF0000u;
-                if (hi) w[y] &= 0xFFFFu;
+        for (int h = 0; h < D / 64; ++h) {
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = (drafts >> (4 * i + lane / 8)) & 1
+                           ? *reinterpret_cast<const uint4*>(mine + h * (kTok * 128) + i * 512)
+                           : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                bool odd = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const bool lo = (w[y] & 0x7F80u) == 0x7F80u, hi = (w[y] & 0x7F800000u) == 0x7F800000u;
+                    odd |= lo || hi;
+                    if (lo) w[y] &= 0xFFFF0000u;
+                    if (hi) w[y] &= 0xFFFFu;
+                }
+                if (odd) {
+                    *static_cast<volatile int*>(odd_flag) = 1;  // known before the element is gone
+                    __threadfence_block();
+                }
+                if (odd || !((tokens >> (4 * i + lane / 8)) & 1))
+                    *reinterpret_cast<uint4*>(mine + h * (kTok * 128) + i * 512) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (token && odd) {
-                *static_cast<volatile int*>(odd_flag) = 1;  // known before the element is gone
-                __threadfence_block();
-            }
-            if (!token || odd) *p = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        fence_async();
     }
-    fence_async();
-    uint32_t see[4];
+    uint32_t see[4] = {sees.x, sees.y, sees.z, sees.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        see[k] = sees32(a, qt, qi, rel + 32 * k - g.ctx);
         const int left = g.len - (rel + 32 * k);
         if (left < 32) see[k] &= left <= 0 ? 0u : (1u << left) - 1u;
         uint32_t real = 0;
-        if (br >= 32)
-            real = ((pages >> (32 * k / br)) & 1) ? 0xFFFFFFFFu : 0u;
+        if (sh >= 5)
+            real = ((pages >> (32 * k >> sh)) & 1) ? 0xFFFFFFFFu : 0u;
         else
-            for (int x = 0; x < 32; ++x) real |= ((pages >> ((32 * k + x) / br)) & 1) << x;
+            for (int x = 0; x < 32; x += 1 << sh)
+                if ((pages >> ((32 * k + x) >> sh)) & 1) real |= ((1u << (1 << sh)) - 1u) << x;
         see[k] &= real;
     }
     return make_uint4(see[0], see[1], see[2], see[3]);
+}
+
+// The next item, or part of one, with tokens in the CTA's share (or a whole one
+// that has none); g.skip: there is none such. One thread's work.
+template <int D, bool TWO>
+__device__ __noinline__ void next_seg(const AttnArgs& a, AttnShare& share, int64_t& from, Seg& g)
+{
+    using S = Wide<D, TWO>;
+    AttnShare sh = share;
+    int64_t u = from, b0;
+    g.skip = 1;
+    while (g.skip && u < sh.end) {
+        const AttnReq q = attn_request(a, sh.r, S::kRows, kTok, kOver);
+        attn_place(sh, q, u, g.h, g.tile, b0);
+        int64_t cnt = min(q.nb - b0, sh.end - u);
+        const int64_t item_end = u + q.nb - b0;
+        u += cnt;
+        // the item's first kOver units stand for what it costs beside its tokens
+        cnt = max(b0 + cnt - kOver, int64_t(0));
+        b0 = max(b0 - kOver, int64_t(0));
+        cnt -= b0;
+        g.skip = cnt <= 0;
+        const int64_t l0 = b0 * kTok, l1 = min((b0 + max(cnt, int64_t(0))) * kTok, q.len);
+        auto from_l0 = [&](int64_t l) {
+            return static_cast<int>(min(max(l - l0, -(int64_t(1) << 30)), int64_t(1) << 30));
+        };
+        g.n = l1 > l0 ? static_cast<int>((l1 - l0 + kTok - 1) / kTok) : 0;
+        g.group = a.group;
+        g.rows = static_cast<int>(min(static_cast<int64_t>(q.n) * a.group - static_cast<int64_t>(g.tile) * S::kRows,
+                                      static_cast<int64_t>(S::kRows)));
+        g.o0 = q.o0;
+        g.steps[0] = TWO ? g.n : (g.n + 1) / 2;
+        g.steps[1] = TWO ? (g.rows > 128 ? g.n : 0) : g.n / 2;
+        g.ctx = from_l0(q.ctx);
+        g.len = min(from_l0(q.len), static_cast<int>(l1 - l0));
+        g.plain = max(0, min(g.ctx, from_l0(q.len)));
+        g.l0 = l0;
+        g.table = sh.r * a.width;
+        g.odd = g.bad = 0;
+        const bool whole = b0 == 0 && cnt == q.nb - kOver;
+        g.parts = whole ? -1 : (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * static_cast<int64_t>(attn_part_floats(S::kRows, D));
+        if (b0 == 0 && !whole && !g.skip)
+            static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(a, sh, q, g.h, g.tile, S::kRows, item_end);
+        if (u < sh.end) {
+            int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
+            while (u == next) {  // the next request with rows
+                ++sh.r;
+                sh.base = next;
+                next += attn_units(a, sh.r, S::kRows, kTok, kOver);
+            }
+        }
+    }
+    share.r = sh.r;
+    share.base = sh.base;
+    from = u;
 }
 
 template <int D, bool TWO>
@@ -274,9 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int64_t s_find[kThreads / kWarp + 2];
     __shared__ AttnShare s_share;
     __shared__ int64_t s_u;
-    __shared__ Seg g;
+    __shared__ Seg s_seg[2];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_odd, s_bad;
     __shared__ float s_mz[TWO ? 1 : 128][2];  // slot 1's m and z, for the join
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const sm = smem_raw + (base - smem_u32(smem_raw));
@@ -312,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) {
             s_share = sh;
             s_u = sh.start;
+            next_seg<D, TWO>(a, s_share, s_u, s_seg[0]);
         }
     }
     __syncthreads();
@@ -321,84 +406,171 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool minus = a.scale < 0.f;
     const float c = fmaxf(fabsf(a.scale), 1e-30f) * kAttnLog2e;
 
-    bool ok = true, more = s_share.start < s_share.end;
+    bool ok = true;
     uint32_t blocks = 0;              // K (and V) blocks before this item
     uint32_t steps_done[2] = {0, 0};  // softmax steps of the slots before this item
     uint32_t items_done[2] = {0, 0};  // items with a step, per slot
     uint32_t turns[2] = {0, 0};       // turns that the slots have handed on
-    while (more) {
-        if (threadIdx.x == 0) {
-            AttnShare sh = s_share;
-            int64_t u = s_u, b0;
-            const AttnReq q = attn_request(a, sh.r, S::kRows, kTok, kOver);
-            attn_place(sh, q, u, g.h, g.tile, b0);
-            int64_t cnt = min(q.nb - b0, sh.end - u);
-            const int64_t item_end = u + q.nb - b0;
-            u += cnt;
-            // the item's first kOver units stand for what it costs beside its tokens
-            cnt = max(b0 + cnt - kOver, int64_t(0));
-            b0 = max(b0 - kOver, int64_t(0));
-            cnt -= b0;
-            g.skip = cnt <= 0;
-            const int64_t l0 = b0 * kTok, l1 = min((b0 + max(cnt, int64_t(0))) * kTok, q.len);
-            auto from_l0 = [&](int64_t l) {
-                return static_cast<int>(min(max(l - l0, -(int64_t(1) << 30)), int64_t(1) << 30));
-            };
-            g.r = static_cast<int>(sh.r);
-            g.n = l1 > l0 ? static_cast<int>((l1 - l0 + kTok - 1) / kTok) : 0;
-            g.group = a.group;
-            g.rows = static_cast<int>(min(static_cast<int64_t>(q.n) * a.group - static_cast<int64_t>(g.tile) * S::kRows,
-                                          static_cast<int64_t>(S::kRows)));
-            g.o0 = q.o0;
-            g.steps[0] = TWO ? g.n : (g.n + 1) / 2;
-            g.steps[1] = TWO ? (g.rows > 128 ? g.n : 0) : g.n / 2;
-            g.ctx = from_l0(q.ctx);
-            g.len = min(from_l0(q.len), static_cast<int>(l1 - l0));
-            g.plain = max(0, min(g.ctx, from_l0(q.len)));
-            g.l0 = l0;
-            g.table = sh.r * a.width;
-            const bool whole = b0 == 0 && cnt == q.nb - kOver;
-            g.parts = whole ? -1 : (2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * static_cast<int64_t>(attn_part_floats(S::kRows, D));
-            if (b0 == 0 && !whole && !g.skip) static_cast<AttnMeta*>(a.ws)[blockIdx.x] = attn_meta(a, sh, q, g.h, g.tile, S::kRows, item_end);
-            g.last = u >= sh.end;
-            if (u < sh.end) {
-                int64_t next = sh.base + q.nb * q.tiles * a.cache.heads;
-                while (u == next) {  // the next request with rows
-                    ++sh.r;
-                    sh.base = next;
-                    next += attn_units(a, sh.r, S::kRows, kTok, kOver);
+    auto advance = [&](int n, int steps0, int steps1) {
+        blocks += n;
+        steps_done[0] += steps0;
+        steps_done[1] += steps1;
+        items_done[0] += steps0 > 0;
+        items_done[1] += steps1 > 0;
+        turns[0] += steps0 > 0 ? steps0 + 1 : 0;
+        turns[1] += steps1 > 0 ? steps1 + 1 : 0;
+    };
+    // The softmax holds a block's scores and more; the other warps need few registers. 128 x 128 + 256 x 184 of the
+    // 384 x 168 that the block has.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+        for (int cur = 0; !s_seg[cur].skip; cur ^= 1) {
+            Seg& g = s_seg[cur];
+            const int n = g.n, steps0 = g.steps[0], steps1 = g.steps[1];
+            if (warp != 0 && warp != 3) named_sync(2, kThreads - 64);  // the loads need not wait for q
+            if (warp == 0 || warp == 3) {
+                // ------------------------------------------------ loads of K (warp 0) or V (warp 3)
+                const bool is_v = warp == 3;
+                const uint32_t stages = is_v ? S::kVS : S::kKS, ring = is_v ? v_at : k_at;
+                const CUtensorMap* map = is_v ? &map_v : &map_k;
+                const int br = min(a.cache.page_size, kTok), nbox = kTok / br;  // tokens per box, boxes per block
+                const int32_t* table = a.table + g.table;
+                auto entry = [&](int rel) -> int {
+                    return lane < nbox && rel < g.len ? table[(g.l0 + rel) >> a.page_shift] : -1;
+                };
+                int rel = lane * br, next = entry(rel);
+                for (int j = 0; j < n; ++j, rel += kTok) {
+                    const int page = next >= 0 && next < a.cache.num_pages ? next : -1;
+                    const int at = static_cast<int>((g.l0 + rel) & (a.cache.page_size - 1));
+                    next = entry(rel + kTok);
+                    const uint32_t b = blocks + j, st = b % stages;
+                    uint64_t* full = is_v ? &bar.vfull[st] : &bar.kfull[st];
+                    uint64_t* empty = is_v ? &bar.vempty[st] : &bar.kempty[st];
+                    if (b >= stages) ok = ok && mbar_wait_warp(empty, (b / stages - 1) & 1, &g_attn_error);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full, S::kBlk);
+                    __syncwarp();
+                    if (lane < nbox) {
+                        const uint32_t dst = ring + st * S::kBlk + lane * br * 128;
+#pragma unroll
+                        for (int d = 0; d < D / 64; ++d) tma_load_4d(dst + d * (kTok * 128), map, 64 * d, at, g.h, page, full);
+                    }
+                    __syncwarp();
                 }
-                s_share.r = sh.r;
-                s_share.base = sh.base;
+                if (threadIdx.x == 0) next_seg<D, TWO>(a, s_share, s_u, s_seg[cur ^ 1]);  // beside the item's products
+            } else if (warp < 3) {
+                // ------------------------------------------------ products of slot warp - 1, by one thread
+                const int t = warp - 1, steps = t ? steps1 : steps0;
+                if (lane == 0 && steps > 0) {
+                    const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // f32 D, bf16 A and B, M = 128
+                    const uint32_t id_s = id | (static_cast<uint32_t>(kTok >> 3) << 17);
+                    const uint32_t id_o = id | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);  // B MN-major
+                    // descriptors advance by addresses / 16, all below 2^14
+                    const uint64_t q_desc = desc_sw128(q_at + (TWO ? t : 0) * S::kQTile, 16), k_desc = desc_sw128(k_at, 16);
+                    const uint64_t v_desc = desc_sw128(v_at, kTok * 128);
+                    const uint32_t s_col = tmem + 128 * t, o_col = tmem + 256 + t * D;
+                    const bool alone = TWO && steps1 == 0;  // the other slot's arrivals are this one's
+                    // turn u of slot 0 follows turn u - 1 of slot 1, which follows turn u - 1 of slot 0
+                    auto my_turn = [&](int u) {
+                        if (steps1 > 0 && (t == 1 || u > 0))
+                            ok = ok && mbar_wait(&bar.turn[t], (turns[1 - t] + (t ? u : u - 1)) & 1, &g_attn_error);
+                    };
+                    auto values = [&](int i) {  // o += p v of step i
+                        const uint32_t b = blocks + (TWO ? i : 2 * i + t), st = b % S::kVS, ph = (steps_done[t] + i) & 1;
+                        const uint64_t vd = v_desc + st * (S::kBlk >> 4);
+                        ok = ok && mbar_wait(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error);
+#pragma unroll
+                        for (int f = 1; f >= 0; --f) {  // p's second half comes first
+                            ok = ok && mbar_wait(&bar.pready[t][f], ph, &g_attn_error);
+                            if (f == 1) my_turn(i + 1);
+                            if (!ok) return;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 4 * f; k < 4 * f + 4; ++k)
+                                mma_ts(o_col, s_col + 64 * f + 8 * (k & 3), vd + (k * 2048 >> 4), id_o,
+                                       i == 0 && k == 4 ? 0u : 1u);
+                        }
+                        mma_commit(&bar.vempty[st]);
+                        if (alone) mma_commit(&bar.vempty[st]);
+                    };
+                    for (int i = 0; i < steps; ++i) {
+                        const uint32_t b = blocks + (TWO ? i : 2 * i + t), st = b % S::kKS;
+                        ok = ok && mbar_wait(&bar.kfull[st], (b / S::kKS) & 1, &g_attn_error);
+                        if (i > 0)
+                            values(i - 1);
+                        else
+                            my_turn(0);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kd = k_desc + st * (S::kBlk >> 4);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+                            mma_ss(s_col, q_desc + off, kd + off, id_s, k ? 1u : 0u);
+                        }
+                        mma_commit(&bar.sfull[t]);
+                        mbar_arrive(&bar.turn[1 - t]);
+                        mma_commit(&bar.kempty[st]);
+                        if (alone) mma_commit(&bar.kempty[st]);
+                    }
+                    if (ok) values(steps - 1);
+                    if (ok) {
+                        mma_commit(&bar.odone[t]);
+                        mbar_arrive(&bar.turn[1 - t]);
+                    }
+                }
+                __syncwarp();
+                ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
             }
-            s_u = u;
-            s_odd = s_bad = 0;
+            advance(n, steps0, steps1);
+            __syncthreads();  // all have read g and their own of the item
+        }
+        if ((warp == 0 || warp == 3) && !ok) {  // a wait ran out: time for the copies in flight to land before the block ends
+            const long long t0 = clock64();
+            while (clock64() - t0 < (1ll << 27)) {
+            }
         }
         __syncthreads();
-        more = !g.last;
-        if (g.skip) {
-            __syncthreads();
-            continue;
+        if (warp == 1) {
+            tc_fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
         }
-        const int n = g.n, steps0 = g.steps[0], steps1 = g.steps[1];
-        const int slot = warp >= 8 ? 1 : 0, quarter = warp % 4;  // of the softmax warps
-        const int row = 32 * quarter + lane;                     // tensor-memory lane of the thread
-        const int rows_s = TWO ? min(max(g.rows - 128 * slot, 0), 128) : g.rows;
-        const bool live = row < rows_s;
-        const uint32_t grow = live ? static_cast<uint32_t>(g.tile) * S::kRows + (TWO ? 128 * slot : 0) + row : 0u;
-        const int qi = static_cast<int>(grow / static_cast<uint32_t>(g.group));
-        const int head = g.h * g.group + static_cast<int>(grow) - qi * g.group;
-
-        if (warp >= 4) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        for (int cur = 0; !s_seg[cur].skip; cur ^= 1) {
+            Seg& g = s_seg[cur];
+            const int n = g.n, steps0 = g.steps[0], steps1 = g.steps[1];
+            const int slot = warp >= 8 ? 1 : 0, quarter = warp % 4;  // of the softmax warps
+            const int row = 32 * quarter + lane;                     // tensor-memory lane of the thread
+            const int rows_s = TWO ? min(max(g.rows - 128 * slot, 0), 128) : g.rows;
+            const bool live = row < rows_s;
+            const uint32_t grow = live ? static_cast<uint32_t>(g.tile) * S::kRows + (TWO ? 128 * slot : 0) + row : 0u;
+            const int qi = static_cast<int>(grow / static_cast<uint32_t>(g.group));
+            const int head = g.h * g.group + static_cast<int>(grow) - qi * g.group;
             // q into shared memory; pages all right?
             if (TWO || slot == 0) {
-                const uint16_t* src = a.q + (g.o0 + static_cast<int64_t>(qi)) * a.q_pitch + static_cast<int64_t>(head) * D;
-                uint8_t* dst = sm + (TWO ? slot : 0) * S::kQTile + row * 128;
+                // a row's 16 bytes a lane, all of a batch's loads ahead of its writes
+                constexpr int kCh = D / 8, kAt = kWarp / kCh, kBatch = 8;
+                const int ch = lane % kCh;
+                uint8_t* dst = sm + (TWO ? slot : 0) * S::kQTile + (ch / 8) * (128 * 128);
 #pragma unroll
-                for (int ch = 0; ch < D / 8; ++ch) {
-                    uint4 x = live ? *reinterpret_cast<const uint4*>(src + 8 * ch) : make_uint4(0, 0, 0, 0);
-                    if (minus) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
-                    *reinterpret_cast<uint4*>(dst + (ch / 8) * (128 * 128) + (((ch % 8) ^ (row & 7)) << 4)) = x;
+                for (int i0 = 0; i0 < kWarp / kAt; i0 += kBatch) {
+                    uint4 x[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = (i0 + i) * kAt + lane / kCh;
+                        const int tok = __shfl_sync(0xFFFFFFFFu, qi, r), hd = __shfl_sync(0xFFFFFFFFu, head, r);
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (32 * quarter + r < rows_s)
+                            x[i] = *reinterpret_cast<const uint4*>(a.q + (g.o0 + static_cast<int64_t>(tok)) * a.q_pitch +
+                                                                   static_cast<int64_t>(hd) * D + 8 * ch);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = 32 * quarter + (i0 + i) * kAt + lane / kCh;
+                        if (minus) x[i].x ^= 0x80008000u, x[i].y ^= 0x80008000u, x[i].z ^= 0x80008000u, x[i].w ^= 0x80008000u;
+                        *reinterpret_cast<uint4*>(dst + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) = x[i];
+                    }
                 }
                 fence_async();
             }
@@ -406,105 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t p1 = (g.l0 + g.len - 1) >> a.page_shift;
                 for (int64_t p = (g.l0 >> a.page_shift) + (threadIdx.x - 128); p <= p1; p += 256) {
                     const int32_t e = a.table[g.table + p];
-                    if (e < 0 || e >= a.cache.num_pages) s_bad = 1;
+                    if (e < 0 || e >= a.cache.num_pages) g.bad = 1;
                 }
             }
-        }
-        if (warp != 0 && warp != 3) named_sync(2, kThreads - 64);  // the loads need not wait for q
-
-        if (warp == 0 || warp == 3) {
-            // ------------------------------------------------ loads of K (warp 0) or V (warp 3)
-            const bool is_v = warp == 3;
-            const uint32_t stages = is_v ? S::kVS : S::kKS, ring = is_v ? v_at : k_at;
-            const CUtensorMap* map = is_v ? &map_v : &map_k;
-            const int br = min(a.cache.page_size, kTok), nbox = kTok / br;  // tokens per box, boxes per block
-            const int32_t* table = a.table + g.table;
-            auto entry = [&](int rel) -> int {
-                return lane < nbox && rel < g.len ? table[(g.l0 + rel) >> a.page_shift] : -1;
-            };
-            int rel = lane * br, next = entry(rel);
-            for (int j = 0; j < n; ++j, rel += kTok) {
-                const int page = next >= 0 && next < a.cache.num_pages ? next : -1;
-                const int at = static_cast<int>((g.l0 + rel) & (a.cache.page_size - 1));
-                next = entry(rel + kTok);
-                const uint32_t b = blocks + j, st = b % stages;
-                uint64_t* full = is_v ? &bar.vfull[st] : &bar.kfull[st];
-                uint64_t* empty = is_v ? &bar.vempty[st] : &bar.kempty[st];
-                if (b >= stages) ok = ok && mbar_wait_warp(empty, (b / stages - 1) & 1, &g_attn_error);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(full, S::kBlk);
-                __syncwarp();
-                if (lane < nbox) {
-                    const uint32_t dst = ring + st * S::kBlk + lane * br * 128;
-#pragma unroll
-                    for (int d = 0; d < D / 64; ++d) tma_load_4d(dst + d * (kTok * 128), map, 64 * d, at, g.h, page, full);
-                }
-                __syncwarp();
-            }
-        } else if (warp < 3) {
-            // ------------------------------------------------ products of slot warp - 1, by one thread
-            const int t = warp - 1, steps = t ? steps1 : steps0;
-            if (lane == 0 && steps > 0) {
-                const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // f32 D, bf16 A and B, M = 128
-                const uint32_t id_s = id | (static_cast<uint32_t>(kTok >> 3) << 17);
-                const uint32_t id_o = id | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);  // B MN-major
-                // descriptors advance by addresses / 16, all below 2^14
-                const uint64_t q_desc = desc_sw128(q_at + (TWO ? t : 0) * S::kQTile, 16), k_desc = desc_sw128(k_at, 16);
-                const uint64_t v_desc = desc_sw128(v_at, kTok * 128);
-                const uint32_t s_col = tmem + 128 * t, o_col = tmem + 256 + t * D;
-                const bool alone = TWO && steps1 == 0;  // the other slot's arrivals are this one's
-                // turn u of slot 0 follows turn u - 1 of slot 1, which follows turn u - 1 of slot 0
-                auto my_turn = [&](int u) {
-                    if (steps1 > 0 && (t == 1 || u > 0))
-                        ok = ok && mbar_wait(&bar.turn[t], (turns[1 - t] + (t ? u : u - 1)) & 1, &g_attn_error);
-                };
-                auto values = [&](int i) {  // o += p v of step i
-                    const uint32_t b = blocks + (TWO ? i : 2 * i + t), st = b % S::kVS, ph = (steps_done[t] + i) & 1;
-                    const uint64_t vd = v_desc + st * (S::kBlk >> 4);
-                    ok = ok && mbar_wait(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error);
-#pragma unroll
-                    for (int f = 1; f >= 0; --f) {  // p's second half comes first
-                        ok = ok && mbar_wait(&bar.pready[t][f], ph, &g_attn_error);
-                        if (f == 1) my_turn(i + 1);
-                        if (!ok) return;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 4 * f; k < 4 * f + 4; ++k)
-                            mma_ts(o_col, s_col + 64 * f + 8 * (k & 3), vd + (k * 2048 >> 4), id_o,
-                                   i == 0 && k == 4 ? 0u : 1u);
-                    }
-                    mma_commit(&bar.vempty[st]);
-                    if (alone) mma_commit(&bar.vempty[st]);
-                };
-                for (int i = 0; i < steps; ++i) {
-                    const uint32_t b = blocks + (TWO ? i : 2 * i + t), st = b % S::kKS;
-                    ok = ok && mbar_wait(&bar.kfull[st], (b / S::kKS) & 1, &g_attn_error);
-                    if (i > 0)
-                        values(i - 1);
-                    else
-                        my_turn(0);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t kd = k_desc + st * (S::kBlk >> 4);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
-                        mma_ss(s_col, q_desc + off, kd + off, id_s, k ? 1u : 0u);
-                    }
-                    mma_commit(&bar.sfull[t]);
-                    mbar_arrive(&bar.turn[1 - t]);
-                    mma_commit(&bar.kempty[st]);
-                    if (alone) mma_commit(&bar.kempty[st]);
-                }
-                if (ok) values(steps - 1);
-                if (ok) {
-                    mma_commit(&bar.odone[t]);
-                    mbar_arrive(&bar.turn[1 - t]);
-                }
-            }
-            __syncwarp();
-            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-        } else {
+            named_sync(2, kThreads - 64);
             // ------------------------------------------------ softmax
             const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
             const uint32_t s_at = tmem + lanes + 128 * slot, o_at = tmem + lanes + 256 + slot * D;
@@ -512,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, z = 0.f;
             {
                 const int steps = slot ? steps1 : steps0;
-                const int all_seen = s_bad ? 0 : g.plain / kTok;  // blocks that every row sees whole
+                const int all_seen = *static_cast<volatile int*>(&g.bad) ? 0 : g.plain / kTok;  // blocks that every row sees whole
                 const uint32_t phase0 = steps_done[slot];
                 for (int i = 0; i < steps; ++i) {
                     const int j = TWO ? i : 2 * i + slot;
@@ -525,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t b = blocks + j, st = b % S::kVS;
                         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&bar.vfull[st], (b / S::kVS) & 1, &g_attn_error));
                         if (!ok) break;
-                        see = special_block<D>(a, g, j, row, g.o0 + static_cast<int64_t>(qi), qi,
-                                               sm + (v_at - base) + st * S::kBlk + row * 128, &s_odd);
+                        see = special_block<D>(a, g, j, 32 * quarter, g.o0 + static_cast<int64_t>(qi), qi,
+                                               sm + (v_at - base) + st * S::kBlk, &g.odd);
                     }
                     if (busy) {
                         // 64 scores at a time: all 128 would not fit beside the rest. The second half is still held
@@ -637,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t qt = g.o0 + static_cast<int64_t>(qi), at = qt * a.Hq + head;
                 const int prow = (TWO ? 128 * slot : 0) + row;
                 float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_meta_bytes()) + g.parts;
-                const bool odd = *static_cast<volatile int*>(&s_odd) != 0;
+                const bool odd = *static_cast<volatile int*>(&g.odd) != 0;
                 for (int k = 0; k < D / 32; ++k) {
                     uint32_t o[32];
                     if (steps0 > 0) {  // a slot that is busy has steps if the other has
@@ -698,25 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             fence_async();  // the join's memory goes back to the copies
+            advance(n, steps0, steps1);
+            __syncthreads();
         }
-        blocks += n;
-        steps_done[0] += steps0;
-        steps_done[1] += steps1;
-        items_done[0] += steps0 > 0;
-        items_done[1] += steps1 > 0;
-        turns[0] += steps0 > 0 ? steps0 + 1 : 0;
-        turns[1] += steps1 > 0 ? steps1 + 1 : 0;
-        __syncthreads();  // all have read g and their own of the item
-    }
-    if ((warp == 0 || warp == 3) && !ok) {  // a wait ran out: time for the copies in flight to land before the block ends
-        const long long t0 = clock64();
-        while (clock64() - t0 < (1ll << 27)) {
-        }
-    }
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        __syncthreads();
     }
 }
 
@@ -779,11 +841,11 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
 
 }  // namespace
 
-// From a mean of 33 rows per kv head: below, the narrow kernel's 16 or 32 rows
-// hold a request in one tile, and its shorter pipeline reads faster (16
-// requests of 8192 tokens, 24 rows: 76 us against 184); above, it would read
-// keys and values once per tile (48 rows: 126 us against 106; 1024 tokens'
-// worth of rows in tiles of 256: 934 against 215 for four contexts of 32768).
+// From a mean of 33 rows per kv head. Up to 32 rows, one tile of the narrow
+// kernel holds a request, and its shorter pipeline reads faster: 16 requests of
+// 24 rows over 8192 tokens take it 76 us, this kernel 184. Above, the narrow one
+// reads keys and values once per tile: with 48 rows 126 us against 106 here, with
+// 512 rows (four contexts of 32768 tokens) 934 against 203.
 bool tree_attention_wide_fits(const AttnArgs& a)
 {
     const bqd_kv_cache& c = a.cache;

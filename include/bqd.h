@@ -4,7 +4,11 @@
  * FP8 block-128), for N = 1 token (plain decode) up to N = 16 (speculative
  * verify), and a top-k routed MoE layer whose experts are NVFP4; around
  * them, decode-path epilogue fusions, bf16 -> NVFP4 / Q8_0 encoders, and
- * NVFP4 prefill GEMMs on the tensor cores with a MoE prefill layer.
+ * NVFP4 prefill GEMMs on the tensor cores with a MoE prefill layer; and the
+ * rest of a decode or verify step around its projections: slots of new tokens
+ * in a paged KV cache, norm, rotary positions and the write of K and V into
+ * it, attention of drafted tokens over it, and the log probabilities, entropy
+ * and top alternatives of the step's logits.
  *
  * Sources (what each call computes):
  *  - "Vemloir/LumenLLM" README, Quantization and Kernels bullets: weights in
@@ -238,8 +242,9 @@ bqd_status q8_0_gemv_path(const int8_t* q, const uint16_t* d, const uint16_t* x,
  * bqd_device_error -- waits for the device, copies the device error words of
  * the streaming and tensor-core GEMV kernels (BQD_PATH_STREAM, BQD_PATH_MMA),
  * of the MoE stream kernels, of the small-batch MoE kernels (the
- * activations' copy in moe_layer / moe_grouped_gemv at T <= 16) and of the
- * prefill GEMM (nvfp4_gemm) to *bits_out (OR of the five) and clears them. Bit 0: a wait ran out
+ * activations' copy in moe_layer / moe_grouped_gemv at T <= 16), of the
+ * prefill GEMM (nvfp4_gemm), of token_logprobs and of tree_attention to
+ * *bits_out (OR of them all) and clears them. Bit 0: a wait ran out
  * (the kernel gave up instead of hanging; its outputs are unspecified).
  * Returns BQD_ERR_DEVICE if any bit was set. Synchronising: do not call it
  * inside a stream capture.
@@ -640,8 +645,9 @@ bqd_status qk_norm_rope_cache(const void* q, const void* k, const void* v, int i
  *      tokens that belong to no request are not written.
  *   workspace: tree_attention_workspace_bytes(...) bytes, 16-byte aligned.
  * Scores, softmax and sums are fp32; the probabilities enter the product
- * with V as bf16 (relative error 2^-9 each). Hq a multiple of cache->heads, Hq / heads
- * <= 64; R * heads < 2^24, T * Hq < 2^31.
+ * with V as bf16 (relative error 2^-9 each), over BQD_E4M3 caches as f16
+ * (2^-12 each). Hq a multiple of cache->heads, Hq / heads <= 64; R * heads <
+ * 2^24, T * Hq < 2^31.
  */
 bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache* cache, const int32_t* block_table,
                           int64_t table_width, const int32_t* context_lens, const int32_t* token_offsets,
@@ -664,8 +670,8 @@ size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int
  * makes its log probabilities and entropy NaN; among the alternatives NaN
  * ranks below -inf. tokens with logprob, entropy, and top_ids with
  * top_logprobs may be NULL; topk 0 .. 32, at most V.
- * workspace: token_logprobs_workspace_bytes(T, V, topk) bytes, 16-byte
- * aligned. T >= 0, 1 <= V < 2^31.
+ * workspace: token_logprobs_workspace_bytes(T, V, topk) bytes (a few today:
+ * rows are joined on chip), 16-byte aligned. T >= 0, 1 <= V < 2^31.
  */
 bqd_status token_logprobs(const void* logits, int in_type, int64_t pitch, const int32_t* tokens, float* logprob,
                           float* entropy, int32_t* top_ids, float* top_logprobs, int topk, void* workspace,
