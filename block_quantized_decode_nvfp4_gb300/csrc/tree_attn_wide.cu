@@ -547,40 +547,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t grow = live ? static_cast<uint32_t>(g.tile) * S::kRows + (TWO ? 128 * slot : 0) + row : 0u;
             const int qi = static_cast<int>(grow / static_cast<uint32_t>(g.group));
             const int head = g.h * g.group + static_cast<int>(grow) - qi * g.group;
-            // q into shared memory; pages all right?
+            // q into shared memory; pages all right? (the first read of them ahead of q)
+            const int64_t p0 = (g.l0 >> a.page_shift) + (threadIdx.x - 128), p1 = (g.l0 + g.len - 1) >> a.page_shift;
+            const int32_t e0 = n > 0 && p0 <= p1 ? a.table[g.table + p0] : 0;
             if (TWO || slot == 0) {
-                // a row's 16 bytes a lane, all of a batch's loads ahead of its writes
-                constexpr int kCh = D / 8, kAt = kWarp / kCh, kBatch = 8;
+                // a row's 16 bytes a lane, all loads ahead of the writes
+                constexpr int kCh = D / 8, kAt = kWarp / kCh, kBatch = kWarp / kAt;
                 const int ch = lane % kCh;
                 uint8_t* dst = sm + (TWO ? slot : 0) * S::kQTile + (ch / 8) * (128 * 128);
+                uint4 x[kBatch];
 #pragma unroll
-                for (int i0 = 0; i0 < kWarp / kAt; i0 += kBatch) {
-                    uint4 x[kBatch];
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = i * kAt + lane / kCh;
+                    const int tok = __shfl_sync(0xFFFFFFFFu, qi, r), hd = __shfl_sync(0xFFFFFFFFu, head, r);
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (32 * quarter + r < rows_s)
+                        x[i] = *reinterpret_cast<const uint4*>(a.q + (g.o0 + static_cast<int64_t>(tok)) * a.q_pitch +
+                                                               static_cast<int64_t>(hd) * D + 8 * ch);
+                }
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = (i0 + i) * kAt + lane / kCh;
-                        const int tok = __shfl_sync(0xFFFFFFFFu, qi, r), hd = __shfl_sync(0xFFFFFFFFu, head, r);
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (32 * quarter + r < rows_s)
-                            x[i] = *reinterpret_cast<const uint4*>(a.q + (g.o0 + static_cast<int64_t>(tok)) * a.q_pitch +
-                                                                   static_cast<int64_t>(hd) * D + 8 * ch);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = 32 * quarter + (i0 + i) * kAt + lane / kCh;
-                        if (minus) x[i].x ^= 0x80008000u, x[i].y ^= 0x80008000u, x[i].z ^= 0x80008000u, x[i].w ^= 0x80008000u;
-                        *reinterpret_cast<uint4*>(dst + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) = x[i];
-                    }
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = 32 * quarter + i * kAt + lane / kCh;
+                    if (minus) x[i].x ^= 0x80008000u, x[i].y ^= 0x80008000u, x[i].z ^= 0x80008000u, x[i].w ^= 0x80008000u;
+                    *reinterpret_cast<uint4*>(dst + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) = x[i];
                 }
                 fence_async();
             }
-            if (n > 0) {
-                const int64_t p1 = (g.l0 + g.len - 1) >> a.page_shift;
-                for (int64_t p = (g.l0 >> a.page_shift) + (threadIdx.x - 128); p <= p1; p += 256) {
-                    const int32_t e = a.table[g.table + p];
-                    if (e < 0 || e >= a.cache.num_pages) g.bad = 1;
-                }
+            bool bad = e0 < 0 || e0 >= a.cache.num_pages;
+            for (int64_t p = p0 + 256; n > 0 && p <= p1; p += 256) {
+                const int32_t e = a.table[g.table + p];
+                bad |= e < 0 || e >= a.cache.num_pages;
             }
+            if (bad) g.bad = 1;
             named_sync(2, kThreads - 64);
             // ------------------------------------------------ softmax
             const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
