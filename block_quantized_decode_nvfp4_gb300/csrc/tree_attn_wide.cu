@@ -26,11 +26,12 @@
 // a row's maximum has grown by more than 2^8 (p then stays below 2^8, and
 // nothing is lost: fp32 sums, bf16's range).
 //
-// Four trees of 64 tokens over 32768 (64 query heads on 8, D = 128): 203 us,
-// 1.06 PFLOP/s of products. A block of both slots takes about 3300 cycles, 2670
-// of them the tensor cores' (90 per M128 N128 K16); beside them the starts of
-// two segments per CTA, their parts and the join, 25 us together, and each of
-// the two tiles of 256 rows reads the keys and values for itself (906 MB).
+// Four trees of 64 tokens over 32768 (64 query heads on 8, D = 128): 191 us,
+// 1.12 PFLOP/s of products. A block of both slots takes about 3000 cycles, 2670
+// of them the tensor cores' (83 per M128 N128 K16: the score product reads 8 KB
+// of shared memory for each); beside them the launch, the starts of two items
+// per CTA, their parts and the join, 27 us together. Each of the two tiles of
+// 256 rows reads the keys and values for itself (906 MB).
 // Tensor memory: s0 | s1 (128 columns each) | o0 | o1 (D each).
 //
 // Blocks that reach past the cached tokens (drafts, the end), and all blocks
@@ -841,9 +842,10 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
 
 // From a mean of 33 rows per kv head. Up to 32 rows, one tile of the narrow
 // kernel holds a request, and its shorter pipeline reads faster: 16 requests of
-// 24 rows over 8192 tokens take it 76 us, this kernel 184. Above, the narrow one
-// reads keys and values once per tile: with 48 rows 126 us against 106 here, with
-// 512 rows (four contexts of 32768 tokens) 934 against 203.
+// 24 rows over 8192 tokens take it 77 us, this kernel 87 (1000 tokens: 25 and
+// 32). Above, the narrow one reads keys and values once per tile: with 48 rows
+// 126 us against 95 here, with 512 rows (four contexts of 32768 tokens) 934
+// against 191.
 bool tree_attention_wide_fits(const AttnArgs& a)
 {
     const bqd_kv_cache& c = a.cache;
