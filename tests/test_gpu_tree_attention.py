@@ -279,3 +279,20 @@ def test_refusals():
     call(T=0)
     call(R=0)
     assert bqd.tree_attention_workspace_bytes(1, 1, 3, 2, 64) == 0
+
+
+@pytest.mark.parametrize("ctx", [0, 1, 37, 64, 91, 127, 300])
+@pytest.mark.parametrize("D,page", [(64, 8), (128, 16), (128, 64)])
+def test_masks_of_several_words(ctx, D, page):
+    """Random bits over more drafts than a block of tokens holds, the first of them anywhere in a block."""
+    n, words = 210, 4
+    rng = np.random.default_rng(ctx + D + page)
+    pages = -(-(ctx + n) // page) + 3
+    cache = Cache(pages, page, 1, D, "bf16", "tokens", ctx, 0)
+    table = table_for([ctx + n], page, pages, ctx)
+    q = queries(n, 2, D, ctx)
+    mask = rng.integers(0, 2 ** 64, (n, words), dtype=np.uint64, endpoint=False)
+    mask[5] = 0
+    rows = {0, 5, 31, 63, 64, 100, 128, 160, 191, 209}
+    out, lse = run_attention(cache, q, table, [ctx], [0, n], mask, D ** -0.5)
+    check_attention(cache, q, table, [ctx], [0, n], mask, D ** -0.5, out, lse, rows, f"{ctx} {D} {page}")
