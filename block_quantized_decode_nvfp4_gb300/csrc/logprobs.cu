@@ -33,10 +33,12 @@
 // passes goes to the warp's own list of up to 64 keys; one that has grown past
 // 32 is cut back to its k best (each entry counts the larger ones), and as a
 // warp's logits come in ascending tiles, those of later tiles have to exceed
-// its k-th from then on. About k (1 + log(tiles)) logits pass in a row of
-// distinct logits; rows of equal ones cost a few cuts in their first tile. At
-// the end the lists are joined, first the CTA's, then the cluster's, by the
-// same count.
+// its k-th from then on: of equal logits the list has those of lower indices.
+// (So the logits after the row's last whole window, its highest indices, join
+// their warp's list after its last tile.) About k (1 + log(tiles)) logits pass
+// in a row of distinct logits; rows of equal ones cost a few cuts in their
+// first tile. At the end the lists are joined, first the CTA's, then the
+// cluster's, by the same count.
 //
 // Measured over 151936 logits: one fp32 row with 20 alternatives 9.8 us, 128 with
 // 8 25.4 us (18.5 without alternatives), 2047 bf16 rows with 5 130.6 us or 4.8
@@ -67,8 +69,10 @@ constexpr int kTileWindows = 2048;
 constexpr int kTileBytes = kTileWindows * 16;
 constexpr int kList = 64;                           // entries of a warp's list
 constexpr int kMaxK = 32;
+constexpr int kTail = 14;                           // logits outside a row's whole windows at most (bf16: 7 and 7)
 constexpr int kMaxCluster = 16;
-static_assert(kList == 2 * kWarp && kMaxK <= kWarp, "a cut handles two keys per lane, and leaves room for a ballot");
+static_assert(kList == 2 * kWarp && kMaxK <= kWarp && kTail <= kWarp,
+              "a cut handles two keys per lane, and leaves room for a ballot");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
@@ -243,6 +247,8 @@ struct Shared {
     // keys to be cut to the k best: at most kMaxK of each warp, or of each CTA; +16: padding
     alignas(16) uint64_t cand[kMaxCluster * kMaxK + 16];
     uint64_t top[kMaxK];                      // this CTA's best, descending
+    uint64_t tail[kTail];                     // keys of the logits after the row's whole windows
+    int tails;                                // their number
     Sums sums[WARPS];
     alignas(16) uint32_t bound[kWarp];        // the lane groups' maxima, as ordered bits; 0: none above -inf
     uint32_t tau;                             // the k-th largest of them; 0: fewer than k
@@ -398,6 +404,7 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
     if (threadIdx.x == 0) {
         s.count = 0;
         s.tau = 0;
+        s.tails = 0;
     }
     // the row's ends, by the first CTA's first warp, a logit per lane
     if (rank == 0 && warp == 0) {
@@ -405,7 +412,8 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
         const int head = whole ? p.whole0 * N - p.pre : 0;
         const int64_t tail0 = whole ? static_cast<int64_t>(p.whole1) * N - p.pre : 0;
         const int64_t i = lane < head ? lane : tail0 + (lane - head);
-        have = head + static_cast<int>(V - tail0);
+        have = head;
+        if (lane == 0) s.tails = static_cast<int>(V - tail0);
         if (i < V) {
             float v;
             if constexpr (sizeof(T) == 4)
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
             raise(sum, v);
             sum.z = v == -INFINITY ? 0.f : v - v + 1.f;  // NaN for NaN (and for +inf)
             seen = v;
-            list[lane] = order_key(v, static_cast<uint32_t>(i));
+            (lane < head ? list[lane] : s.tail[lane - head]) = order_key(v, static_cast<uint32_t>(i));
         }
     }
     __syncthreads();
@@ -525,6 +533,11 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[st]);
+    }
+    if (warp == 0) {  // the list holds 32 at most
+        const int tails = s.tails;
+        if (lane < tails) list[have + lane] = s.tail[lane];
+        have += tails;
     }
     // the block's sums
     sum = join_warp(sum);

@@ -227,3 +227,33 @@ def test_refusals():
         assert e.value.status == status, kw
     call(T=0)
     assert bqd.token_logprobs_workspace_bytes(1, 10, 11) == 0
+
+
+def tie_with_the_end(V, T, dtype, k, low=0.0):
+    """Constant rows but for k - 1 larger logits at the row's start and two equal ones: the row's last, and one of the
+    second thousand 16-byte windows, which the same warp meets later and which has the lower index."""
+    n = 4 if dtype == "f32" else 8
+    x = torch.full((T, V), low)
+    x[:, :k - 1] = 6.0
+    x[:, 1025 * n] = 5.0
+    x[:, V - 1] = 5.0
+    return (x if dtype == "f32" else x.to(torch.bfloat16)).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [32769, 50257, 151937, 151939])
+@pytest.mark.parametrize("k", [2, 20, 32])
+@pytest.mark.parametrize("T", [1, 200])
+def test_ties_with_the_end_of_the_row(dtype, V, k, T):
+    # odd V: rows begin and end at every alignment
+    check(tie_with_the_end(V, T, dtype, k), [V - 1] * T, k, rows=sorted({0, min(1, T - 1), min(6, T - 1), T - 1}))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 13, 21, 16385, 32769, 50257])
+@pytest.mark.parametrize("T", [1, 4])
+def test_coarse_rows_of_any_end(dtype, V, T):
+    x = torch.randint(-3, 4, (T, V), generator=torch.Generator().manual_seed(V)).float()
+    x[:, -3:] = 3.0  # the end ties with the largest
+    for k in (1, min(5, V), min(32, V)):
+        check((x if dtype == "f32" else x.to(torch.bfloat16)).cuda(), [V - 1] * T, k)
