@@ -106,9 +106,17 @@ struct Sums {
     float m, z, u;
 };
 
-// Beyond this size a maximum's product with log2(e) may overflow (a row masked
-// throughout by the type's lowest value): differences are taken first there.
-constexpr float kHuge = 1e38f;
+// From this size of a maximum on, differences are taken before the product with
+// log2(e): the product's rounding, which t and with it z carry as a shift, would
+// exceed 2^6 and leave the range of 2^t (logits masked throughout by a large
+// negative value), and further on the product itself would overflow.
+constexpr float kHuge = 1073741824.f;
+
+// The shift of t and log2(z) for a maximum m: what m log2(e) lost when rounded.
+__device__ __forceinline__ float shift_of(float m)
+{
+    return fabsf(m) < kHuge ? fmaf(m, kLog2e, -__fmul_rn(m, kLog2e)) : 0.f;
+}
 
 __device__ __forceinline__ void raise(Sums& s, float m)  // s relative to m >= s.m
 {
@@ -421,7 +429,9 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
             else
                 v = __bfloat162float(p.x[i]);
             raise(sum, v);
-            sum.z = v == -INFINITY ? 0.f : v - v + 1.f;  // NaN for NaN (and for +inf)
+            const float shift = shift_of(v);
+            sum.z = v == -INFINITY ? 0.f : v - v + ex2(shift);  // NaN for NaN (and for +inf)
+            sum.u = sum.z * shift;
             seen = v;
             (lane < head ? list[lane] : s.tail[lane - head]) = order_key(v, static_cast<uint32_t>(i));
         }
@@ -612,8 +622,7 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
     if (warp == 0) {
         if (sum.m == INFINITY) sum.z = sum.m - sum.m;  // +inf among the logits: NaN
         // an empty row: every log probability is -inf
-        const float moved = fabsf(sum.m) < kHuge ? fmaf(sum.m, kLog2e, -__fmul_rn(sum.m, kLog2e)) : 0.f;
-        const float lse = sum.z == 0.f ? INFINITY : sum.m + (log2f(sum.z) - moved) * kLn2;
+        const float lse = sum.z == 0.f ? INFINITY : sum.m + (log2f(sum.z) - shift_of(sum.m)) * kLn2;
         if (lane == 0) {
             if (a.logprob) {
                 const int tok = a.tokens[t];

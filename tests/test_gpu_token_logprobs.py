@@ -257,3 +257,31 @@ def test_coarse_rows_of_any_end(dtype, V, T):
     x[:, -3:] = 3.0  # the end ties with the largest
     for k in (1, min(5, V), min(32, V)):
         check((x if dtype == "f32" else x.to(torch.bfloat16)).cuda(), [V - 1] * T, k)
+
+
+def check_masked(x, tok, k):
+    """Rows of a few distinct values whose gaps are 0 or more than 1000: the entropy is that of the largest's copies,
+    good to 2^-12 (1 + entropy) and the shift that the maximum's product with log2(e) leaves, at most 64, times 2^-13."""
+    rows = [0, 1, 2, 3, 4, x.shape[0] - 1]
+    _, ent, _, _ = check(x, tok, k, rows=rows)
+    for t in rows:
+        row = x[t].double().cpu().numpy()
+        H = np.log((row == row.max()).sum())
+        shift = min(64.0, np.abs(row.max()) * 2.0 ** -23)
+        assert abs(ent[t] - H) <= 2.0 ** -12 * (1 + H) + 2.0 ** -13 * shift, (t, ent[t], H)
+
+
+@pytest.mark.parametrize("low", [-1e5, -1e9, -3e9, -1e10, -1e20, -1e30, -9e37, -1.1e38])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [5, 200])
+def test_rows_masked_by_a_large_value(low, dtype, T):
+    # what a mask other than -inf or the type's lowest value leaves: all of a row hidden, one logit, a few, the first half
+    V = 40007
+    x = torch.full((T, V), low)
+    x[1, 39999] = 2.0
+    x[2, 100:104] = 1.0
+    x[3, V // 2:] = 0.5
+    x[4, :] = -low
+    x = (x if dtype == "f32" else x.to(torch.bfloat16)).cuda()
+    tok = [3, 39999, 102, V - 1, 7] + [0] * (T - 5)
+    check_masked(x, tok, 8)
