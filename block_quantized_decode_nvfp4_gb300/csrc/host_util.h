@@ -1,5 +1,5 @@
 // host_util.h -- host-side launch helpers shared by the kernels' launchers:
-// per-device attributes and per-kernel occupancy, both cached.
+// per-device attributes, and per-kernel occupancy and attributes, all cached.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -42,6 +42,7 @@ inline DevInfo dev_info(int dev)
 struct OccCache {
     std::mutex mu;
     bool attr_set[64] = {};
+    bool wide_clusters[64] = {};
     size_t smem[64][4] = {};
     int val[64][4] = {};
 };
@@ -76,6 +77,21 @@ inline int blocks_per_sm(OccCache& c, const void* kern, int dev, int threads, si
             break;
         }
     return n;
+}
+
+// Allows a kernel clusters of more than 8 CTAs on the device: an attribute of
+// the kernel on that device, so it is set once for each. A failure is returned
+// and not kept.
+inline cudaError_t allow_wide_clusters(OccCache& c, const void* kern, int dev)
+{
+    std::lock_guard<std::mutex> g(c.mu);
+    if (dev >= 0 && dev < 64 && c.wide_clusters[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess)
+        cudaGetLastError();  // consumed: it must not surface as a launch error later
+    else if (dev >= 0 && dev < 64)
+        c.wide_clusters[dev] = true;
+    return e;
 }
 
 }  // namespace bqd

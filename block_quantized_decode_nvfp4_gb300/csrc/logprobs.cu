@@ -654,15 +654,15 @@ cudaError_t launch_as(const LogprobArgs& a, int C, cudaStream_t s)
     const unsigned grid = static_cast<unsigned>(a.T * C);
     static OccCache occ;
     int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, (WARPS + 1) * kWarp, kSmem);  // opts in to kSmem
     if (!CLUSTER) {
         kern<<<grid, (WARPS + 1) * kWarp, kSmem, s>>>(a, 1);
         return cudaGetLastError();
     }
-    static const cudaError_t wide = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (wide != cudaSuccess) return wide;
+    e = allow_wide_clusters(occ, reinterpret_cast<const void*>(kern), dev);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((WARPS + 1) * kWarp);
