@@ -667,7 +667,7 @@ static bool attn_sizes_ok(int64_t R, int64_t T, int64_t Hq, int64_t Hkv, int64_t
 size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int D)
 {
     if (!attn_sizes_ok(R, T, Hq, Hkv, D)) return 0;
-    return bqd::tree_attention_ws(R, T, Hq, Hkv, D);
+    return bqd::tree_attention_ws(T, Hq, Hkv, D);
 }
 
 bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache* cache, const int32_t* block_table,
@@ -689,7 +689,7 @@ bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache
         !elem_aligned(mask) || !elem_aligned(lse))
         return BQD_ERR_ALIGN;
     if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < bqd::tree_attention_ws(R, T, Hq, cache->heads, cache->head_dim))
+        workspace_bytes < bqd::tree_attention_ws(T, Hq, cache->heads, cache->head_dim))
         return BQD_ERR_WORKSPACE;
     if ((st = check_arch()) != BQD_OK) return st;
     bqd::AttnArgs a{};

@@ -49,7 +49,7 @@ struct AttnArgs {
     int group, page_shift;  // query heads per kv head, log2 of the page size
     bqd_kv_cache cache;
 };
-size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D);
+size_t tree_attention_ws(int64_t T, int Hq, int Hkv, int D);
 cudaError_t launch_tree_attention(const AttnArgs& a, cudaStream_t s);
 cudaError_t read_and_clear_attn_error(unsigned int* out);
 

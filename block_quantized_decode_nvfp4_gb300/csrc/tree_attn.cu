@@ -642,11 +642,14 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 
 }  // namespace
 
-size_t tree_attention_ws(int64_t R, int64_t T, int Hq, int Hkv, int D)
+// Parts are as tall as a call's tiles, which grow with the mean rows per
+// request: the size is that for one request with all T tokens, the tallest, so
+// that it holds for any number of requests and grows with T alone.
+size_t tree_attention_ws(int64_t T, int Hq, int Hkv, int D)
 {
-    const int rows = kRows16 * row_groups(R, T, Hq, Hkv);
+    const int rows = kRows16 * row_groups(1, T, Hq, Hkv);
     const size_t narrow = attn_meta_bytes() + 2 * kAttnMaxGrid * attn_part_floats(rows, D) * sizeof(float);
-    const size_t wide = tree_attention_wide_ws(R, T, Hq, Hkv, D);
+    const size_t wide = tree_attention_wide_ws(T, Hq, Hkv, D);
     return narrow > wide ? narrow : wide;
 }
 

@@ -437,7 +437,7 @@ inline cudaError_t launch_attn_join(void (*kernel)(AttnArgs, int), const AttnArg
 
 // The kernel for many rows a kv head (tree_attn_wide.cu), bf16 caches.
 bool tree_attention_wide_fits(const AttnArgs& a);
-size_t tree_attention_wide_ws(int64_t R, int64_t T, int Hq, int Hkv, int D);
+size_t tree_attention_wide_ws(int64_t T, int Hq, int Hkv, int D);
 cudaError_t launch_tree_attention_wide(const AttnArgs& a, cudaStream_t s);
 
 }  // namespace bqd

@@ -858,10 +858,10 @@ bool tree_attention_wide_fits(const AttnArgs& a)
            c.num_pages < (int64_t(1) << 31) && a.T * a.group > 32 * a.R;
 }
 
-size_t tree_attention_wide_ws(int64_t R, int64_t T, int Hq, int Hkv, int D)
+size_t tree_attention_wide_ws(int64_t T, int Hq, int Hkv, int D)
 {
     if (D > 128) return 0;
-    return attn_meta_bytes() + 2 * kGrid * attn_part_floats(wide_two(R, T, Hq, Hkv) ? 256 : 128, D) * sizeof(float);
+    return attn_meta_bytes() + 2 * kGrid * attn_part_floats(wide_two(1, T, Hq, Hkv) ? 256 : 128, D) * sizeof(float);
 }
 
 cudaError_t launch_tree_attention_wide(const AttnArgs& a, cudaStream_t s)

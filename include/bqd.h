@@ -654,7 +654,12 @@ bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache
                           const uint64_t* mask, int mask_words, float scale, uint16_t* out, float* lse,
                           void* workspace, size_t workspace_bytes, int64_t R, int64_t T, int Hq, cudaStream_t stream);
 
-/* Bytes of device workspace tree_attention needs for these sizes (0 if a size is out of range). */
+/*
+ * Bytes of device workspace tree_attention needs for these sizes (0 if a size
+ * is out of range; 41 MB at most). It holds for every call of no more
+ * requests and tokens with these heads and this head dimension: a program
+ * sizes it once, for its largest batch.
+ */
 size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int D);
 
 /*

@@ -83,3 +83,15 @@ def test_token_logprobs(L):
     assert call(ws=None) == 6 and call(ws=U) == 6 and call(wsb=size - 1) == 6
     assert call(T=0) == 0
     assert L.token_logprobs_workspace_bytes(1, 4, 5) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (8, 1), (40, 8), (64, 1)])
+def test_tree_attention_workspace_serves_smaller_calls(L, Hq, Hkv, D):
+    # a program sizes it once, for its largest batch: a batch that shrinks to one wide draft needs no more
+    sizes = [0, 1, 2, 3, 4, 7, 16, 17, 32, 33, 63, 64, 128, 129, 256, 1024, 8191]
+    need = {(R, T): L.tree_attention_workspace_bytes(R, T, Hq, Hkv, D) for R in sizes[:-2] for T in sizes}
+    assert all(n > 0 for n in need.values())
+    for (R, T), n in need.items():
+        for (r, t), m in need.items():
+            assert m <= n or r > R or t > T, ((R, T, n), (r, t, m))
