@@ -65,6 +65,7 @@ constexpr int kTok = 128;  // tokens per block (and unit of the split)
 constexpr int kGrid = 152;
 constexpr int kOver = 4;  // units that an item's beginning and end cost
 constexpr float kGrow = 8.f;
+constexpr float kHuge = 67108864.f;  // of a maximum in log2 units: below it, its rounding moves p by 2^4 at most
 
 template <int D, bool TWO>
 struct Wide {
@@ -171,6 +172,42 @@ __device__ __noinline__ void rescale(uint32_t o_at, float f)
         tmem_st(o_at + 32 * k, o);
     }
     tmem_st_wait();
+}
+
+// The softmax of a block in which a row's scores are huge: s c - m in one
+// rounding would leave of the row's largest what m was rounded by, which p
+// cannot hold, so differences are taken of the rounded products. Writes p and
+// hands it on as the loop does; the row's sum of p.
+__device__ __noinline__ float far_block(uint32_t s_at, uint4 see, float c, float m, uint64_t* ready)
+{
+    const float sub = m == -INFINITY ? 0.f : m;
+    float z = 0.f;
+#pragma unroll 1
+    for (int k = 1; k >= 0; --k) {
+        uint32_t s[64], p[32];
+        tmem_ld(s_at + 64 * k, s);
+        tmem_ld(s_at + 64 * k + 32, s + 32);
+        tmem_ld_wait();
+        const uint32_t lo = k ? see.z : see.x, hi = k ? see.w : see.y;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            float x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * e + i;
+                const bool seen = ((t < 32 ? lo : hi) >> (t & 31)) & 1;
+                x[i] = seen ? attn_ex2(__fmul_rn(__uint_as_float(s[t]), c) - sub) : 0.f;
+            }
+            z += x[0] + x[1];
+            p[e] = attn_bf16x2(x[0], x[1]);
+        }
+        tmem_st(s_at + 64 * k, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (threadIdx.x % kWarp == 0) mbar_arrive(&ready[k]);
+    }
+    return z;
 }
 
 // Bits 0 .. 127: whether token i of the request (t of the call) sees draft j0 +
@@ -630,12 +667,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
                         const bool grown = m != -INFINITY && mn > m + kGrow;
-                        if (__any_sync(0xFFFFFFFFu, grown)) {
+                        const bool far = fabsf(mn) >= kHuge && mn != -INFINITY;
+                        bool plain = true;
+                        if (__any_sync(0xFFFFFFFFu, grown || far)) {
                             const float f = grown ? attn_ex2(m - mn) : 1.f;
                             z *= f;
                             rescale<D>(o_at, f);
+                            plain = !__any_sync(0xFFFFFFFFu, far);
                         }
                         if (grown || m == -INFINITY) m = mn;
+                        if (!plain) {
+                            z += far_block(s_at, see, c, m, bar.pready[slot]);
+                            continue;
+                        }
                         const float sub = m == -INFINITY ? 0.f : -m;
                         const uint64_t cc = pack(c, c), ss = pack(sub, sub);
                         uint64_t z0 = 0, z1 = 0;

@@ -296,3 +296,31 @@ def test_masks_of_several_words(ctx, D, page):
     rows = {0, 5, 31, 63, 64, 100, 128, 160, 191, 209}
     out, lse = run_attention(cache, q, table, [ctx], [0, n], mask, D ** -0.5)
     check_attention(cache, q, table, [ctx], [0, n], mask, D ** -0.5, out, lse, rows, f"{ctx} {D} {page}")
+
+
+@pytest.mark.parametrize("gain", [1e4, 1e7, 1e9, 3e10, 1e20])
+@pytest.mark.parametrize("kind,D,n", [("bf16", 64, 2), ("bf16", 128, 10), ("bf16", 128, 40), ("bf16", 256, 10)])
+def test_scores_of_any_size(kind, D, n, gain):
+    # scores far apart: each token's largest takes all, whatever the scores' size; the second token is a copy of the first
+    ctx, Hq, Hkv, page = [300], 8, 2, 16
+    cache = Cache(40, page, Hkv, D, kind, seed=3)
+    table = table_for([ctx[0] + n], page, 40, 3)
+    q = queries(n, Hq, D, 4, gain)
+    pg, at = int(table[0, 0]), 0
+    cache.k[int(table[0, 0]), 1] = cache.k[pg, at]
+    out, lse = run_attention(cache, q, table, ctx, [0, n], None, D ** -0.5)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    K, V = cache.values("k"), cache.values("v")
+    slot = table[0][np.arange(ctx[0] + n) // page] * page + np.arange(ctx[0] + n) % page
+    o = out.double().cpu().numpy()
+    for t in range(n):
+        for h in range(Hq):
+            k, v = K[slot[:ctx[0] + t + 1], h // (Hq // Hkv)], V[slot[:ctx[0] + t + 1], h // (Hq // Hkv)]
+            s = (k @ q[t, h].double().cpu().numpy()) * D ** -0.5
+            order = np.argsort(-s, kind="stable")
+            best, second = s[order[0]], s[order[2 if order[0] == 0 else 1]]
+            err = 2 * (D + 8) * 2.0 ** -24 * float((np.abs(k) @ np.abs(q[t, h].double().cpu().numpy())).max()) * D ** -0.5
+            if best - second <= 40 + err:
+                continue  # another token may be as large once rounded
+            y = (v[0] + v[1]) / 2 if order[0] in (0, 1) else v[order[0]]
+            assert np.all(np.abs(o[t, h] - y) <= 2.0 ** -7 * np.abs(y) + 2.0 ** -7 * 2.0 ** -8), (t, h)
