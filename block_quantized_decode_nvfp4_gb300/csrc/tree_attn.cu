@@ -157,6 +157,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// What is taken from a row's scores: its maximum, for E4M3 less p's shift. Where
+// the difference rounds to less than that (maxima from 2^25 on, whose scores
+// are further apart than it rounds), the maximum alone: p must stay within f16.
+template <bool F8>
+__device__ __forceinline__ float shifted(float m)
+{
+    if (m == -INFINITY) m = 0.f;
+    const float x = m - (F8 ? kAttnPShift : 0.f);
+    return F8 && m - x > kAttnPShift ? m : x;
+}
+
 // Byte offset of 16-byte chunk `ch` of token row `row` in a block. The chunk
 // index is permuted by the row so that the reads of a phase fall into
 // different banks: ldmatrix takes one chunk of 8 rows; the E4M3 reads take
@@ -417,8 +428,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, RG, F8>::kCtas) tree_attn_k
                 m0 = n0;
                 m1 = n1;
             }
-            const float sub0 = (m0 == -INFINITY ? 0.f : m0) - (F8 ? kAttnPShift : 0.f);
-            const float sub1 = (m1 == -INFINITY ? 0.f : m1) - (F8 ? kAttnPShift : 0.f);
+            const float sub0 = shifted<F8>(m0), sub1 = shifted<F8>(m1);
             uint32_t pa[NB][4];
 #pragma unroll
             for (int nt = 0; nt < 2 * NB; ++nt) {

@@ -299,7 +299,8 @@ def test_masks_of_several_words(ctx, D, page):
 
 
 @pytest.mark.parametrize("gain", [1e4, 1e7, 1e9, 3e10, 1e20])
-@pytest.mark.parametrize("kind,D,n", [("bf16", 64, 2), ("bf16", 128, 10), ("bf16", 128, 40), ("bf16", 256, 10)])
+@pytest.mark.parametrize("kind,D,n", [("bf16", 64, 2), ("bf16", 128, 10), ("bf16", 128, 40), ("bf16", 256, 10),
+                                      ("e4m3", 128, 2), ("e4m3", 128, 40)])
 def test_scores_of_any_size(kind, D, n, gain):
     # scores far apart: each token's largest takes all, whatever the scores' size; the second token is a copy of the first
     ctx, Hq, Hkv, page = [300], 8, 2, 16
