@@ -544,6 +544,7 @@ __global__ void __launch_bounds__((WARPS + 1) * kWarp, CTAS) logprobs_kernel(con
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[st]);
     }
+    if (!ok) let_copies_land();
     if (warp == 0) {  // the list holds 32 at most
         const int tails = s.tails;
         if (lane < tails) list[have + lane] = s.tail[lane];

@@ -82,6 +82,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
     return __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
 }
 
+// For a thread whose wait ran out: time (2^27 cycles, 70 ms) for the block's
+// copies and products in flight to land before the block ends and its shared
+// and tensor memory are another's.
+__device__ __forceinline__ void let_copies_land()
+{
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 27)) {
+    }
+}
+
 // 1-D bulk copy global -> shared of `bytes` (multiple of 16, both addresses
 // 16-byte aligned); completion is counted on `bar` as transaction bytes.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar)

@@ -563,11 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             advance(n, steps0, steps1);
             __syncthreads();  // all have read g and their own of the item
         }
-        if ((warp == 0 || warp == 3) && !ok) {  // a wait ran out: time for the copies in flight to land before the block ends
-            const long long t0 = clock64();
-            while (clock64() - t0 < (1ll << 27)) {
-            }
-        }
+        if (!ok) let_copies_land();
         __syncthreads();
         if (warp == 1) {
             tc_fence_after();
@@ -821,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             advance(n, steps0, steps1);
             __syncthreads();
         }
+        if (!ok) let_copies_land();
         __syncthreads();
     }
 }
