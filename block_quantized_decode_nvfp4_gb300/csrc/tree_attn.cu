@@ -158,14 +158,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 }
 
 // What is taken from a row's scores: its maximum, for E4M3 less p's shift. Where
-// the difference rounds to less than that (maxima from 2^25 on, whose scores
+// that difference rounds to 2 less or more (maxima from 2^25 on, whose scores
 // are further apart than it rounds), the maximum alone: p must stay within f16.
 template <bool F8>
 __device__ __forceinline__ float shifted(float m)
 {
     if (m == -INFINITY) m = 0.f;
     const float x = m - (F8 ? kAttnPShift : 0.f);
-    return F8 && m - x > kAttnPShift ? m : x;
+    return F8 && m - x > kAttnPShift + 1.f ? m : x;
 }
 
 // Byte offset of 16-byte chunk `ch` of token row `row` in a block. The chunk

@@ -325,3 +325,15 @@ def test_scores_of_any_size(kind, D, n, gain):
                 continue  # another token may be as large once rounded
             y = (v[0] + v[1]) / 2 if order[0] in (0, 1) else v[order[0]]
             assert np.all(np.abs(o[t, h] - y) <= 2.0 ** -7 * np.abs(y) + 2.0 ** -7 * 2.0 ** -8), (t, h)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_sums_of_one_seen_token(kind, n):
+    # lse is the one score itself: what p is shifted or scaled by leaves no trace, whatever the score's size
+    for seed, gain in enumerate([0.01, 0.1, 1.0, 3.0, 10.0, 100.0]):
+        case([1], [n], 64, 1, 64, kind, tree=False, seed=seed, gain=gain, rows={0, n - 1})
+        cache, q, table, off, _, scale, _, _ = case([1], [n], 64, 1, 64, kind, seed=seed + 50, gain=gain, rows={0})
+        mask = np.zeros((n, 1), np.uint64)
+        out, lse = run_attention(cache, q, table, [1], off, mask, scale)
+        check_attention(cache, q, table, [1], off, mask, scale, out, lse, None, f"{gain}")
