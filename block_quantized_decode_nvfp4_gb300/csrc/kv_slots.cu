@@ -12,7 +12,7 @@
 // share of the tokens, found by a search of the chunk's sums, and its own
 // share of the requests' new pages. Pages of new blocks are taken from the
 // list and not from the table, which another CTA may be writing. 8 requests of
-// one token take 3.5 us, 1024 requests with 49 thousand new tokens 5.1 us (an
+// one token take 3.4 us, 1024 requests with 49 thousand new tokens 5.1 us (an
 // empty launch in the same graph: 2 us).
 #include <cuda_runtime.h>
 

@@ -16,9 +16,9 @@
 // two elements an instruction. Weights and angles come from L1 at every step,
 // which leaves the registers to loads in flight: two steps of bf16 or one of
 // fp32 ahead of the work, 2 KiB a warp and 64 KiB an SM. 8191 bf16 tokens of
-// 16 + 2 x 2 heads of 256 take 33.9 us, 168 MB at 5.0 TB/s (54 % of the issue
+// 16 + 2 x 2 heads of 256 take 33.8 us, 168 MB at 5.0 TB/s (54 % of the issue
 // slots, 41 % of the warps: the loads' latency and the instructions share the
-// rest); one token 2.6 us, 128 tokens 4.0 us.
+// rest); one token 2.4 us, 128 tokens over an E4M3 cache 4.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t e4m3x4(uint64_t u, uint64_t v)
 // between codes: one step from its remainder (Markstein 1990) makes it the
 // quotient, rounded once. Where that leaves fp32's range (infinities, products
 // past it, scales beyond 2^+-60: inv is NaN) the codes are NaN, and are made
-// again by division. By division alone 8191 bf16 tokens of 8 + 2 x 8 heads took
-// 23.8 us.
+// again by division. 8191 bf16 tokens of 8 + 2 x 8 heads: 21.7 us, by division
+// alone 23.8, by the product alone 20.7.
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const uint64_t (&y)[kRun / 2], float scale, float inv)
 {
     const uint64_t i2 = pack(inv, inv), s2 = pack(-scale, -scale);
@@ -268,7 +268,7 @@ void launch(const QkRopeArgs& a, cudaStream_t s)
 {
     // Heads per warp: one step's (512 / D), doubled while the warps still fill
     // the GPU once. Longer runs start fewer warps, each with the latency of its
-    // first loads: 8191 tokens of 20 heads 33.5 us, against 36.0 where they fill
+    // first loads: 8191 tokens of 20 heads 33.8 us, against 36.0 where they fill
     // it four times and 44.1 at one step a warp.
     const int heads = a.Hq + 2 * a.cache.heads;
     int run = 512 / D;

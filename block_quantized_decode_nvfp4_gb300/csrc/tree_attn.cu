@@ -24,29 +24,35 @@
 //
 // A CTA's four warps are 4 / RG token groups of RG warps, a warp per 16 rows.
 // A token group streams blocks of 32 tokens (16 where two stages of 32 do not
-// fit) through a shared-memory ring of its own (cp.async, 16 bytes a lane, waited for by the group alone: no
-// barrier of the whole CTA in the loop) and holds its own (m, z, o) in
-// registers; the groups join at the end of an item. Products run on
-// mma.sync m16n8k16: scores from q (A, as fragments in shared memory, a 16-byte read each: in
-// registers they left too few for three CTAs) and keys (B), then the
-// probabilities, rounded, are the A operand as they lie in the score
-// accumulators, and the values B.
+// fit) through a shared-memory ring of its own (cp.async, 16 bytes a lane,
+// waited for by the group alone: no barrier of the whole CTA in the loop) and
+// holds its own (m, z, o) in registers; the groups join at the end of an item.
+// Products run on mma.sync m16n8k16: scores from q (A, as fragments in shared
+// memory, a 16-byte read each: in registers they left too few for three CTAs)
+// and keys (B), then the probabilities, rounded, are the A operand as they lie
+// in the score accumulators, and the values B.
 //  - bf16 cache: B operands by ldmatrix (transposed for the values); p is
-//    rounded to bf16, its relative 2^-9 averages over the tokens.
+//    rounded to bf16, by up to 2^-8 of itself, which averages over the tokens.
 //  - E4M3 cache: codes become f16 (exact) after the shared-memory read, which
 //    takes 16 bytes of a token at a time: the order of the d along k, and of
 //    the output columns along n, is permuted to fit. q enters as f16 times a
 //    power of two per row that brings the row's largest element to 2^14
 //    (what that drops is below 2^-38 of it); p is scaled by 2^12 before its
-//    rounding to f16, so that p down to 2^-26 keeps 11 bits.
+//    rounding to f16, so that p down to 2^-26 keeps 11 bits (what is smaller
+//    keeps steps of 2^-36).
 //
 // Measured (8 kv heads, D = 128; 32 query heads over bf16, 64 over E4M3):
-//  - 16 requests of 8 drafts over 8192 tokens, bf16: 75.6 us for 395 MB, 5.2
+//  - 16 requests of 8 drafts over 8192 tokens, bf16: 77 us for 395 MB, 5.1
 //    TB/s; the slope over longer contexts is 6.9 TB/s, the rest is start, the
-//    spread of the CTAs' ends (56 to 71 us) and the join;
-//  - 64 decodes over 8192 tokens, E4M3: 138 us, 5.8 TB/s, and in between the
-//    conversions' latency (16 tokens a step: 156 us);
+//    spread of the CTAs' ends (56 to 71 us) and the join; over E4M3 73.5 us, half
+//    the bytes: both row groups convert every code for themselves;
+//  - 64 decodes over 8192 tokens, E4M3: 138 to 151 us from process to process,
+//    5.3 to 5.8 TB/s, and in between the conversions' latency (16 tokens a step: 156 us);
 //  - one decode over 1024 tokens: 8.9 us, two launches and one chain of loads.
+//  - Many rows over E4M3, or at D = 256, come here too, in tiles of 32 that
+//    each read and convert the cache: four trees of 64 drafts (64 query heads)
+//    over 8192 tokens, E4M3, take 198 us where bf16 in tensor memory takes 66;
+//    with 32 query heads on 4 of D = 256, bf16, 209 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

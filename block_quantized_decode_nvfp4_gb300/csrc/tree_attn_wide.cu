@@ -20,11 +20,11 @@
 // memory and v MN-major, a block's o before the next block's s. The slots take
 // turns block by block (left to themselves they fall into step, and both
 // softmaxes run while the tensor cores wait); an issuing thread keeps pace with
-// the tensor cores, so it does its waiting while the other issues. Warps 4..7 and 8..11 are the slots' softmax, a
-// row per thread (tensor-memory lane): they read s, write p in bf16 over the
-// columns of s that they have read, and rescale o in tensor memory only when
-// a row's maximum has grown by more than 2^8 (p then stays below 2^8, and
-// nothing is lost: fp32 sums, bf16's range).
+// the tensor cores, so it does its waiting while the other issues. Warps 4..7
+// and 8..11 are the slots' softmax, a row per thread (tensor-memory lane): they
+// read s, write p in bf16 over the columns of s that they have read, and rescale
+// o in tensor memory only when a row's maximum has grown by more than 2^8 (p
+// then stays below 2^8, and nothing is lost: fp32 sums, bf16's range).
 //
 // Four trees of 64 tokens over 32768 (64 query heads on 8, D = 128): 191 us,
 // 1.12 PFLOP/s of products. A block of both slots takes about 3000 cycles, 2670

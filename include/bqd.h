@@ -613,8 +613,10 @@ bqd_status paged_slots(const int32_t* context_lens, const int32_t* new_lens, con
  *      outside [0, max_pos) is not stored and its q_out row is zero
  *      (with rot_dim 0 positions are not read and may be NULL).
  *   q_out: bf16 [T][Hq][D].
- * All arithmetic is fp32, rounded once (to nearest even) where it is stored.
- * Two tokens of one call must not share a slot. Hq >= 1, T >= 0.
+ * All arithmetic is fp32, rounded once (to nearest even) where it is stored
+ * (over BQD_E4M3 caches the quotient by the scale).
+ * Two tokens of one call must not share a slot. Hq 1 .. 65535, pitches and
+ * T >= 0 below 2^31, max_pos 0 .. 2^31.
  */
 enum { BQD_ROPE_HALVES = 0, BQD_ROPE_PAIRS = 1 };
 bqd_status qk_norm_rope_cache(const void* q, const void* k, const void* v, int in_type, int64_t q_pitch,
@@ -645,9 +647,15 @@ bqd_status qk_norm_rope_cache(const void* q, const void* k, const void* v, int i
  *      tokens that belong to no request are not written.
  *   workspace: tree_attention_workspace_bytes(...) bytes, 16-byte aligned.
  * Scores, softmax and sums are fp32; the probabilities enter the product
- * with V as bf16 (relative error 2^-9 each), over BQD_E4M3 caches as f16
- * (2^-12 each). Hq a multiple of cache->heads, Hq / heads <= 64; R * heads <
- * 2^24, T * Hq < 2^31.
+ * with V as bf16 (relative error up to 2^-8 each), over BQD_E4M3 caches as
+ * f16 (up to 2^-11 each, and below 2^-26 of the row's largest in steps of
+ * 2^-36 of it). Hq a multiple of cache->heads, Hq / heads <= 64; R * heads <
+ * 2^24, T * Hq < 2^31, q_pitch < 2^31, mask_words 1 .. 2^20, R * table_width
+ * < 2^40.
+ * Speed: more than 32 rows (new tokens times Hq / heads, the call's mean over
+ * its requests) over a BQD_BF16 cache of head_dim 64 or 128 and pages of 8
+ * tokens or more read keys and values once per 128 or 256 rows, any other
+ * call once per 16 or 32.
  */
 bqd_status tree_attention(const uint16_t* q, int64_t q_pitch, const bqd_kv_cache* cache, const int32_t* block_table,
                           int64_t table_width, const int32_t* context_lens, const int32_t* token_offsets,
@@ -669,7 +677,8 @@ size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int
  *   top_ids, top_logprobs [T][topk]: the topk largest logits in descending
  *      order, equal values by ascending index (-0 equals +0), with their log
  *      probabilities.
- * logits: BQD_F32 or BQD_BF16 [T][V], row pitch in elements (any >= V).
+ * logits: BQD_F32 or BQD_BF16 [T][V], row pitch in elements (any >= V below
+ * 2^31: the first row starts on 16 bytes, the others anywhere).
  * Logits of -inf have probability 0. A row that is -inf throughout has
  * log probability -inf everywhere and entropy 0. A NaN or +inf in a row
  * makes its log probabilities and entropy NaN; among the alternatives NaN
