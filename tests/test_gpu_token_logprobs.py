@@ -261,7 +261,7 @@ def test_coarse_rows_of_any_end(dtype, V, T):
 
 def check_masked(x, tok, k):
     """Rows of a few distinct values whose gaps are 0 or more than 1000: the entropy is that of the largest's copies,
-    good to 2^-12 (1 + entropy) and the shift that the maximum's product with log2(e) leaves, at most 64, times 2^-13."""
+    good to 2^-12 (1 + entropy) and 2^-13 of the shift that the maximum's product with log2(e) leaves, at most 64."""
     rows = [0, 1, 2, 3, 4, x.shape[0] - 1]
     _, ent, _, _ = check(x, tok, k, rows=rows)
     for t in rows:
@@ -275,7 +275,7 @@ def check_masked(x, tok, k):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [5, 200])
 def test_rows_masked_by_a_large_value(low, dtype, T):
-    # what a mask other than -inf or the type's lowest value leaves: all of a row hidden, one logit, a few, the first half
+    # what a mask other than -inf or the type's lowest value leaves: all of a row hidden, one logit, a few, a half
     V = 40007
     x = torch.full((T, V), low)
     x[1, 39999] = 2.0

@@ -302,7 +302,7 @@ def test_masks_of_several_words(ctx, D, page):
 @pytest.mark.parametrize("kind,D,n", [("bf16", 64, 2), ("bf16", 128, 10), ("bf16", 128, 40), ("bf16", 256, 10),
                                       ("e4m3", 128, 2), ("e4m3", 128, 40)])
 def test_scores_of_any_size(kind, D, n, gain):
-    # scores far apart: each token's largest takes all, whatever the scores' size; the second token is a copy of the first
+    # scores far apart: each token's largest takes all, whatever the scores' size (two keys are equal)
     ctx, Hq, Hkv, page = [300], 8, 2, 16
     cache = Cache(40, page, Hkv, D, kind, seed=3)
     table = table_for([ctx[0] + n], page, 40, 3)
@@ -320,7 +320,8 @@ def test_scores_of_any_size(kind, D, n, gain):
             s = (k @ q[t, h].double().cpu().numpy()) * D ** -0.5
             order = np.argsort(-s, kind="stable")
             best, second = s[order[0]], s[order[2 if order[0] == 0 else 1]]
-            err = 2 * (D + 8) * 2.0 ** -24 * float((np.abs(k) @ np.abs(q[t, h].double().cpu().numpy())).max()) * D ** -0.5
+            size = float((np.abs(k) @ np.abs(q[t, h].double().cpu().numpy())).max()) * D ** -0.5
+            err = 2 * (D + 8) * 2.0 ** -24 * size
             if best - second <= 40 + err:
                 continue  # another token may be as large once rounded
             y = (v[0] + v[1]) / 2 if order[0] in (0, 1) else v[order[0]]
