@@ -681,9 +681,9 @@ size_t tree_attention_workspace_bytes(int64_t R, int64_t T, int Hq, int Hkv, int
  * 2^31: the first row starts on 16 bytes, the others anywhere).
  * Logits of -inf have probability 0. A row that is -inf throughout has
  * log probability -inf everywhere and entropy 0. A NaN or +inf in a row
- * makes its log probabilities and entropy NaN; among the alternatives NaN
- * ranks below -inf. tokens with logprob, entropy, and top_ids with
- * top_logprobs may be NULL; topk 0 .. 32, at most V.
+ * makes its log probabilities and entropy NaN (a token outside [0, V) stays
+ * -inf); among the alternatives NaN ranks below -inf. tokens with logprob,
+ * entropy, and top_ids with top_logprobs may be NULL; topk 0 .. 32, at most V.
  * workspace: token_logprobs_workspace_bytes(T, V, topk) bytes (a few today:
  * rows are joined on chip), 16-byte aligned. T >= 0, 1 <= V < 2^31.
  */

@@ -113,7 +113,7 @@ def logprobs(x, token, topk):
     order = sorted(range(x.size), key=lambda i: (bool(np.isnan(x[i])), -key[i], i))[:topk]
     if np.isnan(d).any() or np.isposinf(d).any():
         nan = float("nan")
-        return nan, nan, order, np.full(topk, nan)
+        return nan if 0 <= token < x.size else NEG, nan, order, np.full(topk, nan)
     m = d.max()
     if m == NEG:
         return NEG, 0.0, order, np.full(topk, NEG)

@@ -285,3 +285,11 @@ def test_rows_masked_by_a_large_value(low, dtype, T):
     x = (x if dtype == "f32" else x.to(torch.bfloat16)).cuda()
     tok = [3, 39999, 102, V - 1, 7] + [0] * (T - 5)
     check_masked(x, tok, 8)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_tokens_outside_the_vocabulary_of_a_row_without_an_answer(bad):
+    x = logits(3, 1000, "f32", 14)
+    x[:, 500] = bad
+    lp, *_ = check(x, [-1, 1000, 7], 3)
+    assert np.isneginf(lp[:2]).all() and np.isnan(lp[2])

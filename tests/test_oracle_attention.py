@@ -80,3 +80,8 @@ def test_logprobs_worked_example():
     assert ref.logprobs(np.full(3, -np.inf), 0, 2)[:3] == (-np.inf, 0.0, [0, 1])
     assert ref.logprobs(np.array([1.0, np.nan, np.inf, -np.inf]), 0, 4)[2] == [2, 0, 3, 1]
     assert ref.logprobs(x, 9, 0)[0] == -np.inf
+
+
+def test_logprobs_of_a_token_outside_the_vocabulary():
+    for x in ([0.0, 1.0], [0.0, np.nan], [0.0, np.inf], [-np.inf, -np.inf]):
+        assert ref.logprobs(x, 2, 0)[0] == ref.logprobs(x, -1, 0)[0] == -np.inf
