@@ -99,6 +99,11 @@ SIGNATURES = {
     "tree_attention_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32, _i32]),
     "token_logprobs": (_i32, [_vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _i64, _i64, _vp]),
     "token_logprobs_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "fp8_x_encode": (_i32, [_vp, _i32, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "residual_norm": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i64, _f32, _vp, _vp, _i32, _vp, _f32, _vp, _i32, _vp,
+                             _i64, _i64, _vp]),
+    "fp8_b128_gemm": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp]),
+    "fp8_b128_gemm_silu_mul": (_i32, [_vp] * 7 + [_i32, _vp, _i64, _i64, _i64, _vp]),
 }
 
 
@@ -400,3 +405,50 @@ def token_logprobs(logits, in_type, pitch, tokens, logprob, entropy, top_ids, to
 
 def token_logprobs_workspace_bytes(T, V, topk) -> int:
     return lib().token_logprobs_workspace_bytes(T, V, topk)
+
+
+def _here(where, *tensors):
+    """Addresses of a call's tensors (None and integers as they are), all of the current device."""
+    import torch
+    dev, out = None, []
+    for a in tensors:
+        if a is None or isinstance(a, int):
+            out.append(a)
+            continue
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if a.get_device() != dev:
+            raise ValueError(f"{where}: a tensor on {a.device}, the current device is cuda:{dev}")
+        out.append(a.data_ptr())
+    return out
+
+
+def fp8_x_encode(x, x_type, x_pitch, codes, scales, K, T, stream=None):
+    """8-bit activations of rows [T][K]: E4M3 codes [T][K], fp32 scales [ceil(K/128)][T]."""
+    x, codes, scales = _here("fp8_x_encode", x, codes, scales)
+    _check(lib().fp8_x_encode(x, x_type, x_pitch, codes, scales, K, T, _stream(stream)), "fp8_x_encode")
+
+
+def residual_norm(x, x_type, x_pitch, post_weight, gate, gate_type, gate_pitch, residual_scale, residual, residual_out,
+                  residual_type, pre_weight, eps, y, y_type, y_scales, H, T, stream=None):
+    """Residual add of a block's output (its norm, gate and scale), then the next block's norm: y bf16 or E4M3."""
+    x, post_weight, gate, residual, residual_out, pre_weight, y, y_scales = _here(
+        "residual_norm", x, post_weight, gate, residual, residual_out, pre_weight, y, y_scales)
+    _check(lib().residual_norm(x, x_type, x_pitch, post_weight, gate, gate_type, gate_pitch, residual_scale, residual,
+                               residual_out, residual_type, pre_weight, eps, y, y_type, y_scales, H, T,
+                               _stream(stream)), "residual_norm")
+
+
+def fp8_b128_gemm(codes, scales, x, x_scales, y, y_type, M, K, T, stream=None):
+    """8-bit activations [T][K] times FP8 block-128 weights [M][K]: y [T][M], fp32 or bf16."""
+    codes, scales, x, x_scales, y = _here("fp8_b128_gemm", codes, scales, x, x_scales, y)
+    _check(lib().fp8_b128_gemm(codes, scales, x, x_scales, y, y_type, M, K, T, _stream(stream)), "fp8_b128_gemm")
+
+
+def fp8_b128_gemm_silu_mul(gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_type, h_scales, I, K, T,
+                           stream=None):
+    """SiLU(gate) * up of 8-bit activations in one kernel: h [T][I], fp32, bf16 or E4M3 with scales."""
+    gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_scales = _here(
+        "fp8_b128_gemm_silu_mul", gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_scales)
+    _check(lib().fp8_b128_gemm_silu_mul(gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_type, h_scales,
+                                        I, K, T, _stream(stream)), "fp8_b128_gemm_silu_mul")

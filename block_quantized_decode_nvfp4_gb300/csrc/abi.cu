@@ -8,6 +8,7 @@
 
 #include "attn.h"
 #include "bqd.h"
+#include "fp8.h"
 #include "gemm.h"
 #include "gemv.h"
 #include "host_util.h"
@@ -386,14 +387,14 @@ bqd_status bqd_device_error(unsigned int* bits_out)
     if (!bits_out) return BQD_ERR_NULL;
     bqd_status st = check_arch();
     if (st != BQD_OK) return st;
-    unsigned int v = 0, w = 0, m = 0, n = 0, g = 0, l = 0, t = 0;
+    unsigned int v = 0, w = 0, m = 0, n = 0, g = 0, l = 0, t = 0, f = 0;
     if (bqd::read_and_clear_stream_error(&v) != cudaSuccess || bqd::read_and_clear_mma_error(&w) != cudaSuccess ||
         bqd::read_and_clear_moe_stream_error(&m) != cudaSuccess ||
         bqd::read_and_clear_moe_small_error(&n) != cudaSuccess ||
         bqd::read_and_clear_gemm_error(&g) != cudaSuccess || bqd::read_and_clear_logprobs_error(&l) != cudaSuccess ||
-        bqd::read_and_clear_attn_error(&t) != cudaSuccess)
+        bqd::read_and_clear_attn_error(&t) != cudaSuccess || bqd::read_and_clear_fp8_error(&f) != cudaSuccess)
         return BQD_ERR_LAUNCH;
-    v |= w | m | n | g | l | t;
+    v |= w | m | n | g | l | t | f;
     *bits_out = v;
     return v ? BQD_ERR_DEVICE : BQD_OK;
 }
@@ -751,6 +752,141 @@ bqd_status token_logprobs(const void* logits, int in_type, int64_t pitch, const 
     a.V = static_cast<int>(V);
     a.topk = topk;
     return from_cuda(bqd::launch_token_logprobs(a, in_type, stream));
+}
+
+// ---------------------------------------------------------------- 8-bit activations
+static bool row_type(int t) { return t == BQD_F32 || t == BQD_BF16; }
+static int64_t row_vec(int t) { return t == BQD_F32 ? 4 : 8; }  // elements in 16 bytes
+
+bqd_status fp8_x_encode(const void* x, int x_type, int64_t x_pitch, uint8_t* codes, float* scales, int64_t K, int64_t T,
+                        cudaStream_t stream)
+{
+    if (!row_type(x_type) || K < 0 || K > (int64_t(1) << 24) || K % 16 != 0 || T < 0 || T > (int64_t(1) << 30))
+        return BQD_ERR_SHAPE;
+    if (x_pitch < K || x_pitch >= (int64_t(1) << 31) || x_pitch % row_vec(x_type) != 0) return BQD_ERR_SHAPE;
+    if (T > 0 && K > (int64_t(1) << 40) / T) return BQD_ERR_SHAPE;
+    if (K == 0 || T == 0) return BQD_OK;
+    if (!x || !codes || !scales) return BQD_ERR_NULL;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return BQD_ERR_ALIGN;
+    bqd_status st = check_arch();
+    if (st != BQD_OK) return st;
+    bqd::EncodeXArgs a{};
+    a.x = x;
+    a.pitch = x_pitch;
+    a.codes = codes;
+    a.scales = scales;
+    a.K = K;
+    a.T = T;
+    return from_cuda(bqd::launch_fp8_x_encode(a, x_type, stream));
+}
+
+bqd_status residual_norm(const void* x, int x_type, int64_t x_pitch, const float* post_weight, const void* gate,
+                         int gate_type, int64_t gate_pitch, float residual_scale, const void* residual,
+                         void* residual_out, int residual_type, const float* pre_weight, float eps, void* y, int y_type,
+                         float* y_scales, int64_t H, int64_t T, cudaStream_t stream)
+{
+    if (H < 16 || H > bqd::kNormMaxH || H % 16 != 0 || T < 0 || T > (int64_t(1) << 30)) return BQD_ERR_SHAPE;
+    if (!row_type(residual_type) || !(eps >= 0.f)) return BQD_ERR_SHAPE;
+    if (x && (!row_type(x_type) || x_pitch < H || x_pitch >= (int64_t(1) << 31) || x_pitch % row_vec(x_type) != 0))
+        return BQD_ERR_SHAPE;
+    if (gate && (!row_type(gate_type) || (gate_pitch != 0 && gate_pitch < H) || gate_pitch >= (int64_t(1) << 31) ||
+                 gate_pitch % row_vec(gate_type) != 0))
+        return BQD_ERR_SHAPE;
+    if (y && y_type != BQD_BF16 && y_type != BQD_E4M3) return BQD_ERR_SHAPE;
+    if (T == 0) return BQD_OK;
+    if (!x && !residual) return BQD_ERR_NULL;
+    if (!x && (post_weight || gate)) return BQD_ERR_NULL;
+    if (!y && !residual_out) return BQD_ERR_NULL;
+    if (y && (!pre_weight || (y_type == BQD_E4M3 && !y_scales))) return BQD_ERR_NULL;
+    for (const void* p : {x, static_cast<const void*>(post_weight), gate, residual, static_cast<const void*>(residual_out),
+                          static_cast<const void*>(pre_weight), static_cast<const void*>(y),
+                          static_cast<const void*>(y_scales)})
+        if (!aligned16(p)) return BQD_ERR_ALIGN;
+    bqd_status st = check_arch();
+    if (st != BQD_OK) return st;
+    bqd::NormArgs a{};
+    a.x = x;
+    a.gate = gate;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.y = y;
+    a.post_weight = post_weight;
+    a.pre_weight = pre_weight;
+    a.y_scales = y_scales;
+    a.x_pitch = x_pitch;
+    a.gate_pitch = gate_pitch;
+    a.T = T;
+    a.scale = residual_scale;
+    a.eps = eps;
+    a.H = static_cast<int>(H);
+    a.x_f32 = x_type == BQD_F32;
+    a.gate_f32 = gate_type == BQD_F32;
+    a.res_f32 = residual_type == BQD_F32;
+    a.y_e4m3 = y_type == BQD_E4M3;
+    return from_cuda(bqd::launch_residual_norm(a, stream));
+}
+
+// The sizes of a product with 8-bit activations.
+static bool fp8_sizes_ok(int64_t M, int64_t K, int64_t T)
+{
+    if (M < 0 || K < 0 || T < 0 || K % 16 != 0) return false;
+    return M == 0 || K == 0 || T == 0 || bqd::fp8_gemm_supported(M, K, T);
+}
+
+bqd_status fp8_b128_gemm(const uint8_t* codes, const float* scales, const uint8_t* x, const float* x_scales, void* y,
+                         int y_type, int64_t M, int64_t K, int64_t T, cudaStream_t stream)
+{
+    if (!row_type(y_type) || !fp8_sizes_ok(M, K, T)) return BQD_ERR_SHAPE;
+    if (M == 0 || K == 0 || T == 0) return M == 0 || T == 0 ? BQD_OK : BQD_ERR_SHAPE;
+    if (!codes || !scales || !x || !x_scales || !y) return BQD_ERR_NULL;
+    for (const void* p : {static_cast<const void*>(codes), static_cast<const void*>(scales), static_cast<const void*>(x),
+                          static_cast<const void*>(x_scales), static_cast<const void*>(y)})
+        if (!aligned16(p)) return BQD_ERR_ALIGN;
+    bqd_status st = check_arch();
+    if (st != BQD_OK) return st;
+    bqd::Fp8GemmArgs a{};
+    a.w0 = codes;
+    a.s0 = scales;
+    a.x = x;
+    a.xs = x_scales;
+    a.y = y;
+    a.M = M;
+    a.K = K;
+    a.T = T;
+    a.y_type = y_type;
+    return from_cuda(bqd::launch_fp8_gemm(a, false, stream));
+}
+
+bqd_status fp8_b128_gemm_silu_mul(const uint8_t* gate_codes, const float* gate_scales, const uint8_t* up_codes,
+                                  const float* up_scales, const uint8_t* x, const float* x_scales, void* h, int h_type,
+                                  float* h_scales, int64_t I, int64_t K, int64_t T, cudaStream_t stream)
+{
+    if ((!row_type(h_type) && h_type != BQD_E4M3) || !fp8_sizes_ok(I, K, T)) return BQD_ERR_SHAPE;
+    if (I == 0 || K == 0 || T == 0) return I == 0 || T == 0 ? BQD_OK : BQD_ERR_SHAPE;
+    if (!gate_codes || !gate_scales || !up_codes || !up_scales || !x || !x_scales || !h ||
+        (h_type == BQD_E4M3 && !h_scales))
+        return BQD_ERR_NULL;
+    for (const void* p : {static_cast<const void*>(gate_codes), static_cast<const void*>(up_codes),
+                          static_cast<const void*>(x), static_cast<const void*>(x_scales), static_cast<const void*>(h),
+                          static_cast<const void*>(h_scales)})
+        if (!aligned16(p)) return BQD_ERR_ALIGN;
+    if (!elem_aligned(gate_scales) || !elem_aligned(up_scales)) return BQD_ERR_ALIGN;
+    bqd_status st = check_arch();
+    if (st != BQD_OK) return st;
+    bqd::Fp8GemmArgs a{};
+    a.w0 = gate_codes;
+    a.s0 = gate_scales;
+    a.w1 = up_codes;
+    a.s1 = up_scales;
+    a.x = x;
+    a.xs = x_scales;
+    a.y = h;
+    a.ys = h_scales;
+    a.M = I;
+    a.K = K;
+    a.T = T;
+    a.y_type = h_type;
+    return from_cuda(bqd::launch_fp8_gemm(a, true, stream));
 }
 
 }  // extern "C"

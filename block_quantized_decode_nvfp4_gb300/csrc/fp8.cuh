@@ -1,0 +1,150 @@
+// fp8.cuh -- device helpers of the calls on 8-bit activations: E4M3 codes with
+// a scale for each block of 128, and the PTX of the products (tensor copies,
+// tcgen05 kind::f8f6f4, tensor memory, clusters).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "f32x2.cuh"
+#include "stream.cuh"
+
+namespace bqd {
+
+// ---------------------------------------------------------------- E4M3 blocks
+// Bits of |x|: their integer order is that of the values, with infinities and
+// then NaN above them, so the largest of a block also tells these.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// The scale of a block whose largest magnitude has these bits: amax / 448,
+// rounded once and at least the smallest normal fp32, so that no quotient
+// passes 448 by more than its rounding; NaN where the block has a NaN or an
+// infinity.
+__device__ __forceinline__ float block_scale(uint32_t amax)
+{
+    if (amax >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    return fmaxf(__fdiv_rn(__uint_as_float(amax), 448.f), 1.17549435e-38f);
+}
+
+// Codes of quotients by one scale, each the fp32 quotient rounded to E4M3. A
+// product with the rounded reciprocal alone would now and then land on the
+// other side of a boundary between codes: one step from its remainder
+// (Markstein 1990) makes it the quotient, rounded once, as long as the
+// remainder keeps its bits (scales from 2^-60); smaller scales divide.
+struct BlockCoder {
+    float s, inv;
+    __device__ __forceinline__ explicit BlockCoder(float scale) : s(scale)
+    {
+        asm("rcp.rn.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+    }
+    __device__ __forceinline__ uint32_t pair(uint64_t v) const  // code of the first in the low byte
+    {
+        float a, b;
+        if (s < 8.6736174e-19f) {  // 2^-60; false for NaN
+            unpack(v, a, b);
+            a = __fdiv_rn(a, s);
+            b = __fdiv_rn(b, s);
+        } else {
+            const uint64_t i2 = pack(inv, inv), q = mul2(v, i2);
+            unpack(fma2(fma2(q, pack(-s, -s), v), i2, q), a, b);
+        }
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+        return r;
+    }
+    __device__ __forceinline__ uint32_t one(float v) const { return pair(pack(v, v)) & 0xFFu; }
+};
+
+__device__ __forceinline__ uint32_t to_bf16x2(float x, float y)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// ---------------------------------------------------------------- tensor cores
+__device__ __forceinline__ void fp8_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void fp8_pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Shared-memory descriptor of a K-major operand with the 128-byte swizzle: rows
+// of 128 bytes (128 k) in atoms of 8 rows, 1024 bytes apart; an MMA's 32 k are
+// 32 bytes further into the row.
+__device__ __forceinline__ uint64_t fp8_desc(uint32_t addr)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// Instruction descriptor: fp32 D (bit 4), A and B E4M3 (0), both K-major.
+constexpr uint32_t fp8_idesc(int M, int N)
+{
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void fp8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void fp8_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool fp8_elect()
+{
+    uint32_t pred = 0;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(pred));
+    return pred != 0;
+}
+// 16 columns of this warp's 32 lanes; several loads may share one wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cta_map(uint32_t local, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    return remote;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+}  // namespace bqd

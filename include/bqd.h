@@ -694,6 +694,86 @@ bqd_status token_logprobs(const void* logits, int in_type, int64_t pitch, const 
 /* Bytes of device workspace token_logprobs needs for these sizes (0 if a size is out of range). */
 size_t token_logprobs_workspace_bytes(int64_t T, int64_t V, int topk);
 
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit activations: one block of an FP8 checkpoint around its products. Rows
+ * become E4M3 codes with an fp32 scale for each token and each 128 channels
+ * (residual_norm, fp8_x_encode, or the gated pair itself), and meet the FP8
+ * block-128 weights on the tensor cores (fp8_b128_gemm,
+ * fp8_b128_gemm_silu_mul), for one token or thousands.
+ *   activations: codes u8 [T][K], dense; scales fp32 [ceil(K/128)][T]:
+ *      block-major, the scales of a block of all tokens side by side.
+ *      A block's scale is s = max(amax / 448, 2^-126) in fp32, a code the
+ *      fp32 quotient v / s rounded to E4M3 (to nearest even); the value is
+ *      code * s. A block with a NaN or an infinity has the scale NaN and the
+ *      codes 0x7F (NaN). The last block of a row may be shorter.
+ *   weights: as fp8_b128_gemv (codes u8 [M][K], scales fp32
+ *      [ceil(M/128)][ceil(K/128)]).
+ * Arrays of one call must not overlap, but where a call says so. None needs a
+ * workspace; all may be captured into graphs and run on any stream of the
+ * current device.
+ */
+
+/*
+ * fp8_x_encode -- activations to codes and scales, for rows that no norm
+ * precedes (attention's output).
+ *   x: BQD_F32 or BQD_BF16 [T][K], row pitch in elements (>= K, below 2^31, a
+ *      multiple of 16 bytes). K a multiple of 16 (0 .. 2^24), T 0 .. 2^30,
+ *      K * T <= 2^40.
+ */
+bqd_status fp8_x_encode(const void* x, int x_type, int64_t x_pitch, uint8_t* codes, float* scales, int64_t K, int64_t T,
+                        cudaStream_t stream);
+
+/*
+ * residual_norm -- what stands between two blocks, in one pass:
+ *   z = x, or with post_weight x * rsqrt(mean(x^2) + eps) * post_weight (the
+ *       norm after a block);
+ *   r = residual + residual_scale * gate * z (gate NULL: 1; residual NULL: 0;
+ *       x NULL: r = residual);
+ *   residual_out = r, if not NULL; may be `residual` itself;
+ *   y = r * rsqrt(mean(r^2) + eps) * pre_weight, if y is not NULL (the norm
+ *       before the next block), of the r that has not been rounded.
+ *   x, gate: BQD_F32 or BQD_BF16 [T][H], each with its row pitch in elements
+ *      (>= H, below 2^31, a multiple of 16 bytes); gate_pitch 0: one row of
+ *      gates for all tokens. residual, residual_out: residual_type BQD_F32 or
+ *      BQD_BF16, dense. post_weight, pre_weight: fp32 [H].
+ *   y: BQD_BF16 [T][H], or BQD_E4M3: codes, with y_scales [ceil(H/128)][T].
+ * All arithmetic is fp32 (so a row's sum of squares must fit in it), rounded
+ * once where it is stored. Types of absent arrays are not looked at, but for
+ * residual_type. H a multiple of 16, 16 .. 16384; T 0 .. 2^30; eps >= 0.
+ */
+bqd_status residual_norm(const void* x, int x_type, int64_t x_pitch, const float* post_weight, const void* gate,
+                         int gate_type, int64_t gate_pitch, float residual_scale, const void* residual,
+                         void* residual_out, int residual_type, const float* pre_weight, float eps, void* y, int y_type,
+                         float* y_scales, int64_t H, int64_t T, cudaStream_t stream);
+
+/*
+ * fp8_b128_gemm -- y[t][m] = sum_k x[t][k] * w[m][k], x and w the values of
+ * 8-bit activations and FP8 block-128 weights.
+ *   y: BQD_F32 or BQD_BF16 [T][M]. K a multiple of 16, 16 .. 2^24; M >= 0,
+ *      T >= 0, up to 2^30, ceil(M/128) * ceil(T/16) <= 2^30.
+ * A block's 128 products are summed by the tensor cores (fp32), the blocks,
+ * each times the product of its two scales, in fp32; rounded once where y is
+ * BQD_BF16. NaN codes and scales spoil the rows that they meet.
+ */
+bqd_status fp8_b128_gemm(const uint8_t* codes, const float* scales, const uint8_t* x, const float* x_scales, void* y,
+                         int y_type, int64_t M, int64_t K, int64_t T, cudaStream_t stream);
+
+/*
+ * fp8_b128_gemm_silu_mul -- a gated feed-forward's first half, both products
+ * in one kernel: h[t][i] = SiLU(g) * u, g = sum_k x w_gate[i], u = sum_k x
+ * w_up[i], SiLU(g) = g / (1 + e^-g), all in fp32.
+ *   gate, up: weights [I][K], each with its own scales [ceil(I/128)]
+ *      [ceil(K/128)] (a fused [2I][K] weight is the two halves, if I is a
+ *      multiple of 128: the scales may start at any fp32).
+ *   h: BQD_F32 or BQD_BF16 [T][I], or BQD_E4M3: codes, with h_scales
+ *      [ceil(I/128)][T]: the 8-bit activations of the down projection. Sizes
+ *      as fp8_b128_gemm with M = I.
+ */
+bqd_status fp8_b128_gemm_silu_mul(const uint8_t* gate_codes, const float* gate_scales, const uint8_t* up_codes,
+                                  const float* up_scales, const uint8_t* x, const float* x_scales, void* h, int h_type,
+                                  float* h_scales, int64_t I, int64_t K, int64_t T, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
