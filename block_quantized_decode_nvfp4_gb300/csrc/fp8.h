@@ -4,6 +4,7 @@
 // (abi.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -44,8 +45,14 @@ struct Fp8GemmArgs {
     int64_t M, K, T;
     int y_type;
 };
+// Codes [rows][K] in boxes of 128 k x `box` rows (a CUtensorMap); k and rows past the ends read as zero.
+bool fp8_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
+// The kernel for many tokens (fp8_gemm_pairs.cu), and whether the sizes are its.
+bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual);
+cudaError_t launch_fp8_gemm_pairs(const Fp8GemmArgs& a, bool dual, cudaStream_t s);
 bool fp8_gemm_supported(int64_t M, int64_t K, int64_t T);
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dual, cudaStream_t s);
 cudaError_t read_and_clear_fp8_error(unsigned int* out);
+cudaError_t read_and_clear_fp8_pairs_error(unsigned int* out);
 
 }  // namespace bqd

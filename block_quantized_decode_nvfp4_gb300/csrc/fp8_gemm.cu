@@ -5,17 +5,21 @@
 //
 // The tensor cores add up the 128 k of a block (E4M3 products, fp32 sums); the
 // blocks' sums meet their two scales in fp32 registers. A CTA computes 128 rows
-// of the weights (the MMA's M, one tile of scales) times BN tokens (its N):
-//  - warp 0 copies a block of 128 k at a time into a ring by 2-D tensor copies
-//    (128-byte swizzle; rows, tokens and k past the ends read as zero);
-//  - warp 1, one elected lane, issues the block's MMAs (K = 32 each) into one of
-//    a few buffers of tensor memory;
-//  - warps 2..5 read a buffer (a row of the weights per thread, BN columns),
-//    scale it and add it to their registers.
-// With few tiles the k blocks of one are shared by a cluster of CTAs, which add
-// up their parts in the order of their ranks, in one shared memory after the
-// other: the same bits every time. With many, a CTA takes tile after tile, and
-// its ring runs on from one to the next.
+// of a weight (the MMA's M, one tile of scales) times BN tokens (its N):
+//  - warps 0 and 1 copy a block of 128 k each in turn into a ring by 2-D tensor
+//    copies (128-byte swizzle; rows, tokens and k past the ends read as zero);
+//  - warps 2 and 3, one elected lane of each, issue the MMAs (K = 32 each) of
+//    every other block into one of a few buffers of tensor memory. A thread takes
+//    about 450 cycles for a block's waits and copies or products, and the blocks
+//    do not depend on one another: hence two of each;
+//  - the other warps read a buffer (a row of the weights per thread), scale it
+//    and add it to their registers.
+// With few tiles the k blocks of one are shared by a cluster of CTAs, and so are
+// the two weights of a gated pair. Each CTA then has a share of the tile's
+// tokens: the others write their parts into its shared memory, and it adds them
+// up in the order of the k blocks: the same bits every time.
+// With many tiles of one weight, a CTA takes tile after tile, and its ring runs
+// on from one to the next.
 // Every wait is bounded (kErrWaitTimeout in the kernel's error word).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -37,40 +41,49 @@ __device__ unsigned int g_fp8_error = 0;
 
 namespace {
 
-constexpr int kRows = 128;               // weight rows of a tile (MMA M), and of a tile of scales
-constexpr int kBlk = 128;                // k of a block of scales and of a ring stage
-constexpr int kTileW = kRows * kBlk;     // bytes
-constexpr int kThreads = 192;
-constexpr int kSumWarps = 4;
+constexpr int kRows = 128;             // weight rows of a tile (MMA M), and of a tile of scales
+constexpr int kBlk = 128;              // k of a block of scales and of a ring stage
+constexpr int kTileW = kRows * kBlk;   // bytes
+constexpr int kMaxCluster = 8;
 
-template <int BN, bool DUAL>
+template <int BN>
 struct Narrow {
-    static constexpr int kMats = DUAL ? 2 : 1;
+    static constexpr int kCtas = BN > 64 ? 1 : 2;  // per SM
+    static constexpr int kSumWarps = BN > 32 ? 8 : 4;
+    static constexpr int kGroups = kSumWarps / 4;  // of 128 threads, a row of the weights each
+    static constexpr int kThreads = (4 + kSumWarps) * kWarp;
     static constexpr int kTileX = BN * kBlk;
-    static constexpr int kStage = kMats * kTileW + kTileX;
-    static constexpr int kCtas = DUAL && BN == 64 ? 1 : 2;  // per SM
-    static constexpr int kRoom = kCtas == 2 ? 110 * 1024 : 220 * 1024;
-    static constexpr int kStages = (kRoom - 1024) / kStage < 8 ? (kRoom - 1024) / kStage : 8;
-    static constexpr int kSmem = kStages * kStage + 1024;  // + alignment slack
-    static constexpr int kCols = kMats * BN;               // tensor-memory columns of a buffer
-    static constexpr int kBufs = 256 / kCols < 4 ? 256 / kCols : 4;
-    static constexpr int kTmem = kBufs * kCols;
-    static constexpr int kAhead = BN == 128 ? 2 : 4;       // blocks whose scales are on their way
+    static constexpr int kStage = kTileW + kTileX;
+    static constexpr int kParts = (BN + kMaxCluster - 1) * kRows * 4;  // a cluster's parts of this CTA's tokens
+    static constexpr bool kOver = BN > 32;  // they lie over the ring: its room is worth more than a barrier
+    static constexpr int kRoom = (kCtas == 2 ? 109 * 1024 : 218 * 1024) - (kOver ? 0 : kParts);
+    static constexpr int kStages = kRoom / kStage / 2 < 4 ? kRoom / kStage / 2 * 2 : 8;  // even: each for one warp
+    static constexpr int kSmem = kStages * kStage + (kOver ? 0 : kParts) + 1024;  // + alignment slack
+    static constexpr int kBufs = 256 / BN < 4 ? 256 / BN : 4;
+    static constexpr int kTmem = kBufs * BN;
+    static constexpr int kCols = BN / kGroups;  // columns of a thread
+    static constexpr int kAhead = 4;            // blocks whose scales are on their way
     static_assert(BN % 16 == 0 && BN >= 16 && BN <= 128, "the MMA's N, and the threads' registers");
     static_assert(kTmem >= 32 && kTmem <= 256 && (kTmem & (kTmem - 1)) == 0, "two CTAs share 512 columns");
-    static_assert(kStages >= 2 && kBufs >= 2, "copies, products and sums overlap");
+    static_assert(kStages >= 2 && kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
+    static_assert(!kOver || kParts <= kStages * kStage, "the parts fit the ring");
     static_assert(kTileX % 1024 == 0, "stages start on 1024-byte boundaries (swizzle atoms)");
-    static_assert(kMats * BN * kRows * 4 <= kStages * kStage, "a cluster's parts lie over the ring");
 };
 
 struct GemmShape {
+    const float *s[2], *xs;
+    void* y;
+    float* ys;
     int64_t M;
-    int T, KB;          // tokens, blocks of k
-    int tilesM, tilesT; // tile = row tile * tilesT + token tile
+    int T, KB;           // tokens, blocks of k
+    int tilesM, tilesT;  // tile = row tile * tilesT + token tile
+    int mats;            // 2: a gated pair
     int y_type;
+    int whole;           // y's rows are so aligned that four elements of one may be stored at once
+    int early;           // weights may be read before the previous kernel has completed
 };
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
 
 __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v)
 {
@@ -80,44 +93,72 @@ __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v)
         static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
 }
 
-template <int BN, bool DUAL>
-__global__ void __launch_bounds__(kThreads, Narrow<BN, DUAL>::kCtas)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
-                    const __grid_constant__ CUtensorMap map_x, const float* __restrict__ ws0,
-                    const float* __restrict__ ws1, const float* __restrict__ xs, void* __restrict__ y,
-                    float* __restrict__ ys, const GemmShape g)
+// Four consecutive elements of a row of y, the first `live` of which there are.
+__device__ __forceinline__ void store_codes4(uint8_t* p, uint32_t codes, int live, bool whole)
 {
-    using S = Narrow<BN, DUAL>;
-    constexpr int NM = S::kMats, kAhead = S::kAhead;
+    if (whole && live == 4) {
+        *reinterpret_cast<uint32_t*>(p) = codes;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < live) p[e] = static_cast<uint8_t>(codes >> (8 * e));
+    }
+}
+__device__ __forceinline__ void store_rows4(void* y, int type, int64_t at, const float (&v)[4], int live, bool whole)
+{
+    if (whole && live == 4) {
+        if (type == BQD_F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = make_uint2(to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < live) store_y(y, type, at + e, v[e]);
+    }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
+                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ GemmShape g)
+{
+    using S = Narrow<BN>;
+    constexpr int H = S::kCols, kAhead = S::kAhead;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], dfull[S::kBufs], dempty[S::kBufs];
+    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], dfull[S::kBufs], dempty[S::kBufs],
+        got;
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) float s_scale[kSumWarps][2][BN * NM];
-    __shared__ uint32_t s_max[kSumWarps][BN];
+    __shared__ __align__(16) float s_scale[S::kSumWarps][2][H];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
-    // This cluster's tiles, and this CTA's blocks of each
-    uint32_t cs;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
-    const int rank = cs > 1 ? static_cast<int>(cta_rank()) : 0;
-    const int tiles = g.tilesM * g.tilesT, step = static_cast<int>(gridDim.x / cs);
-    const int tile0 = static_cast<int>(blockIdx.x / cs);
-    const int kb0 = static_cast<int>(static_cast<int64_t>(g.KB) * rank / cs);
-    const int nkb = static_cast<int>(static_cast<int64_t>(g.KB) * (rank + 1) / cs) - kb0;
+    // This cluster's tiles, and this CTA's weight and blocks of k of each
+    uint32_t ranks_;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks_));
+    const int ranks = static_cast<int>(ranks_), rank = ranks > 1 ? static_cast<int>(cta_rank()) : 0;
+    const int mat = g.mats > 1 ? rank & 1 : 0, cs = ranks / g.mats, ks = rank / g.mats;
+    const int tiles = g.tilesM * g.tilesT, step = static_cast<int>(gridDim.x) / ranks;
+    const int tile0 = static_cast<int>(blockIdx.x) / ranks;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(g.KB) * ks / cs);
+    const int nkb = static_cast<int>(static_cast<int64_t>(g.KB) * (ks + 1) / cs) - kb0;
+    const CUtensorMap* map_w = mat ? &map_w1 : &map_w0;
 
     if (threadIdx.x == 0) {
+        prefetch_map(map_w);
+        prefetch_map(&map_x);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], kSumWarps);
+            mbar_init(&dempty[i], S::kSumWarps);
         }
+        mbar_init(&got, 1);
         fence_barrier_init();
     }
-    if (warp == 1) {
+    if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                      "r"(S::kTmem)
                      : "memory");
@@ -127,30 +168,39 @@ __global__ void __launch_bounds__(kThreads, Narrow<BN, DUAL>::kCtas)
     __syncthreads();
     tc_after();
     const uint32_t tmem = s_tmem;
-    fp8_pdl_trigger();
+    float* parts = reinterpret_cast<float*>(ring + (S::kOver ? 0 : S::kStages * S::kStage));  // [part][token][row]
+    if (ranks > 1) {
+        if (threadIdx.x == 0) {
+            const int here = min(BN, g.T - tile0 % g.tilesT * BN);
+            mbar_arrive_expect_tx(&got, ranks * ((here - rank + ranks - 1) / ranks) * (kRows * 4));
+        }
+        cluster_arrive();  // its barrier may be counted at
+    }
 
     bool ok = true;
-    if (warp == 0) {
-        // ------------------------------------------------ copies
+    if (warp < 2) {
+        // ------------------------------------------------ copies, of every other block
         if (lane == 0) {
             auto copy_w = [&](int st, int tile, int kb) {
-                const uint32_t at = smem_u32(ring + st * S::kStage);
-                const int row = tile / g.tilesT * kRows;
                 mbar_arrive_expect_tx(&full[st], S::kStage);
-                tma_2d(at, &map_w0, kb * kBlk, row, &full[st]);
-                if constexpr (DUAL) tma_2d(at + kTileW, &map_w1, kb * kBlk, row, &full[st]);
+                tma_2d(smem_u32(ring + st * S::kStage), map_w, kb * kBlk, tile / g.tilesT * kRows, &full[st]);
             };
             auto copy_x = [&](int st, int tile, int kb) {
-                tma_2d(smem_u32(ring + st * S::kStage + NM * kTileW), &map_x, kb * kBlk, tile % g.tilesT * BN, &full[st]);
+                tma_2d(smem_u32(ring + st * S::kStage + kTileW), &map_x, kb * kBlk, tile % g.tilesT * BN, &full[st]);
             };
             // the first stages' weights before the wait for the previous kernel, whose output x may be
-            const int first = min(S::kStages, tile0 < tiles ? nkb : 0);
-            for (int i = 0; i < first; ++i) copy_w(i, tile0, kb0 + i);
+            const int first = min(S::kStages, nkb);
+            if (g.early)
+                for (int i = warp; i < first; i += 2) copy_w(i, tile0, kb0 + i);
             fp8_pdl_wait();
-            for (int i = 0; i < first; ++i) copy_x(i, tile0, kb0 + i);
+            for (int i = warp; i < first; i += 2) {
+                if (!g.early) copy_w(i, tile0, kb0 + i);
+                copy_x(i, tile0, kb0 + i);
+            }
             int it = first;
             for (int tile = tile0; tile < tiles && ok; tile += step) {
-                for (int i = tile == tile0 ? first : 0; i < nkb && ok; ++i, ++it) {
+                for (int i = tile == tile0 ? first : 0; i < nkb; ++i, ++it) {
+                    if ((it & 1) != warp) continue;
                     const int st = it % S::kStages;
                     if (it >= S::kStages) ok = mbar_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, &g_fp8_error);
                     if (!ok) break;
@@ -158,27 +208,28 @@ __global__ void __launch_bounds__(kThreads, Narrow<BN, DUAL>::kCtas)
                     copy_x(st, tile, kb0 + i);
                 }
             }
+            // The next kernel's start may overlap this one's end. No earlier: CTAs of the calls behind
+            // it would take the SMs' places and leave this one's unevenly spread.
+            fp8_pdl_trigger();
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ products
+    } else if (warp < 4) {
+        // ------------------------------------------------ products, of every other block
         constexpr uint32_t idesc = fp8_idesc(kRows, BN);
         int it = 0;
         for (int tile = tile0; tile < tiles && ok; tile += step) {
             for (int i = 0; i < nkb; ++i, ++it) {
+                if ((it & 1) != warp - 2) continue;
                 const int st = it % S::kStages, b = it % S::kBufs;
-                ok = mbar_wait_warp(&full[st], (it / S::kStages) & 1, &g_fp8_error);
-                if (ok && it >= S::kBufs) ok = mbar_wait_warp(&dempty[b], ((it / S::kBufs) & 1) ^ 1, &g_fp8_error);
+                ok = fp8_wait(&full[st], (it / S::kStages) & 1, &g_fp8_error);
+                if (ok && it >= S::kBufs) ok = fp8_wait(&dempty[b], ((it / S::kBufs) & 1) ^ 1, &g_fp8_error);
                 if (!ok) break;
                 tc_after();
                 if (fp8_elect()) {
-                    const uint32_t at = smem_u32(ring + st * S::kStage), xat = at + NM * kTileW;
+                    const uint32_t at = smem_u32(ring + st * S::kStage);
 #pragma unroll
-                    for (int m = 0; m < NM; ++m)
-#pragma unroll
-                        for (int j = 0; j < kBlk / 32; ++j)
-                            fp8_mma(tmem + b * S::kCols + m * BN, fp8_desc(at + m * kTileW + 32 * j),
-                                    fp8_desc(xat + 32 * j), idesc, j != 0 ? 1u : 0u);
+                    for (int j = 0; j < kBlk / 32; ++j)
+                        fp8_mma(tmem + b * BN, fp8_desc(at + 32 * j), fp8_desc(at + kTileW + 32 * j), idesc, j != 0 ? 1u : 0u);
                     fp8_commit(&empty[st]);
                     fp8_commit(&dfull[b]);
                 }
@@ -186,187 +237,272 @@ __global__ void __launch_bounds__(kThreads, Narrow<BN, DUAL>::kCtas)
             }
         }
     } else {
-        // ------------------------------------------------ sums, a row of the weights per thread
-        const int q = warp % 4, sw = warp - 2;  // tensor-memory lane quarter; this warp's scales
-        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        // ------------------------------------------------ sums: a row of the weights and kCols tokens per thread
+        const int q = warp % 4, sw = warp - 4, c0 = sw / 4 * H;  // tensor-memory lane quarter; columns
+        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + c0;
         const int r = 32 * q + lane;
-        constexpr int L = (BN + kWarp - 1) / kWarp;  // tokens of a lane when it fetches scales
+        constexpr int L = (H + kWarp - 1) / kWarp;  // tokens of a lane when it fetches scales
         int it = 0;
         fp8_pdl_wait();
         for (int tile = tile0; tile < tiles; tile += step) {
-            const int mt = tile / g.tilesT, n0 = tile % g.tilesT * BN;
-            uint64_t acc[NM][BN / 2];
+            const int mt = tile / g.tilesT, n0 = tile % g.tilesT * BN + c0;
+            uint64_t acc[H / 2];
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
-#pragma unroll
-                for (int c = 0; c < BN / 2; ++c) acc[m][c] = 0;
-            float far_x[kAhead][L], far_w[kAhead][NM];
+            for (int c = 0; c < H / 2; ++c) acc[c] = 0;
+            float far_x[kAhead][L], far_w[kAhead];
+            const float* ws = g.s[mat] + static_cast<int64_t>(mt) * g.KB + kb0;
+            const float* xs = g.xs + static_cast<int64_t>(kb0) * g.T + n0 + lane;
             auto fetch = [&](int slot, int i) {
 #pragma unroll
-                for (int l = 0; l < L; ++l) {
-                    const int t = n0 + lane + l * kWarp;
-                    far_x[slot][l] = i < nkb && t < g.T && lane + l * kWarp < BN
-                                         ? __ldg(xs + static_cast<int64_t>(kb0 + i) * g.T + t)
+                for (int l = 0; l < L; ++l)
+                    far_x[slot][l] = i < nkb && n0 + lane + l * kWarp < g.T && (H % kWarp == 0 || lane + l * kWarp < H)
+                                         ? __ldg(xs + static_cast<int64_t>(i) * g.T + l * kWarp)
                                          : 0.f;
-                }
-                const int64_t at = static_cast<int64_t>(mt) * g.KB + kb0 + i;
-                far_w[slot][0] = i < nkb ? __ldg(ws0 + at) : 0.f;
-                if constexpr (DUAL) far_w[slot][1] = i < nkb ? __ldg(ws1 + at) : 0.f;
+                far_w[slot] = i < nkb ? __ldg(ws + i) : 0.f;
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) fetch(i, i);
-            for (int i = 0; i < nkb; ++i, ++it) {
-                // the block's scales, to where every lane reads them all
-                float* sc = s_scale[sw][it & 1];
+            for (int i0 = 0; i0 < nkb; i0 += kAhead) {
 #pragma unroll
-                for (int l = 0; l < L; ++l)
-                    if (BN % kWarp == 0 || lane + l * kWarp < BN)
+                for (int u = 0; u < kAhead; ++u) {  // a register of scales on their way may not be moved
+                    const int i = i0 + u;
+                    if (i >= nkb) break;
+                    // the block's scales, to where every lane reads them all
+                    float* sc = s_scale[sw][it & 1];
 #pragma unroll
-                        for (int m = 0; m < NM; ++m) sc[m * BN + lane + l * kWarp] = far_x[0][l] * far_w[0][m];
+                    for (int l = 0; l < L; ++l)
+                        if (H % kWarp == 0 || lane + l * kWarp < H) sc[lane + l * kWarp] = far_x[u][l] * far_w[u];
+                    fetch(u, i + kAhead);
+                    const int b = it % S::kBufs;
+                    // After a wait that ran out the loops go on without waiting, so that the warps
+                    // still meet at every barrier.
+                    if (ok) ok = fp8_wait(&dfull[b], (it / S::kBufs) & 1, &g_fp8_error);
+                    __syncwarp();  // the scales are there
+                    tc_after();
+                    constexpr int C = BN > 64 ? 32 : 16;
 #pragma unroll
-                for (int d = 0; d + 1 < kAhead; ++d) {
-#pragma unroll
-                    for (int l = 0; l < L; ++l) far_x[d][l] = far_x[d + 1][l];
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) far_w[d][m] = far_w[d + 1][m];
-                }
-                fetch(kAhead - 1, i + kAhead);
-                const int b = it % S::kBufs;
-                // (also orders the scales). After a wait that ran out the loops go on without
-                // waiting, so that the warps still meet at every barrier.
-                if (ok) ok = mbar_wait_warp(&dfull[b], (it / S::kBufs) & 1, &g_fp8_error);
-                __syncwarp();
-                tc_after();
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int c = 0; c < BN; c += 16) {
-                        uint32_t d[16];
-                        tmem_ld16(base + b * S::kCols + m * BN + c, d);
+                    for (int c = 0; c < H; c += C) {
+                        uint32_t d[C];
+                        tmem_load<C>(base + b * BN + c, d);
                         tmem_wait_ld();
-                        const float4* s4 = reinterpret_cast<const float4*>(sc + m * BN + c);
+                        if (c + C == H) {  // the buffer has been read
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&dempty[b]);
+                        }
+                        const float4* s4 = reinterpret_cast<const float4*>(sc + c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < C / 4; ++e) {
                             const float4 f = s4[e];
-                            uint64_t* o = &acc[m][(c + 4 * e) / 2];
+                            uint64_t* o = &acc[(c + 4 * e) / 2];
                             o[0] = fma2(pack(__uint_as_float(d[4 * e]), __uint_as_float(d[4 * e + 1])), pack(f.x, f.y), o[0]);
                             o[1] = fma2(pack(__uint_as_float(d[4 * e + 2]), __uint_as_float(d[4 * e + 3])), pack(f.z, f.w), o[1]);
                         }
                     }
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&dempty[b]);
-            }
-            // ---- the tile's outputs
-            const int64_t row = static_cast<int64_t>(mt) * kRows + r;
-            const bool live = row < g.M;
-            float* part = reinterpret_cast<float*>(ring);  // [matrix][token][row], with a cluster
-            int c0 = 0, c1 = BN;                           // this CTA's tokens of the tile
-            if (cs > 1) {
-                // the ring is done with (all its products have been read); the other warps
-                // meet this barrier and the last one after their loops
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int c = 0; c < BN; c += 2) {
-                        float u, v;
-                        unpack(acc[m][c / 2], u, v);
-                        part[(m * BN + c) * kRows + r] = u;
-                        part[(m * BN + c + 1) * kRows + r] = v;
-                    }
-                cluster_barrier();
-                c0 = BN * rank / static_cast<int>(cs);
-                c1 = BN * (rank + 1) / static_cast<int>(cs);
-                for (int c = c0; c < c1; ++c) {
-                    float sum[NM];
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) {
-                        const uint32_t at = smem_u32(part + (m * BN + c) * kRows + r);
-                        float v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = k < static_cast<int>(cs) ? ld_cluster(cta_map(at, k)) : 0.f;
-                        sum[m] = v[0];
-#pragma unroll
-                        for (int k = 1; k < 8; ++k) sum[m] += v[k];
-                    }
-                    if constexpr (DUAL) sum[0] = silu_mul(sum[0], sum[1]);
-                    if (g.y_type == BQD_E4M3) {
-                        part[c * kRows + r] = sum[0];
-                        const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, live ? abs_bits(sum[0]) : 0u);
-                        if (lane == 0) s_max[sw][c] = w;
-                    } else if (live && n0 + c < g.T) {
-                        store_y(y, g.y_type, static_cast<int64_t>(n0 + c) * g.M + row, sum[0]);
-                    }
+                    ++it;
                 }
-            } else {
+            }
+            if (ranks > 1) {
+                // the parts to their tokens' CTAs
+                cluster_wait();
+                if (S::kOver) {  // once every ring of the cluster is done with
+                    cluster_arrive();
+                    cluster_wait();
+                }
+                const int here = min(BN, g.T - (n0 - c0)), most = (here + ranks - 1) / ranks;
+                const uint32_t mine = smem_u32(parts) + static_cast<uint32_t>(rank * most * kRows + r) * 4;
+                int to = c0 % ranks, j = c0 / ranks;
 #pragma unroll
-                for (int c = 0; c < BN; c += 2) {
+                for (int c = 0; c < H; c += 2) {
                     float v[2];
-                    unpack(acc[0][c / 2], v[0], v[1]);
-                    if constexpr (DUAL) {
-                        float u[2];
-                        unpack(acc[1][c / 2], u[0], u[1]);
-                        v[0] = silu_mul(v[0], u[0]);
-                        v[1] = silu_mul(v[1], u[1]);
-                        acc[0][c / 2] = pack(v[0], v[1]);
-                    }
+                    unpack(acc[c / 2], v[0], v[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (DUAL && g.y_type == BQD_E4M3) {
-                            const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, live ? abs_bits(v[e]) : 0u);
-                            if (lane == 0) s_max[sw][c + e] = w;
-                        } else if (live && n0 + c + e < g.T) {
-                            store_y(y, g.y_type, static_cast<int64_t>(n0 + c + e) * g.M + row, v[e]);
+                        if (c0 + c + e < here)
+                            st_async(cta_map(mine + j * (kRows * 4), to), v[e], cta_map(smem_u32(&got), to));
+                        if (++to == ranks) {
+                            to = 0;
+                            ++j;
                         }
                     }
                 }
-            }
-            if (DUAL && g.y_type == BQD_E4M3) {
-                named_sync(1, kSumWarps * kWarp);
-                auto code = [&](int c, float v) {
-                    const float s = block_scale(max(max(s_max[0][c], s_max[1][c]), max(s_max[2][c], s_max[3][c])));
-                    if (n0 + c < g.T) {
-                        if (live)
-                            static_cast<uint8_t*>(y)[static_cast<int64_t>(n0 + c) * g.M + row] =
-                                static_cast<uint8_t>(BlockCoder(s).one(v));
-                        if (r == 0) ys[static_cast<int64_t>(mt) * g.T + n0 + c] = s;
-                    }
-                };
-                if (cs > 1) {
-                    for (int c = c0; c < c1; ++c) code(c, part[c * kRows + r]);
-                } else {
+            } else {
+                const int64_t row = static_cast<int64_t>(mt) * kRows + r;
+                if (row < g.M) {
 #pragma unroll
-                    for (int c = 0; c < BN; c += 2) {
+                    for (int c = 0; c < H; c += 2) {
                         float u, v;
-                        unpack(acc[0][c / 2], u, v);
-                        code(c, u);
-                        code(c + 1, v);
+                        unpack(acc[c / 2], u, v);
+                        const int64_t at = static_cast<int64_t>(n0 + c) * g.M + row;
+                        if (n0 + c < g.T) store_y(g.y, g.y_type, at, u);
+                        if (n0 + c + 1 < g.T) store_y(g.y, g.y_type, at + g.M, v);
                     }
                 }
-                named_sync(1, kSumWarps * kWarp);  // before the next tile's maxima
             }
         }
         tc_before();
     }
     if (!ok) let_copies_land();
-    if (cs > 1) {
-        // a cluster takes one tile, so each warp meets two barriers: parts written, parts read
+    if (ranks > 1) {
+        // ---- a cluster takes one tile: this CTA's tokens, every so manieth of them in each group of warps
         __syncwarp();
-        if (warp < 2) cluster_barrier();
-        cluster_barrier();
+        if (warp < 4) {
+            cluster_wait();
+            if (S::kOver) {
+                cluster_arrive();
+                cluster_wait();
+            }
+        } else {
+            // a token per warp at a time, four rows a lane
+            const int mt = tile0 / g.tilesT, n0 = tile0 % g.tilesT * BN, here = min(BN, g.T - n0);
+            const int most = (here + ranks - 1) / ranks, n = (here - rank + ranks - 1) / ranks;
+            const int64_t row = static_cast<int64_t>(mt) * kRows + 4 * lane;
+            const int live = static_cast<int>(min(static_cast<int64_t>(4), max(static_cast<int64_t>(0), g.M - row)));
+            // (four times the limit of the other waits: a CTA that gives up one of those still stores)
+            if (!fp8_wait_cluster(&got, 0, &g_fp8_error, 4 * kWaitCycles)) ok = false;
+            for (int j = warp - 4; j < n; j += S::kSumWarps) {
+                const float4* part = reinterpret_cast<const float4*>(parts + j * kRows) + lane;
+                const int step4 = most * (kRows / 4);  // to the next part
+                float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+                for (int k = 0; k < ranks; k += g.mats) {  // over the blocks of k, in order
+                    const float4 p = part[k * step4];
+                    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+                    if (g.mats > 1) {
+                        const float4 w = part[(k + 1) * step4];
+                        u[0] += w.x, u[1] += w.y, u[2] += w.z, u[3] += w.w;
+                    }
+                }
+                if (g.mats > 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], u[e]);
+                }
+                const int64_t t = n0 + rank + j * ranks;
+                if (g.y_type == BQD_E4M3) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m = max(m, e < live ? abs_bits(v[e]) : 0u);
+                    const float sc = block_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+                    const BlockCoder coder(sc);
+                    store_codes4(static_cast<uint8_t*>(g.y) + t * g.M + row,
+                                 coder.pair(pack(v[0], v[1])) | (coder.pair(pack(v[2], v[3])) << 16), live, g.whole);
+                    if (lane == 0) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
+                } else {
+                    store_rows4(g.y, g.y_type, t * g.M + row, v, live, g.whole);
+                }
+            }
+        }
     }
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 2) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem) : "memory");
     }
 }
 
+// Clusters of `ranks` CTAs that run at once on the device: fewer than its slots
+// hold, as a cluster stays within a group of SMs. Cached.
+template <int BN>
+int clusters_at_once(int dev, int ranks)
+{
+    using S = Narrow<BN>;
+    static std::mutex mu;
+    static int known[64][kMaxCluster + 1];
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64) return 0;
+    int& n = known[dev][ranks];
+    if (n == 0) {
+        if (cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+            cudaGetLastError();
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(ranks * S::kCtas * dev_info(dev).sms));
+        cfg.blockDim = dim3(S::kThreads);
+        cfg.dynamicSmemBytes = S::kSmem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int found = 0;
+        if (cudaOccupancyMaxActiveClusters(&found, fp8_gemm_kernel<BN>, &cfg) != cudaSuccess) {
+            cudaGetLastError();  // consumed: it must not surface as a launch error later
+            return 0;
+        }
+        n = found > 0 ? found : -1;
+    }
+    return n;
+}
+
+template <int BN>
+cudaError_t launch_narrow(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
+{
+    using S = Narrow<BN>;
+    CUtensorMap w0, w1, x;
+    if (!fp8_codes_map(&w0, a.w0, a.M, a.K, kRows) || !fp8_codes_map(&x, a.x, a.T, a.K, BN)) return cudaErrorInvalidValue;
+    if (!dual)
+        w1 = w0;
+    else if (!fp8_codes_map(&w1, a.w1, a.M, a.K, kRows))
+        return cudaErrorInvalidValue;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    auto kern = fp8_gemm_kernel<BN>;
+    static OccCache occ;
+    blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, S::kThreads, S::kSmem);
+    GemmShape g{};
+    g.s[0] = a.s0;
+    g.s[1] = a.s1;
+    g.xs = a.xs;
+    g.y = a.y;
+    g.ys = a.ys;
+    g.M = a.M;
+    g.T = static_cast<int>(a.T);
+    g.KB = static_cast<int>((a.K + kBlk - 1) / kBlk);
+    g.tilesM = static_cast<int>((a.M + kRows - 1) / kRows);
+    g.tilesT = static_cast<int>((a.T + BN - 1) / BN);
+    g.mats = dual ? 2 : 1;
+    g.y_type = a.y_type;
+    g.whole = a.M % 4 == 0;  // y starts on 16 bytes
+    g.early = (launch_flags() & kLaunchPdl) != 0;
+    // the k blocks of a tile over as many CTAs as may be with every cluster running at once (with
+    // one weight and many tiles: a CTA for tile after tile)
+    const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, slots = static_cast<int64_t>(dev_info(dev).sms) * S::kCtas;
+    int cs = kMaxCluster / g.mats < g.KB ? kMaxCluster / g.mats : g.KB;
+    while (cs > 1 && (tiles * cs * g.mats > slots || tiles > S::kCtas * clusters_at_once<BN>(dev, cs * g.mats))) --cs;
+    const int ranks = cs * g.mats;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : tiles < slots ? tiles : slots));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    // the kernel itself waits for the one before it, ahead of its first access to memory (but
+    // for the weights, if the launch flags allow that), so its start may overlap the other's end
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    int na = 1;
+    if (ranks > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = static_cast<unsigned>(na);
+    return cudaLaunchKernelEx(&cfg, kern, w0, w1, x, g);
+}
+
+}  // namespace
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiledFn encode_fn()
+static EncodeTiledFn encode_fn()
 {
     static std::once_flag once;
     static EncodeTiledFn fn = nullptr;
@@ -382,8 +518,7 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// Codes [rows][K] in boxes of 128 k x `box` rows; k and rows past the ends read as zero.
-bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box)
+bool fp8_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -396,56 +531,6 @@ bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool DUAL>
-cudaError_t launch_narrow(const Fp8GemmArgs& a, cudaStream_t s)
-{
-    using S = Narrow<BN, DUAL>;
-    CUtensorMap w0, w1, x;
-    if (!codes_map(&w0, a.w0, a.M, a.K, kRows) || !codes_map(&w1, DUAL ? a.w1 : a.w0, a.M, a.K, kRows) ||
-        !codes_map(&x, a.x, a.T, a.K, BN))
-        return cudaErrorInvalidValue;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    auto kern = fp8_gemm_kernel<BN, DUAL>;
-    static OccCache occ;
-    blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, kThreads, S::kSmem);
-    GemmShape g{};
-    g.M = a.M;
-    g.T = static_cast<int>(a.T);
-    g.KB = static_cast<int>((a.K + kBlk - 1) / kBlk);
-    g.tilesM = static_cast<int>((a.M + kRows - 1) / kRows);
-    g.tilesT = static_cast<int>((a.T + BN - 1) / BN);
-    g.y_type = a.y_type;
-    const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, slots = static_cast<int64_t>(dev_info(dev).sms) * S::kCtas;
-    int cs = 1;
-    while (cs < 8 && tiles * cs * 2 <= slots && cs * 2 <= g.KB) cs *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cs > 1 ? tiles * cs : tiles < slots ? tiles : slots));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    int na = 0;
-    if (cs > 1) {
-        attr[na].id = cudaLaunchAttributeClusterDimension;
-        attr[na].val.clusterDim.x = static_cast<unsigned>(cs);
-        attr[na].val.clusterDim.y = 1;
-        attr[na].val.clusterDim.z = 1;
-        ++na;
-    }
-    if (launch_flags() & kLaunchPdl) {
-        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[na].val.programmaticStreamSerializationAllowed = 1;
-        ++na;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = static_cast<unsigned>(na);
-    return cudaLaunchKernelEx(&cfg, kern, w0, w1, x, a.s0, a.s1, a.xs, a.y, a.ys, g);
-}
-
-}  // namespace
-
 bool fp8_gemm_supported(int64_t M, int64_t K, int64_t T)
 {
     return K >= 16 && K % 16 == 0 && K <= (int64_t(1) << 24) && M >= 1 && M <= (int64_t(1) << 30) && T >= 1 &&
@@ -454,23 +539,20 @@ bool fp8_gemm_supported(int64_t M, int64_t K, int64_t T)
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
 {
-    if (dual) {
-        if (a.T <= 16) return launch_narrow<16, true>(a, s);
-        if (a.T <= 32) return launch_narrow<32, true>(a, s);
-        return launch_narrow<64, true>(a, s);
-    }
-    if (a.T <= 16) return launch_narrow<16, false>(a, s);
-    if (a.T <= 32) return launch_narrow<32, false>(a, s);
-    if (a.T <= 64) return launch_narrow<64, false>(a, s);
-    return launch_narrow<128, false>(a, s);
+    if (fp8_gemm_wants_pairs(a, dual)) return launch_fp8_gemm_pairs(a, dual, s);
+    if (a.T <= 16) return launch_narrow<16>(a, dual, s);
+    if (a.T <= 32) return launch_narrow<32>(a, dual, s);
+    if (a.T <= 64) return launch_narrow<64>(a, dual, s);
+    return launch_narrow<128>(a, dual, s);
 }
 
 cudaError_t read_and_clear_fp8_error(unsigned int* out)
 {
-    unsigned int v = 0;
+    unsigned int v = 0, w = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_error, sizeof(v));
+    if (e == cudaSuccess) e = read_and_clear_fp8_pairs_error(&w);
     if (e != cudaSuccess) return e;
-    *out = v;
+    *out = v | w;
     if (v) {
         const unsigned int zero = 0;
         e = cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof(zero));

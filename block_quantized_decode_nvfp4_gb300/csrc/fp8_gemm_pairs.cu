@@ -1,0 +1,434 @@
+// fp8_gemm_pairs.cu -- the products of fp8_gemm.cu for many tokens, where the
+// tensor cores are the bound: pairs of CTAs (cta_group::2) on tiles of 256
+// tokens x 256 rows of a weight, or x 128 rows of each of a gated pair.
+//
+// A CTA of a pair holds 128 tokens (the MMA's rows; its lanes of tensor memory)
+// and half of the weight's rows in its ring, 32 KiB a block of 128 k, and the
+// tensor cores of both read both halves: half the copies and reads of shared
+// memory per product that a CTA alone needs, whose port would be the bound.
+// Tokens lie on the lanes, so a block's scales are one register for a thread's
+// token times one value for its columns. Per CTA:
+//  - warps 0 and 1 copy every other block (counted at the first CTA's barriers);
+//  - warps 2 and 3 of the first CTA issue every other block's MMAs (M = 256,
+//    N = 256, K = 32) into one of two buffers of 256 columns;
+//  - warps 4..11 read a buffer, 128 columns of a token a thread, scale it and
+//    add it to 128 registers, while the next block's products run.
+// Pairs are persistent, so the ring runs on over the outputs of a tile, which go
+// through shared memory to be stored in whole lines.
+// Every wait is bounded (kErrWaitTimeout in the kernel's error word).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "f32x2.cuh"
+#include "fp8.cuh"
+#include "fp8.h"
+#include "host_util.h"
+#include "stream.cuh"
+
+namespace bqd {
+
+__device__ unsigned int g_fp8_pairs_error = 0;
+
+namespace {
+
+constexpr int kBlk = 128;                 // k of a block of scales and of a ring stage
+constexpr int kHalf = 128;                // tokens and weight rows of a CTA's half
+constexpr int kTile = 2 * kHalf;          // tokens of a tile (MMA M), columns of a buffer (N)
+constexpr int kHalfBytes = kHalf * kBlk;
+constexpr int kStage = 2 * kHalfBytes;    // of one CTA
+constexpr int kStages = 6;
+constexpr int kBufs = 2;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = (4 + kSumWarps) * kWarp;
+constexpr int kLineBytes = 128;           // of a token's outputs, staged by a warp at once
+constexpr int kOut = kWarp * kLineBytes;  // staging of a warp
+constexpr int kSmem = kStages * kStage + kSumWarps * kOut + 1024;  // + alignment slack
+constexpr int kAhead = 4;                 // blocks whose scales are on their way
+constexpr int kGroup = 8;                 // token tiles that share a sweep over the weights
+// 128 x 80 + 256 x 208 of the 384 x 168 registers that the block has
+constexpr int kRegs = 168, kFewRegs = 80, kSumRegs = 208;
+static_assert(4 * kWarp * kFewRegs + kSumWarps * kWarp * kSumRegs <= kThreads * kRegs, "the split of the registers");
+static_assert(kSmem <= 227 * 1024 - 512, "shared memory of one CTA, static beside it");
+static_assert(kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
+
+struct PairShape {
+    const float *s[2], *xs;
+    void* y;
+    float* ys;
+    int64_t M;
+    int T, KB;
+    int tilesM, tilesT;
+    int blocksM;  // of 128 rows
+    int y_type;
+    int align;    // bytes to which every row of y is aligned: 16, 4, or an element's
+};
+
+// Tile i: kGroup token tiles under each tile of the weights, group after group.
+__device__ __forceinline__ void find_tile(const PairShape& g, int i, int& mt, int& tt)
+{
+    const int per = kGroup * g.tilesM, group = i / per, in = i - group * per;
+    const int wide = min(kGroup, g.tilesT - group * kGroup);
+    mt = in / wide;
+    tt = group * kGroup + in - mt * wide;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
+
+// A warp's 32 tokens x BYTES of outputs, as lane l has token l's in v, to rows of
+// y: through shared memory, so that a store has whole lines. at: bytes from y to
+// token 0's; pitch: bytes of a row; left: bytes of the row from `at`; tokens: how
+// many there are.
+template <int BYTES>
+__device__ __forceinline__ void store_lines(uint8_t* stage, const uint4 (&v)[BYTES / 16], uint8_t* at, int64_t pitch,
+                                            int64_t left, int tokens, int align)
+{
+    constexpr int C = BYTES / 16;  // 16-byte pieces of a line
+    const int lane = threadIdx.x % kWarp;
+    __syncwarp();  // what was staged before has been read
+#pragma unroll
+    for (int i = 0; i < C; ++i) *reinterpret_cast<uint4*>(stage + lane * BYTES + ((i ^ (lane & (C - 1))) << 4)) = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int t = i * (kWarp / C) + lane / C, c = lane & (C - 1);
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + t * BYTES + ((c ^ (t & (C - 1))) << 4));
+        if (t >= tokens) continue;
+        uint8_t* p = at + t * pitch + c * 16;
+        const int64_t n = left - c * 16;  // bytes of the row from here
+        if (align == 16 && n >= 16) {
+            *reinterpret_cast<uint4*>(p) = w;
+        } else {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (align >= 4 && n >= 4 * e + 4) {
+                    reinterpret_cast<uint32_t*>(p)[e] = x[e];
+                } else if (align == 2) {
+                    if (n >= 4 * e + 2) reinterpret_cast<uint16_t*>(p)[2 * e] = static_cast<uint16_t>(x[e]);
+                    if (n >= 4 * e + 4) reinterpret_cast<uint16_t*>(p)[2 * e + 1] = static_cast<uint16_t>(x[e] >> 16);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (n > 4 * e + b) p[4 * e + b] = static_cast<uint8_t>(x[e] >> (8 * b));
+                }
+            }
+        }
+    }
+}
+
+template <bool DUAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_pairs_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
+                     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ PairShape g)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], dfull[kBufs], dempty[kBufs];
+    __shared__ uint32_t s_tmem;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    const int rank = static_cast<int>(cta_rank());
+    const int tiles = g.tilesM * g.tilesT, step = static_cast<int>(gridDim.x) / 2, tile0 = static_cast<int>(blockIdx.x) / 2;
+    const CUtensorMap* map_w = DUAL && rank ? &map_w1 : &map_w0;
+
+    if (threadIdx.x == 0) {
+        prefetch_map(map_w);
+        prefetch_map(&map_x);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 2);  // the first CTA's counts, for both
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 2 * kSumWarps);  // the first CTA's counts, for both
+        }
+        fence_barrier_init();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = s_tmem;
+    cluster_arrive();  // the pair's barriers and tensor memory are there
+    cluster_wait();
+    fp8_pdl_wait();
+
+    bool ok = true;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp < 2) {
+            // -------------------------------------------- copies, of every other block
+            if (lane == 0) {
+                int it = 0;
+                for (int tile = tile0; tile < tiles && ok; tile += step) {
+                    int mt, tt;
+                    find_tile(g, tile, mt, tt);
+                    const int row = DUAL ? mt * kHalf : mt * kTile + rank * kHalf, tok = tt * kTile + rank * kHalf;
+                    for (int i = 0; i < g.KB; ++i, ++it) {
+                        if ((it & 1) != warp) continue;
+                        const int st = it % kStages;
+                        if (it >= kStages) ok = mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1, &g_fp8_pairs_error);
+                        if (!ok) break;
+                        const uint32_t at = smem_u32(ring + st * kStage), bar = cta_map(smem_u32(&full[st]), 0);
+                        arrive_expect_cluster(bar, kStage);
+                        tma_2d_pair(at, &map_x, i * kBlk, tok, bar);
+                        tma_2d_pair(at + kHalfBytes, map_w, i * kBlk, row, bar);
+                    }
+                }
+                fp8_pdl_trigger();
+            }
+            __syncwarp();
+        } else if (rank == 0) {
+            // -------------------------------------------- products, of every other block
+            constexpr uint32_t idesc = fp8_idesc(kTile, kTile);
+            int it = 0;
+            for (int tile = tile0; tile < tiles && ok; tile += step) {
+                for (int i = 0; i < g.KB; ++i, ++it) {
+                    if ((it & 1) != warp - 2) continue;
+                    const int st = it % kStages, b = it % kBufs;
+                    ok = fp8_wait(&full[st], (it / kStages) & 1, &g_fp8_pairs_error);
+                    if (ok && it >= kBufs) ok = fp8_wait(&dempty[b], ((it / kBufs) & 1) ^ 1, &g_fp8_pairs_error);
+                    if (!ok) break;
+                    tc_after();
+                    if (fp8_elect()) {
+                        const uint32_t at = smem_u32(ring + st * kStage);
+#pragma unroll
+                        for (int j = 0; j < kBlk / 32; ++j)
+                            fp8_mma_pair(tmem + b * kTile, fp8_desc(at + 32 * j), fp8_desc(at + kHalfBytes + 32 * j), idesc,
+                                         j != 0 ? 1u : 0u);
+                        fp8_commit_pair(&empty[st]);
+                        fp8_commit_pair(&dfull[b]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------ sums: a token and 128 columns per thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        const int q = warp % 4, half = (warp - 4) / 4;
+        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        // its columns, 32 at a time: 128 of one weight block, or 64 each of the two weights
+        const int col0 = DUAL ? 64 * half : kHalf * half, col2 = DUAL ? kHalf + 64 * half : kHalf * half + 64;
+        uint8_t* stage = ring + kStages * kStage + (warp - 4) * kOut;
+        const uint32_t free0 = cta_map(smem_u32(&dempty[0]), 0);
+        int it = 0, turn = 0;
+        for (int tile = tile0; tile < tiles; tile += step, turn ^= 1) {
+            int mt, tt;
+            find_tile(g, tile, mt, tt);
+            const int t = tt * kTile + rank * kHalf + 32 * q + lane;
+            const int mb = DUAL ? mt : min(2 * mt + half, g.blocksM - 1);
+            const float* ws0 = g.s[0] + static_cast<int64_t>(mb) * g.KB;
+            const float* ws1 = DUAL ? g.s[1] + static_cast<int64_t>(mb) * g.KB : nullptr;
+            const float* xs = g.xs + t;
+            uint64_t acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = 0;
+            float far_x[kAhead], far_w[kAhead], far_u[kAhead];
+            auto fetch = [&](int slot, int i) {
+                far_x[slot] = i < g.KB && t < g.T ? __ldg(xs + static_cast<int64_t>(i) * g.T) : 0.f;
+                far_w[slot] = i < g.KB ? __ldg(ws0 + i) : 0.f;
+                if constexpr (DUAL) far_u[slot] = i < g.KB ? __ldg(ws1 + i) : 0.f;
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) fetch(i, i);
+            for (int i0 = 0; i0 < g.KB; i0 += kAhead) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {  // a register of scales on their way may not be moved
+                    const int i = i0 + u;
+                    if (i >= g.KB) break;
+                    const float f0 = far_x[u] * far_w[u], f1 = DUAL ? far_x[u] * far_u[u] : f0;
+                    fetch(u, i + kAhead);
+                    const int b = it % kBufs;
+                    // After a wait that ran out the loops go on without waiting, so that the warps
+                    // still meet at every barrier.
+                    if (ok) ok = fp8_wait(&dfull[b], (it / kBufs) & 1, &g_fp8_pairs_error);
+                    __syncwarp();
+                    tc_after();
+                    // 16 columns at a time, the next on their way
+                    uint32_t d[2][16];
+                    tmem_load<16>(base + b * kTile + col0, d[0]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (c < 7) tmem_load<16>(base + b * kTile + (c < 3 ? col0 + 16 * (c + 1) : col2 + 16 * (c - 3)), d[(c + 1) & 1]);
+                        const float f = c < 4 ? f0 : f1;
+                        const uint64_t ff = pack(f, f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            acc[8 * c + e] = fma2(pack(__uint_as_float(d[c & 1][2 * e]), __uint_as_float(d[c & 1][2 * e + 1])),
+                                                  ff, acc[8 * c + e]);
+                        if (c < 7) tmem_wait_ld();
+                        if (c == 6) {  // the buffer has been read
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_cluster(free0 + b * 8);
+                        }
+                    }
+                    ++it;
+                }
+            }
+            // ---- the tile's outputs
+            const int tok0 = tt * kTile + rank * kHalf + 32 * q, tokens = g.T - tok0;
+            auto value = [&](int c) {
+                float x, y;
+                unpack(acc[c / 2], x, y);
+                return c & 1 ? y : x;
+            };
+            const int64_t m0 = DUAL ? static_cast<int64_t>(mt) * kHalf + 64 * half : static_cast<int64_t>(mt) * kTile + kHalf * half;
+            constexpr int N = DUAL ? 64 : 128;  // outputs of a thread
+            if constexpr (DUAL) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float g0, g1, u0, u1;
+                    unpack(acc[c], g0, g1);
+                    unpack(acc[32 + c], u0, u1);
+                    acc[c] = pack(silu_mul(g0, u0), silu_mul(g1, u1));
+                }
+            }
+            const int64_t left = g.M - m0;  // elements of the row from this thread's first
+            if (DUAL && g.y_type == BQD_E4M3) {
+                uint32_t most = 0;
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+                    if (c < left) most = max(most, abs_bits(value(c)));
+                // with the warp that has the other half of these tokens: past the codes' lines in its
+                // staging, at another place for the next tile
+                const int seen = kOut / 2 + turn * (4 * kWarp) + 4 * lane;
+                *reinterpret_cast<uint32_t*>(stage + seen) = most;
+                named_sync(1 + q, 2 * kWarp);
+                const float sc = block_scale(max(most, *reinterpret_cast<const uint32_t*>(stage + (half ? -4 : 4) * kOut + seen)));
+                const BlockCoder coder(sc);
+                if (half == 0 && t < g.T) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = coder.pair(acc[8 * i + 2 * e]) | (coder.pair(acc[8 * i + 2 * e + 1]) << 16);
+                    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                store_lines<64>(stage, v, static_cast<uint8_t*>(g.y) + static_cast<int64_t>(tok0) * g.M + m0, g.M, left, tokens,
+                                g.align);
+            } else if (g.y_type == BQD_BF16) {
+#pragma unroll
+                for (int k = 0; k < N / 64; ++k) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = to_bf16x2(value(64 * k + 8 * i + 2 * e), value(64 * k + 8 * i + 2 * e + 1));
+                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 2 * (static_cast<int64_t>(tok0) * g.M + m0 + 64 * k),
+                                     2 * g.M, 2 * (left - 64 * k), tokens, g.align);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < N / 32; ++k) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = make_uint4(__float_as_uint(value(32 * k + 4 * i)), __float_as_uint(value(32 * k + 4 * i + 1)),
+                                          __float_as_uint(value(32 * k + 4 * i + 2)), __float_as_uint(value(32 * k + 4 * i + 3)));
+                    store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 4 * (static_cast<int64_t>(tok0) * g.M + m0 + 32 * k),
+                                     4 * g.M, 4 * (left - 32 * k), tokens, g.align);
+                }
+            }
+        }
+        tc_before();
+    }
+    if (!ok) let_copies_land();
+    __syncwarp();
+    cluster_arrive();  // the pair's products and arrivals are over
+    cluster_wait();
+    if (warp == 2) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <bool DUAL>
+cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t s)
+{
+    CUtensorMap w0, w1, x;
+    if (!fp8_codes_map(&w0, a.w0, a.M, a.K, kHalf) || !fp8_codes_map(&x, a.x, a.T, a.K, kHalf)) return cudaErrorInvalidValue;
+    if (!DUAL)
+        w1 = w0;
+    else if (!fp8_codes_map(&w1, a.w1, a.M, a.K, kHalf))
+        return cudaErrorInvalidValue;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    auto kern = fp8_pairs_kernel<DUAL>;
+    static OccCache occ;
+    blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, kThreads, kSmem);
+    // the split of the registers needs what the block is launched with
+    static const int regs = [] {
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, fp8_pairs_kernel<DUAL>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < kRegs) return cudaErrorInvalidConfiguration;
+    PairShape g{};
+    g.s[0] = a.s0;
+    g.s[1] = a.s1;
+    g.xs = a.xs;
+    g.y = a.y;
+    g.ys = a.ys;
+    g.M = a.M;
+    g.T = static_cast<int>(a.T);
+    g.KB = static_cast<int>((a.K + kBlk - 1) / kBlk);
+    g.tilesM = static_cast<int>((a.M + (DUAL ? kHalf : kTile) - 1) / (DUAL ? kHalf : kTile));
+    g.tilesT = static_cast<int>((a.T + kTile - 1) / kTile);
+    g.blocksM = static_cast<int>((a.M + 127) / 128);
+    g.y_type = a.y_type;
+    const int64_t size = a.y_type == BQD_F32 ? 4 : a.y_type == BQD_BF16 ? 2 : 1, pitch = a.M * size;
+    g.align = static_cast<int>(pitch % 16 == 0 ? 16 : pitch % 4 == 0 ? 4 : size);
+    const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, pairs = dev_info(dev).sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel itself waits for the one before it
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, w0, w1, x, g);
+}
+
+}  // namespace
+
+bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual) { return a.T > 512; }
+
+cudaError_t launch_fp8_gemm_pairs(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
+{
+    return dual ? launch<true>(a, s) : launch<false>(a, s);
+}
+
+cudaError_t read_and_clear_fp8_pairs_error(unsigned int* out)
+{
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_pairs_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    *out = v;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_fp8_pairs_error, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace bqd
