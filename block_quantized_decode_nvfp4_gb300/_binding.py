@@ -407,20 +407,23 @@ def token_logprobs_workspace_bytes(T, V, topk) -> int:
     return lib().token_logprobs_workspace_bytes(T, V, topk)
 
 
+def _elsewhere(where, a, dev):
+    raise ValueError(f"{where}: a tensor on {a.device}, the current device is cuda:{dev}")
+
+
+_current_device = None  # torch's current device, by its own shortcut
+
+
 def _here(where, *tensors):
     """Addresses of a call's tensors (None and integers as they are), all of the current device."""
-    import torch
-    dev, out = None, []
-    for a in tensors:
-        if a is None or isinstance(a, int):
-            out.append(a)
-            continue
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if a.get_device() != dev:
-            raise ValueError(f"{where}: a tensor on {a.device}, the current device is cuda:{dev}")
-        out.append(a.data_ptr())
-    return out
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        torch.cuda.current_stream()  # initialises CUDA, or raises
+    dev = _current_device()
+    return [a if a is None or type(a) is int else a.data_ptr() if a.get_device() == dev else _elsewhere(where, a, dev)
+            for a in tensors]
 
 
 def fp8_x_encode(x, x_type, x_pitch, codes, scales, K, T, stream=None):

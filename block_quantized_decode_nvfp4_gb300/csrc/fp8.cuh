@@ -14,48 +14,73 @@
 namespace bqd {
 
 // ---------------------------------------------------------------- E4M3 blocks
-// Bits of |x|: their integer order is that of the values, with infinities and
-// then NaN above them, so the largest of a block also tells these.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// The scale of a block whose largest magnitude has these bits: amax / 448,
-// rounded once and at least the smallest normal fp32, so that no quotient
-// passes 448 by more than its rounding; NaN where the block has a NaN or an
-// infinity.
-__device__ __forceinline__ float block_scale(uint32_t amax)
+// The largest magnitude of three, NaN if there is one (an infinity is larger
+// than any number), so that a block's largest tells what the block holds.
+__device__ __forceinline__ float max_abs(float a, float b, float c)
 {
-    if (amax >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-    return fmaxf(__fdiv_rn(__uint_as_float(amax), 448.f), 1.17549435e-38f);
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_abs(float a, float b) { return max_abs(a, b, b); }
+
+// The scale of a block of largest magnitude amax: amax / 448, rounded once and
+// at least the smallest normal fp32, so that no quotient passes 448 by more than
+// its rounding; NaN where the block has a NaN or an infinity. The quotient is a
+// product with 1 / 448 and one step from its remainder (Markstein 1990), which
+// is exact down to that smallest scale.
+__device__ __forceinline__ float block_scale(float amax)
+{
+    constexpr float kInv = 1.f / 448.f;
+    const float q = amax * kInv, s = __fmaf_rn(__fmaf_rn(q, -448.f, amax), kInv, q);
+    return amax < INFINITY ? fmaxf(s, 1.17549435e-38f) : __uint_as_float(0x7FC00000u);
 }
 
 // Codes of quotients by one scale, each the fp32 quotient rounded to E4M3. A
 // product with the rounded reciprocal alone would now and then land on the
-// other side of a boundary between codes: one step from its remainder
-// (Markstein 1990) makes it the quotient, rounded once, as long as the
-// remainder keeps its bits (scales from 2^-60); smaller scales divide.
-struct BlockCoder {
-    float s, inv;
-    __device__ __forceinline__ explicit BlockCoder(float scale) : s(scale)
-    {
-        asm("rcp.rn.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+// other side of a boundary between codes: one step from its remainder makes it
+// the quotient, rounded once, as long as the remainder keeps its bits (scales
+// from 2^-60); smaller scales divide, and so does NaN.
+__device__ __forceinline__ uint32_t e4m3x2(uint64_t v)  // code of the first in the low byte
+{
+    float a, b;
+    unpack(v, a, b);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+// The quotients of v by s through its reciprocal; by division.
+template <int N>
+__device__ __forceinline__ void quotients(uint64_t (&v)[N], float s)
+{
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = __fmaf_rn(__fmaf_rn(-s, inv, 1.f), inv, inv);
+    const uint64_t i2 = pack(inv, inv), s2 = pack(-s, -s);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint64_t q = mul2(v[i], i2);
+        v[i] = fma2(fma2(q, s2, v[i]), i2, q);
     }
-    __device__ __forceinline__ uint32_t pair(uint64_t v) const  // code of the first in the low byte
-    {
+}
+template <int N>
+__device__ __forceinline__ void divide(uint64_t (&v)[N], float s)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
         float a, b;
-        if (s < 8.6736174e-19f) {  // 2^-60; false for NaN
-            unpack(v, a, b);
-            a = __fdiv_rn(a, s);
-            b = __fdiv_rn(b, s);
-        } else {
-            const uint64_t i2 = pack(inv, inv), q = mul2(v, i2);
-            unpack(fma2(fma2(q, pack(-s, -s), v), i2, q), a, b);
-        }
-        uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-        return r;
+        unpack(v[i], a, b);
+        v[i] = pack(__fdiv_rn(a, s), __fdiv_rn(b, s));
     }
-    __device__ __forceinline__ uint32_t one(float v) const { return pair(pack(v, v)) & 0xFFu; }
-};
+}
+template <int N>
+__device__ __forceinline__ void scale_down(uint64_t (&v)[N], float s)
+{
+    if (s >= 8.6736174e-19f)  // 2^-60; false for NaN
+        quotients(v, s);
+    else
+        divide(v, s);
+}
 
 __device__ __forceinline__ uint32_t to_bf16x2(float x, float y)
 {

@@ -59,12 +59,12 @@ struct Narrow {
     static constexpr int kRoom = (kCtas == 2 ? 109 * 1024 : 218 * 1024) - (kOver ? 0 : kParts);
     static constexpr int kStages = kRoom / kStage / 2 < 4 ? kRoom / kStage / 2 * 2 : 8;  // even: each for one warp
     static constexpr int kSmem = kStages * kStage + (kOver ? 0 : kParts) + 1024;  // + alignment slack
-    static constexpr int kBufs = 256 / BN < 4 ? 256 / BN : 4;
+    static constexpr int kBufs = 512 / kCtas / BN < 4 ? 512 / kCtas / BN : 4;
     static constexpr int kTmem = kBufs * BN;
     static constexpr int kCols = BN / kGroups;  // columns of a thread
-    static constexpr int kAhead = 4;            // blocks whose scales are on their way
+    static constexpr int kAhead = BN == 64 ? 2 : 4;  // blocks whose scales are on their way
     static_assert(BN % 16 == 0 && BN >= 16 && BN <= 128, "the MMA's N, and the threads' registers");
-    static_assert(kTmem >= 32 && kTmem <= 256 && (kTmem & (kTmem - 1)) == 0, "two CTAs share 512 columns");
+    static_assert(kTmem >= 32 && kTmem <= 512 / kCtas && (kTmem & (kTmem - 1)) == 0, "an SM's CTAs share 512 columns");
     static_assert(kStages >= 2 && kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
     static_assert(!kOver || kParts <= kStages * kStage, "the parts fit the ring");
     static_assert(kTileX % 1024 == 0, "stages start on 1024-byte boundaries (swizzle atoms)");
@@ -279,20 +279,22 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                     if (ok) ok = fp8_wait(&dfull[b], (it / S::kBufs) & 1, &g_fp8_error);
                     __syncwarp();  // the scales are there
                     tc_after();
-                    constexpr int C = BN > 64 ? 32 : 16;
+                    // all its columns at once where the registers allow it, so that the buffer is soon free
+                    constexpr int C = 16, D = C;
 #pragma unroll
-                    for (int c = 0; c < H; c += C) {
-                        uint32_t d[C];
-                        tmem_load<C>(base + b * BN + c, d);
+                    for (int c = 0; c < H; c += D) {
+                        uint32_t d[D];
+#pragma unroll
+                        for (int x = 0; x < D; x += C) tmem_load<C>(base + b * BN + c + x, d + x);
                         tmem_wait_ld();
-                        if (c + C == H) {  // the buffer has been read
+                        if (c + D == H) {  // the buffer has been read
                             tc_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&dempty[b]);
                         }
                         const float4* s4 = reinterpret_cast<const float4*>(sc + c);
 #pragma unroll
-                        for (int e = 0; e < C / 4; ++e) {
+                        for (int e = 0; e < D / 4; ++e) {
                             const float4 f = s4[e];
                             uint64_t* o = &acc[(c + 4 * e) / 2];
                             o[0] = fma2(pack(__uint_as_float(d[4 * e]), __uint_as_float(d[4 * e + 1])), pack(f.x, f.y), o[0]);
@@ -379,13 +381,14 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                 }
                 const int64_t t = n0 + rank + j * ranks;
                 if (g.y_type == BQD_E4M3) {
-                    uint32_t m = 0;
+                    float m = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m = max(m, e < live ? abs_bits(v[e]) : 0u);
-                    const float sc = block_scale(__reduce_max_sync(0xFFFFFFFFu, m));
-                    const BlockCoder coder(sc);
-                    store_codes4(static_cast<uint8_t*>(g.y) + t * g.M + row,
-                                 coder.pair(pack(v[0], v[1])) | (coder.pair(pack(v[2], v[3])) << 16), live, g.whole);
+                    for (int e = 0; e < 4; ++e) m = max_abs(m, e < live ? v[e] : 0.f);
+                    // (non-negative floats order as integers, NaN above all)
+                    const float sc = block_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
+                    uint64_t w[2] = {pack(v[0], v[1]), pack(v[2], v[3])};
+                    scale_down(w, sc);
+                    store_codes4(static_cast<uint8_t*>(g.y) + t * g.M + row, e4m3x2(w[0]) | (e4m3x2(w[1]) << 16), live, g.whole);
                     if (lane == 0) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
                 } else {
                     store_rows4(g.y, g.y_type, t * g.M + row, v, live, g.whole);

@@ -47,10 +47,9 @@ constexpr int kThreads = (4 + kSumWarps) * kWarp;
 constexpr int kLineBytes = 128;           // of a token's outputs, staged by a warp at once
 constexpr int kOut = kWarp * kLineBytes;  // staging of a warp
 constexpr int kSmem = kStages * kStage + kSumWarps * kOut + 1024;  // + alignment slack
-constexpr int kAhead = 4;                 // blocks whose scales are on their way
 constexpr int kGroup = 8;                 // token tiles that share a sweep over the weights
-// 128 x 80 + 256 x 208 of the 384 x 168 registers that the block has
-constexpr int kRegs = 168, kFewRegs = 80, kSumRegs = 208;
+// 128 x 56 + 256 x 224 are the 384 x 168 registers that the block has
+constexpr int kRegs = 168, kFewRegs = 56, kSumRegs = 224;
 static_assert(4 * kWarp * kFewRegs + kSumWarps * kWarp * kSumRegs <= kThreads * kRegs, "the split of the registers");
 static_assert(kSmem <= 227 * 1024 - 512, "shared memory of one CTA, static beside it");
 static_assert(kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
@@ -92,30 +91,34 @@ __device__ __forceinline__ void store_lines(uint8_t* stage, const uint4 (&v)[BYT
 #pragma unroll
     for (int i = 0; i < C; ++i) *reinterpret_cast<uint4*>(stage + lane * BYTES + ((i ^ (lane & (C - 1))) << 4)) = v[i];
     __syncwarp();
+    if (align == 16) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int t = i * (kWarp / C) + lane / C, c = lane & (C - 1);
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + t * BYTES + ((c ^ (t & (C - 1))) << 4));
+        for (int i = 0; i < C; ++i) {
+            const int t = i * (kWarp / C) + lane / C, c = lane & (C - 1);
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + t * BYTES + ((c ^ (t & (C - 1))) << 4));
+            if (t < tokens && 16 * c < left) *reinterpret_cast<uint4*>(at + t * pitch + 16 * c) = w;
+        }
+        return;
+    }
+    // rows that start anywhere: words, halves or bytes, neighbours by neighbouring lanes
+    constexpr int W = BYTES / 4;  // words of a line
+    const int c = lane & (W - 1);
+    const int64_t n = left - 4 * c;  // bytes of the row from this lane's
+#pragma unroll 4
+    for (int i = 0; i < W; ++i) {
+        const int t = i * (kWarp / W) + lane / W;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + t * BYTES + (((c / 4) ^ (t & (C - 1))) << 4) + c % 4 * 4);
         if (t >= tokens) continue;
-        uint8_t* p = at + t * pitch + c * 16;
-        const int64_t n = left - c * 16;  // bytes of the row from here
-        if (align == 16 && n >= 16) {
-            *reinterpret_cast<uint4*>(p) = w;
+        uint8_t* p = at + t * pitch + 4 * c;
+        if (align >= 4) {
+            if (n > 0) *reinterpret_cast<uint32_t*>(p) = w;
+        } else if (align == 2) {
+            if (n > 0) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w);
+            if (n > 2) *reinterpret_cast<uint16_t*>(p + 2) = static_cast<uint16_t>(w >> 16);
         } else {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (align >= 4 && n >= 4 * e + 4) {
-                    reinterpret_cast<uint32_t*>(p)[e] = x[e];
-                } else if (align == 2) {
-                    if (n >= 4 * e + 2) reinterpret_cast<uint16_t*>(p)[2 * e] = static_cast<uint16_t>(x[e]);
-                    if (n >= 4 * e + 4) reinterpret_cast<uint16_t*>(p)[2 * e + 1] = static_cast<uint16_t>(x[e] >> 16);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (n > 4 * e + b) p[4 * e + b] = static_cast<uint8_t>(x[e] >> (8 * b));
-                }
-            }
+            for (int b = 0; b < 4; ++b)
+                if (n > b) p[b] = static_cast<uint8_t>(w >> (8 * b));
         }
     }
 }
@@ -227,92 +230,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* ws0 = g.s[0] + static_cast<int64_t>(mb) * g.KB;
             const float* ws1 = DUAL ? g.s[1] + static_cast<int64_t>(mb) * g.KB : nullptr;
             const float* xs = g.xs + t;
-            uint64_t acc[64];
+            uint64_t sum[64];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = 0;
-            float far_x[kAhead], far_w[kAhead], far_u[kAhead];
-            auto fetch = [&](int slot, int i) {
-                far_x[slot] = i < g.KB && t < g.T ? __ldg(xs + static_cast<int64_t>(i) * g.T) : 0.f;
-                far_w[slot] = i < g.KB ? __ldg(ws0 + i) : 0.f;
-                if constexpr (DUAL) far_u[slot] = i < g.KB ? __ldg(ws1 + i) : 0.f;
+            for (int c = 0; c < 64; ++c) sum[c] = 0;
+            // a block's scales are on their way while the one before it is added up
+            float far_x, far_w, far_u = 0.f;
+            auto fetch = [&](int i) {
+                far_x = i < g.KB && t < g.T ? __ldg(xs + static_cast<int64_t>(i) * g.T) : 0.f;
+                far_w = i < g.KB ? __ldg(ws0 + i) : 0.f;
+                if constexpr (DUAL) far_u = i < g.KB ? __ldg(ws1 + i) : 0.f;
             };
+            fetch(0);
+            for (int i = 0; i < g.KB; ++i, ++it) {
+                const float f[2] = {far_x * far_w, DUAL ? far_x * far_u : far_x * far_w};
+                fetch(i + 1);
+                // a token's scale comes from the L2, which may take longer than a block: called into the L1
+                // one block before (the pair's three loads gained nothing from it)
+                if (!DUAL && i + 2 < g.KB && t < g.T)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(xs + static_cast<int64_t>(i + 2) * g.T));
+                const int b = it % kBufs;
+                // After a wait that ran out the loops go on without waiting, so that the warps
+                // still meet at every barrier.
+                if (ok) ok = fp8_wait(&dfull[b], (it / kBufs) & 1, &g_fp8_pairs_error);
+                __syncwarp();
+                tc_after();
+                // 64 columns at a time: the fewer loads wait for one another, the sooner is the buffer free
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) fetch(i, i);
-            for (int i0 = 0; i0 < g.KB; i0 += kAhead) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {  // a register of scales on their way may not be moved
-                    const int i = i0 + u;
-                    if (i >= g.KB) break;
-                    const float f0 = far_x[u] * far_w[u], f1 = DUAL ? far_x[u] * far_u[u] : f0;
-                    fetch(u, i + kAhead);
-                    const int b = it % kBufs;
-                    // After a wait that ran out the loops go on without waiting, so that the warps
-                    // still meet at every barrier.
-                    if (ok) ok = fp8_wait(&dfull[b], (it / kBufs) & 1, &g_fp8_pairs_error);
-                    __syncwarp();
-                    tc_after();
-                    // 16 columns at a time, the next on their way
-                    uint32_t d[2][16];
-                    tmem_load<16>(base + b * kTile + col0, d[0]);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t d[64];
+                    tmem_load<32>(base + b * kTile + (h ? col2 : col0), d);
+                    tmem_load<32>(base + b * kTile + (h ? col2 : col0) + 32, d + 32);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c < 7) tmem_load<16>(base + b * kTile + (c < 3 ? col0 + 16 * (c + 1) : col2 + 16 * (c - 3)), d[(c + 1) & 1]);
-                        const float f = c < 4 ? f0 : f1;
-                        const uint64_t ff = pack(f, f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            acc[8 * c + e] = fma2(pack(__uint_as_float(d[c & 1][2 * e]), __uint_as_float(d[c & 1][2 * e + 1])),
-                                                  ff, acc[8 * c + e]);
-                        if (c < 7) tmem_wait_ld();
-                        if (c == 6) {  // the buffer has been read
-                            tc_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_cluster(free0 + b * 8);
-                        }
+                    if (h) {  // the buffer has been read
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(free0 + b * 8);
                     }
-                    ++it;
+                    const uint64_t ff = pack(f[h], f[h]);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        sum[32 * h + e] = fma2(pack(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])), ff, sum[32 * h + e]);
                 }
             }
             // ---- the tile's outputs
+            float acc[128];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) unpack(sum[c], acc[2 * c], acc[2 * c + 1]);
             const int tok0 = tt * kTile + rank * kHalf + 32 * q, tokens = g.T - tok0;
-            auto value = [&](int c) {
-                float x, y;
-                unpack(acc[c / 2], x, y);
-                return c & 1 ? y : x;
-            };
             const int64_t m0 = DUAL ? static_cast<int64_t>(mt) * kHalf + 64 * half : static_cast<int64_t>(mt) * kTile + kHalf * half;
             constexpr int N = DUAL ? 64 : 128;  // outputs of a thread
             if constexpr (DUAL) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float g0, g1, u0, u1;
-                    unpack(acc[c], g0, g1);
-                    unpack(acc[32 + c], u0, u1);
-                    acc[c] = pack(silu_mul(g0, u0), silu_mul(g1, u1));
-                }
+                for (int c = 0; c < 64; ++c) acc[c] = silu_mul(acc[c], acc[64 + c]);
             }
             const int64_t left = g.M - m0;  // elements of the row from this thread's first
             if (DUAL && g.y_type == BQD_E4M3) {
-                uint32_t most = 0;
+                float most = 0.f;
 #pragma unroll
-                for (int c = 0; c < N; ++c)
-                    if (c < left) most = max(most, abs_bits(value(c)));
+                for (int c = 0; c < N; c += 2) most = max_abs(most, c < left ? acc[c] : 0.f, c + 1 < left ? acc[c + 1] : 0.f);
                 // with the warp that has the other half of these tokens: past the codes' lines in its
                 // staging, at another place for the next tile
                 const int seen = kOut / 2 + turn * (4 * kWarp) + 4 * lane;
-                *reinterpret_cast<uint32_t*>(stage + seen) = most;
+                *reinterpret_cast<float*>(stage + seen) = most;
                 named_sync(1 + q, 2 * kWarp);
-                const float sc = block_scale(max(most, *reinterpret_cast<const uint32_t*>(stage + (half ? -4 : 4) * kOut + seen)));
-                const BlockCoder coder(sc);
+                const float sc = block_scale(max_abs(most, *reinterpret_cast<const float*>(stage + (half ? -4 : 4) * kOut + seen)));
                 if (half == 0 && t < g.T) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
                 uint4 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4];
+                    uint64_t w[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = coder.pair(acc[8 * i + 2 * e]) | (coder.pair(acc[8 * i + 2 * e + 1]) << 16);
-                    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 8; ++e) w[e] = pack(acc[16 * i + 2 * e], acc[16 * i + 2 * e + 1]);
+                    scale_down(w, sc);
+                    v[i] = make_uint4(e4m3x2(w[0]) | (e4m3x2(w[1]) << 16), e4m3x2(w[2]) | (e4m3x2(w[3]) << 16),
+                                      e4m3x2(w[4]) | (e4m3x2(w[5]) << 16), e4m3x2(w[6]) | (e4m3x2(w[7]) << 16));
                 }
                 store_lines<64>(stage, v, static_cast<uint8_t*>(g.y) + static_cast<int64_t>(tok0) * g.M + m0, g.M, left, tokens,
                                 g.align);
@@ -324,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 8; ++i) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = to_bf16x2(value(64 * k + 8 * i + 2 * e), value(64 * k + 8 * i + 2 * e + 1));
+                        for (int e = 0; e < 4; ++e) w[e] = to_bf16x2(acc[64 * k + 8 * i + 2 * e], acc[64 * k + 8 * i + 2 * e + 1]);
                         v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 2 * (static_cast<int64_t>(tok0) * g.M + m0 + 64 * k),
@@ -336,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = make_uint4(__float_as_uint(value(32 * k + 4 * i)), __float_as_uint(value(32 * k + 4 * i + 1)),
-                                          __float_as_uint(value(32 * k + 4 * i + 2)), __float_as_uint(value(32 * k + 4 * i + 3)));
+                        v[i] = make_uint4(__float_as_uint(acc[32 * k + 4 * i]), __float_as_uint(acc[32 * k + 4 * i + 1]),
+                                          __float_as_uint(acc[32 * k + 4 * i + 2]), __float_as_uint(acc[32 * k + 4 * i + 3]));
                     store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 4 * (static_cast<int64_t>(tok0) * g.M + m0 + 32 * k),
                                      4 * g.M, 4 * (left - 32 * k), tokens, g.align);
                 }
@@ -411,7 +402,24 @@ cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t s)
 
 }  // namespace
 
-bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual) { return a.T > 512; }
+// Up to 64 tokens the weights' one read is the bound, and a CTA of fp8_gemm.cu
+// takes tokens by 16. Beyond that a block of k takes either kernel about as long
+// (0.45 us; 128 x 128 there, twice that here), so the one that goes through fewer
+// of them does it sooner. Measured, us there and here: 12288 x 4096 by 256 tokens
+// 36 and 22, 4096 x 4096 by 256 16 and 20, 4096 x 12288 by 512 48 and 48.
+bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual)
+{
+    if (a.T <= 64) return false;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const int64_t sms = dev_info(dev).sms > 1 ? dev_info(dev).sms : 2, KB = (a.K + kBlk - 1) / kBlk;
+    const int64_t alone = (a.M + 127) / 128 * ((a.T + 127) / 128) * (dual ? 2 : 1);
+    const int64_t share = alone < sms ? sms / alone : 1;  // CTAs that share a tile's k
+    const int64_t rows = dual ? kHalf : kTile, tiles = (a.M + rows - 1) / rows * ((a.T + kTile - 1) / kTile);
+    const int64_t there = (alone * share + sms - 1) / sms * ((KB + share - 1) / share);
+    const int64_t here = (tiles + sms / 2 - 1) / (sms / 2) * KB;
+    return here <= there;
+}
 
 cudaError_t launch_fp8_gemm_pairs(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
 {
