@@ -47,6 +47,8 @@ struct Fp8GemmArgs {
 };
 // Codes [rows][K] in boxes of 128 k x `box` rows (a CUtensorMap); k and rows past the ends read as zero.
 bool fp8_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
+// The kernel for more than 64 tokens (fp8_gemm_tokens.cu).
+cudaError_t launch_fp8_gemm_tokens(const Fp8GemmArgs& a, bool dual, cudaStream_t s);
 // The kernel for many tokens (fp8_gemm_pairs.cu), and whether the sizes are its.
 bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual);
 cudaError_t launch_fp8_gemm_pairs(const Fp8GemmArgs& a, bool dual, cudaStream_t s);
@@ -54,5 +56,6 @@ bool fp8_gemm_supported(int64_t M, int64_t K, int64_t T);
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dual, cudaStream_t s);
 cudaError_t read_and_clear_fp8_error(unsigned int* out);
 cudaError_t read_and_clear_fp8_pairs_error(unsigned int* out);
+cudaError_t read_and_clear_fp8_tokens_error(unsigned int* out);
 
 }  // namespace bqd

@@ -31,6 +31,7 @@
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "fp8.cuh"
+#include "fp8_gemm.cuh"
 #include "fp8.h"
 #include "host_util.h"
 #include "stream.cuh"
@@ -41,82 +42,31 @@ __device__ unsigned int g_fp8_error = 0;
 
 namespace {
 
-constexpr int kRows = 128;             // weight rows of a tile (MMA M), and of a tile of scales
-constexpr int kBlk = 128;              // k of a block of scales and of a ring stage
-constexpr int kTileW = kRows * kBlk;   // bytes
-constexpr int kMaxCluster = 8;
+using namespace fp8;
 
 template <int BN>
 struct Narrow {
-    static constexpr int kCtas = BN > 64 ? 1 : 2;  // per SM
+    static constexpr int kCtas = 2;  // per SM
     static constexpr int kSumWarps = BN > 32 ? 8 : 4;
     static constexpr int kGroups = kSumWarps / 4;  // of 128 threads, a row of the weights each
     static constexpr int kThreads = (4 + kSumWarps) * kWarp;
     static constexpr int kTileX = BN * kBlk;
-    static constexpr int kStage = kTileW + kTileX;
+    static constexpr int kStage = kTileBytes + kTileX;
     static constexpr int kParts = (BN + kMaxCluster - 1) * kRows * 4;  // a cluster's parts of this CTA's tokens
     static constexpr bool kOver = BN > 32;  // they lie over the ring: its room is worth more than a barrier
-    static constexpr int kRoom = (kCtas == 2 ? 109 * 1024 : 218 * 1024) - (kOver ? 0 : kParts);
+    static constexpr int kRoom = 109 * 1024 - (kOver ? 0 : kParts);
     static constexpr int kStages = kRoom / kStage / 2 < 4 ? kRoom / kStage / 2 * 2 : 8;  // even: each for one warp
     static constexpr int kSmem = kStages * kStage + (kOver ? 0 : kParts) + 1024;  // + alignment slack
     static constexpr int kBufs = 512 / kCtas / BN < 4 ? 512 / kCtas / BN : 4;
     static constexpr int kTmem = kBufs * BN;
     static constexpr int kCols = BN / kGroups;  // columns of a thread
     static constexpr int kAhead = BN == 64 ? 2 : 4;  // blocks whose scales are on their way
-    static_assert(BN % 16 == 0 && BN >= 16 && BN <= 128, "the MMA's N, and the threads' registers");
+    static_assert(BN % 16 == 0 && BN >= 16 && BN <= 64, "the MMA's N, and the threads' registers");
     static_assert(kTmem >= 32 && kTmem <= 512 / kCtas && (kTmem & (kTmem - 1)) == 0, "an SM's CTAs share 512 columns");
     static_assert(kStages >= 2 && kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
     static_assert(!kOver || kParts <= kStages * kStage, "the parts fit the ring");
     static_assert(kTileX % 1024 == 0, "stages start on 1024-byte boundaries (swizzle atoms)");
 };
-
-struct GemmShape {
-    const float *s[2], *xs;
-    void* y;
-    float* ys;
-    int64_t M;
-    int T, KB;           // tokens, blocks of k
-    int tilesM, tilesT;  // tile = row tile * tilesT + token tile
-    int mats;            // 2: a gated pair
-    int y_type;
-    int whole;           // y's rows are so aligned that four elements of one may be stored at once
-    int early;           // weights may be read before the previous kernel has completed
-};
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
-
-__device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v)
-{
-    if (type == BQD_F32)
-        static_cast<float*>(y)[at] = v;
-    else
-        static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-}
-
-// Four consecutive elements of a row of y, the first `live` of which there are.
-__device__ __forceinline__ void store_codes4(uint8_t* p, uint32_t codes, int live, bool whole)
-{
-    if (whole && live == 4) {
-        *reinterpret_cast<uint32_t*>(p) = codes;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < live) p[e] = static_cast<uint8_t>(codes >> (8 * e));
-    }
-}
-__device__ __forceinline__ void store_rows4(void* y, int type, int64_t at, const float (&v)[4], int live, bool whole)
-{
-    if (whole && live == 4) {
-        if (type == BQD_F32)
-            *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = make_uint2(to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < live) store_y(y, type, at + e, v[e]);
-    }
-}
 
 template <int BN>
 __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
@@ -186,7 +136,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                 tma_2d(smem_u32(ring + st * S::kStage), map_w, kb * kBlk, tile / g.tilesT * kRows, &full[st]);
             };
             auto copy_x = [&](int st, int tile, int kb) {
-                tma_2d(smem_u32(ring + st * S::kStage + kTileW), &map_x, kb * kBlk, tile % g.tilesT * BN, &full[st]);
+                tma_2d(smem_u32(ring + st * S::kStage + kTileBytes), &map_x, kb * kBlk, tile % g.tilesT * BN, &full[st]);
             };
             // the first stages' weights before the wait for the previous kernel, whose output x may be
             const int first = min(S::kStages, nkb);
@@ -229,7 +179,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                     const uint32_t at = smem_u32(ring + st * S::kStage);
 #pragma unroll
                     for (int j = 0; j < kBlk / 32; ++j)
-                        fp8_mma(tmem + b * BN, fp8_desc(at + 32 * j), fp8_desc(at + kTileW + 32 * j), idesc, j != 0 ? 1u : 0u);
+                        fp8_mma(tmem + b * BN, fp8_desc(at + 32 * j), fp8_desc(at + kTileBytes + 32 * j), idesc, j != 0 ? 1u : 0u);
                     fp8_commit(&empty[st]);
                     fp8_commit(&dfull[b]);
                 }
@@ -279,13 +229,11 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                     if (ok) ok = fp8_wait(&dfull[b], (it / S::kBufs) & 1, &g_fp8_error);
                     __syncwarp();  // the scales are there
                     tc_after();
-                    // all its columns at once where the registers allow it, so that the buffer is soon free
-                    constexpr int C = 16, D = C;
+                    constexpr int D = 16;  // columns at a time
 #pragma unroll
                     for (int c = 0; c < H; c += D) {
                         uint32_t d[D];
-#pragma unroll
-                        for (int x = 0; x < D; x += C) tmem_load<C>(base + b * BN + c + x, d + x);
+                        tmem_load<D>(base + b * BN + c, d);
                         tmem_wait_ld();
                         if (c + D == H) {  // the buffer has been read
                             tc_before();
@@ -355,45 +303,11 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                 cluster_wait();
             }
         } else {
-            // a token per warp at a time, four rows a lane
-            const int mt = tile0 / g.tilesT, n0 = tile0 % g.tilesT * BN, here = min(BN, g.T - n0);
-            const int most = (here + ranks - 1) / ranks, n = (here - rank + ranks - 1) / ranks;
-            const int64_t row = static_cast<int64_t>(mt) * kRows + 4 * lane;
-            const int live = static_cast<int>(min(static_cast<int64_t>(4), max(static_cast<int64_t>(0), g.M - row)));
             // (four times the limit of the other waits: a CTA that gives up one of those still stores)
             if (!fp8_wait_cluster(&got, 0, &g_fp8_error, 4 * kWaitCycles)) ok = false;
-            for (int j = warp - 4; j < n; j += S::kSumWarps) {
-                const float4* part = reinterpret_cast<const float4*>(parts + j * kRows) + lane;
-                const int step4 = most * (kRows / 4);  // to the next part
-                float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-                for (int k = 0; k < ranks; k += g.mats) {  // over the blocks of k, in order
-                    const float4 p = part[k * step4];
-                    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-                    if (g.mats > 1) {
-                        const float4 w = part[(k + 1) * step4];
-                        u[0] += w.x, u[1] += w.y, u[2] += w.z, u[3] += w.w;
-                    }
-                }
-                if (g.mats > 1) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], u[e]);
-                }
-                const int64_t t = n0 + rank + j * ranks;
-                if (g.y_type == BQD_E4M3) {
-                    float m = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m = max_abs(m, e < live ? v[e] : 0.f);
-                    // (non-negative floats order as integers, NaN above all)
-                    const float sc = block_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
-                    uint64_t w[2] = {pack(v[0], v[1]), pack(v[2], v[3])};
-                    scale_down(w, sc);
-                    store_codes4(static_cast<uint8_t*>(g.y) + t * g.M + row, e4m3x2(w[0]) | (e4m3x2(w[1]) << 16), live, g.whole);
-                    if (lane == 0) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
-                } else {
-                    store_rows4(g.y, g.y_type, t * g.M + row, v, live, g.whole);
-                }
-            }
+            const int n0 = tile0 % g.tilesT * BN, here = min(BN, g.T - n0);
+            finish_tokens<false>(g, parts, (here + ranks - 1) / ranks, (here - rank + ranks - 1) / ranks, ranks, tile0 / g.tilesT,
+                                 n0 + rank, ranks, 0, warp - 4, S::kSumWarps);
         }
     }
     __syncthreads();
@@ -401,42 +315,6 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem) : "memory");
     }
-}
-
-// Clusters of `ranks` CTAs that run at once on the device: fewer than its slots
-// hold, as a cluster stays within a group of SMs. Cached.
-template <int BN>
-int clusters_at_once(int dev, int ranks)
-{
-    using S = Narrow<BN>;
-    static std::mutex mu;
-    static int known[64][kMaxCluster + 1];
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64) return 0;
-    int& n = known[dev][ranks];
-    if (n == 0) {
-        if (cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-            cudaGetLastError();
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(ranks * S::kCtas * dev_info(dev).sms));
-        cfg.blockDim = dim3(S::kThreads);
-        cfg.dynamicSmemBytes = S::kSmem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int found = 0;
-        if (cudaOccupancyMaxActiveClusters(&found, fp8_gemm_kernel<BN>, &cfg) != cudaSuccess) {
-            cudaGetLastError();  // consumed: it must not surface as a launch error later
-            return 0;
-        }
-        n = found > 0 ? found : -1;
-    }
-    return n;
 }
 
 template <int BN>
@@ -470,33 +348,14 @@ cudaError_t launch_narrow(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
     g.y_type = a.y_type;
     g.whole = a.M % 4 == 0;  // y starts on 16 bytes
     g.early = (launch_flags() & kLaunchPdl) != 0;
-    // the k blocks of a tile over as many CTAs as may be with every cluster running at once (with
-    // one weight and many tiles: a CTA for tile after tile)
+    // the k blocks of a tile over as many CTAs as may be (with one weight and many tiles: a CTA
+    // for tile after tile)
     const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, slots = static_cast<int64_t>(dev_info(dev).sms) * S::kCtas;
-    int cs = kMaxCluster / g.mats < g.KB ? kMaxCluster / g.mats : g.KB;
-    while (cs > 1 && (tiles * cs * g.mats > slots || tiles > S::kCtas * clusters_at_once<BN>(dev, cs * g.mats))) --cs;
-    const int ranks = cs * g.mats;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : tiles < slots ? tiles : slots));
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    // the kernel itself waits for the one before it, ahead of its first access to memory (but
-    // for the weights, if the launch flags allow that), so its start may overlap the other's end
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    int na = 1;
-    if (ranks > 1) {
-        attr[na].id = cudaLaunchAttributeClusterDimension;
-        attr[na].val.clusterDim.x = static_cast<unsigned>(ranks);
-        attr[na].val.clusterDim.y = 1;
-        attr[na].val.clusterDim.z = 1;
-        ++na;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = static_cast<unsigned>(na);
-    return cudaLaunchKernelEx(&cfg, kern, w0, w1, x, g);
+    static ClusterCache clusters;
+    const int ranks =
+        g.mats * share_k(clusters, reinterpret_cast<const void*>(kern), dev, S::kThreads, S::kSmem, S::kCtas, tiles, g.mats, g.KB);
+    return launch_clusters(kern, static_cast<unsigned>(ranks > 1 ? tiles * ranks : tiles < slots ? tiles : slots), ranks,
+                           S::kThreads, S::kSmem, s, w0, w1, x, g);
 }
 
 }  // namespace
@@ -546,16 +405,18 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
     if (a.T <= 16) return launch_narrow<16>(a, dual, s);
     if (a.T <= 32) return launch_narrow<32>(a, dual, s);
     if (a.T <= 64) return launch_narrow<64>(a, dual, s);
-    return launch_narrow<128>(a, dual, s);
+    return launch_fp8_gemm_tokens(a, dual, s);
 }
 
 cudaError_t read_and_clear_fp8_error(unsigned int* out)
 {
     unsigned int v = 0, w = 0;
+    unsigned int x = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_error, sizeof(v));
     if (e == cudaSuccess) e = read_and_clear_fp8_pairs_error(&w);
+    if (e == cudaSuccess) e = read_and_clear_fp8_tokens_error(&x);
     if (e != cudaSuccess) return e;
-    *out = v | w;
+    *out = v | w | x;
     if (v) {
         const unsigned int zero = 0;
         e = cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof(zero));

@@ -25,6 +25,7 @@
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "fp8.cuh"
+#include "fp8_gemm.cuh"
 #include "fp8.h"
 #include "host_util.h"
 #include "stream.cuh"
@@ -35,7 +36,7 @@ __device__ unsigned int g_fp8_pairs_error = 0;
 
 namespace {
 
-constexpr int kBlk = 128;                 // k of a block of scales and of a ring stage
+using namespace fp8;
 constexpr int kHalf = 128;                // tokens and weight rows of a CTA's half
 constexpr int kTile = 2 * kHalf;          // tokens of a tile (MMA M), columns of a buffer (N)
 constexpr int kHalfBytes = kHalf * kBlk;
@@ -63,7 +64,7 @@ struct PairShape {
     int tilesM, tilesT;
     int blocksM;  // of 128 rows
     int y_type;
-    int align;    // bytes to which every row of y is aligned: 16, 4, or an element's
+    int align;    // of y's rows: see row_align
 };
 
 // Tile i: kGroup token tiles under each tile of the weights, group after group.
@@ -73,54 +74,6 @@ __device__ __forceinline__ void find_tile(const PairShape& g, int i, int& mt, in
     const int wide = min(kGroup, g.tilesT - group * kGroup);
     mt = in / wide;
     tt = group * kGroup + in - mt * wide;
-}
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
-
-// A warp's 32 tokens x BYTES of outputs, as lane l has token l's in v, to rows of
-// y: through shared memory, so that a store has whole lines. at: bytes from y to
-// token 0's; pitch: bytes of a row; left: bytes of the row from `at`; tokens: how
-// many there are.
-template <int BYTES>
-__device__ __forceinline__ void store_lines(uint8_t* stage, const uint4 (&v)[BYTES / 16], uint8_t* at, int64_t pitch,
-                                            int64_t left, int tokens, int align)
-{
-    constexpr int C = BYTES / 16;  // 16-byte pieces of a line
-    const int lane = threadIdx.x % kWarp;
-    __syncwarp();  // what was staged before has been read
-#pragma unroll
-    for (int i = 0; i < C; ++i) *reinterpret_cast<uint4*>(stage + lane * BYTES + ((i ^ (lane & (C - 1))) << 4)) = v[i];
-    __syncwarp();
-    if (align == 16) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int t = i * (kWarp / C) + lane / C, c = lane & (C - 1);
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + t * BYTES + ((c ^ (t & (C - 1))) << 4));
-            if (t < tokens && 16 * c < left) *reinterpret_cast<uint4*>(at + t * pitch + 16 * c) = w;
-        }
-        return;
-    }
-    // rows that start anywhere: words, halves or bytes, neighbours by neighbouring lanes
-    constexpr int W = BYTES / 4;  // words of a line
-    const int c = lane & (W - 1);
-    const int64_t n = left - 4 * c;  // bytes of the row from this lane's
-#pragma unroll 4
-    for (int i = 0; i < W; ++i) {
-        const int t = i * (kWarp / W) + lane / W;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + t * BYTES + (((c / 4) ^ (t & (C - 1))) << 4) + c % 4 * 4);
-        if (t >= tokens) continue;
-        uint8_t* p = at + t * pitch + 4 * c;
-        if (align >= 4) {
-            if (n > 0) *reinterpret_cast<uint32_t*>(p) = w;
-        } else if (align == 2) {
-            if (n > 0) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w);
-            if (n > 2) *reinterpret_cast<uint16_t*>(p + 2) = static_cast<uint16_t>(w >> 16);
-        } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (n > b) p[b] = static_cast<uint8_t>(w >> (8 * b));
-        }
-    }
 }
 
 template <bool DUAL>
@@ -380,33 +333,20 @@ cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t s)
     g.tilesT = static_cast<int>((a.T + kTile - 1) / kTile);
     g.blocksM = static_cast<int>((a.M + 127) / 128);
     g.y_type = a.y_type;
-    const int64_t size = a.y_type == BQD_F32 ? 4 : a.y_type == BQD_BF16 ? 2 : 1, pitch = a.M * size;
-    g.align = static_cast<int>(pitch % 16 == 0 ? 16 : pitch % 4 == 0 ? 4 : size);
+    g.align = row_align(a.M, a.y_type);
     const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, pairs = dev_info(dev).sms / 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel itself waits for the one before it
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, w0, w1, x, g);
+    return launch_clusters(kern, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 2, kThreads, kSmem, s, w0, w1, x, g);
 }
 
 }  // namespace
 
-// Up to 64 tokens the weights' one read is the bound, and a CTA of fp8_gemm.cu
-// takes tokens by 16. Beyond that a block of k takes either kernel about as long
-// (0.45 us; 128 x 128 there, twice that here), so the one that goes through fewer
-// of them does it sooner. Measured, us there and here: 12288 x 4096 by 256 tokens
-// 36 and 22, 4096 x 4096 by 256 16 and 20, 4096 x 12288 by 512 48 and 48.
+// Up to 64 tokens the weights' one read is the bound, and fp8_gemm.cu takes tokens
+// by 16. Beyond that a block of k takes a CTA of fp8_gemm_tokens.cu 0.35 us and a
+// pair here, with four times the products, 0.45 us: the kernel that goes through
+// fewer blocks one after the other is the sooner done. Measured, us there and here:
+// 12288 x 4096 by 256 tokens (64 blocks there, 32 here) 31 and 21, 4096 x 4096 by 256
+// (16, 32) 16 and 18, 4096 x 12288 by 512 (96, 96) 40 and 43, 4870 x 4096 by 1000
+// (96, 64) 41 and 36; gated 6144 x 4096 by 100 (32, 32) 22 and 21.
 bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual)
 {
     if (a.T <= 64) return false;
@@ -418,7 +358,7 @@ bool fp8_gemm_wants_pairs(const Fp8GemmArgs& a, bool dual)
     const int64_t rows = dual ? kHalf : kTile, tiles = (a.M + rows - 1) / rows * ((a.T + kTile - 1) / kTile);
     const int64_t there = (alone * share + sms - 1) / sms * ((KB + share - 1) / share);
     const int64_t here = (tiles + sms / 2 - 1) / (sms / 2) * KB;
-    return here <= there;
+    return dual ? here <= there : here < there;
 }
 
 cudaError_t launch_fp8_gemm_pairs(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
