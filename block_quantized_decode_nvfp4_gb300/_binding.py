@@ -414,44 +414,55 @@ def _elsewhere(where, a, dev):
 _current_device = None  # torch's current device, by its own shortcut
 
 
-def _here(where, *tensors):
-    """Addresses of a call's tensors (None and integers as they are), all of the current device."""
+def _here(where, stream, *tensors):
+    """Addresses of a call's tensors (None and integers as they are), all of the current device, and the handle of its
+    stream, the current one of that device where none is given."""
     global _current_device
     if _current_device is None:
         import torch
+        _find_current_raw_stream()  # initialises CUDA, or raises
         _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-        torch.cuda.current_stream()  # initialises CUDA, or raises
     dev = _current_device()
-    return [a if a is None or type(a) is int else a.data_ptr() if a.get_device() == dev else _elsewhere(where, a, dev)
-            for a in tensors]
+    at = [a if a is None or type(a) is int else a.data_ptr() if a.get_device() == dev else _elsewhere(where, a, dev)
+          for a in tensors]
+    at.append(_current_raw_stream() if stream is None else _stream(stream))
+    return at
 
 
 def fp8_x_encode(x, x_type, x_pitch, codes, scales, K, T, stream=None):
     """8-bit activations of rows [T][K]: E4M3 codes [T][K], fp32 scales [ceil(K/128)][T]."""
-    x, codes, scales = _here("fp8_x_encode", x, codes, scales)
-    _check(lib().fp8_x_encode(x, x_type, x_pitch, codes, scales, K, T, _stream(stream)), "fp8_x_encode")
+    x, codes, scales, stream = _here("fp8_x_encode", stream, x, codes, scales)
+    status = (_lib or lib()).fp8_x_encode(x, x_type, x_pitch, codes, scales, K, T, stream)
+    if status:
+        raise BqdError(status, "fp8_x_encode")
 
 
 def residual_norm(x, x_type, x_pitch, post_weight, gate, gate_type, gate_pitch, residual_scale, residual, residual_out,
                   residual_type, pre_weight, eps, y, y_type, y_scales, H, T, stream=None):
     """Residual add of a block's output (its norm, gate and scale), then the next block's norm: y bf16 or E4M3."""
-    x, post_weight, gate, residual, residual_out, pre_weight, y, y_scales = _here(
-        "residual_norm", x, post_weight, gate, residual, residual_out, pre_weight, y, y_scales)
-    _check(lib().residual_norm(x, x_type, x_pitch, post_weight, gate, gate_type, gate_pitch, residual_scale, residual,
-                               residual_out, residual_type, pre_weight, eps, y, y_type, y_scales, H, T,
-                               _stream(stream)), "residual_norm")
+    x, post_weight, gate, residual, residual_out, pre_weight, y, y_scales, stream = _here(
+        "residual_norm", stream, x, post_weight, gate, residual, residual_out, pre_weight, y, y_scales)
+    status = (_lib or lib()).residual_norm(x, x_type, x_pitch, post_weight, gate, gate_type, gate_pitch, residual_scale,
+                                           residual, residual_out, residual_type, pre_weight, eps, y, y_type, y_scales, H,
+                                           T, stream)
+    if status:
+        raise BqdError(status, "residual_norm")
 
 
 def fp8_b128_gemm(codes, scales, x, x_scales, y, y_type, M, K, T, stream=None):
     """8-bit activations [T][K] times FP8 block-128 weights [M][K]: y [T][M], fp32 or bf16."""
-    codes, scales, x, x_scales, y = _here("fp8_b128_gemm", codes, scales, x, x_scales, y)
-    _check(lib().fp8_b128_gemm(codes, scales, x, x_scales, y, y_type, M, K, T, _stream(stream)), "fp8_b128_gemm")
+    codes, scales, x, x_scales, y, stream = _here("fp8_b128_gemm", stream, codes, scales, x, x_scales, y)
+    status = (_lib or lib()).fp8_b128_gemm(codes, scales, x, x_scales, y, y_type, M, K, T, stream)
+    if status:
+        raise BqdError(status, "fp8_b128_gemm")
 
 
 def fp8_b128_gemm_silu_mul(gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_type, h_scales, I, K, T,
                            stream=None):
     """SiLU(gate) * up of 8-bit activations in one kernel: h [T][I], fp32, bf16 or E4M3 with scales."""
-    gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_scales = _here(
-        "fp8_b128_gemm_silu_mul", gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_scales)
-    _check(lib().fp8_b128_gemm_silu_mul(gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_type, h_scales,
-                                        I, K, T, _stream(stream)), "fp8_b128_gemm_silu_mul")
+    gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_scales, stream = _here(
+        "fp8_b128_gemm_silu_mul", stream, gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_scales)
+    status = (_lib or lib()).fp8_b128_gemm_silu_mul(gate_codes, gate_scales, up_codes, up_scales, x, x_scales, h, h_type,
+                                                    h_scales, I, K, T, stream)
+    if status:
+        raise BqdError(status, "fp8_b128_gemm_silu_mul")

@@ -98,6 +98,15 @@ def test_ffn_sizes(I, K, T, kind):
     check_ffn(Data(I, K, T, n=2, seed=I + K + T, lo=-16, hi=-6), kind)
 
 
+# more tiles than CTAs, so that each takes one after the other; a K of many blocks shared by eight CTAs
+@pytest.mark.parametrize("M,K,T", [(40000, 272, 20), (40000, 144, 40), (30000, 272, 100), (20000, 144, 700), (130, 16384, 40),
+                                   (130, 16384, 100), (130, 1152, 100)])
+def test_gemm_many_tiles_and_long_k(M, K, T):
+    check_gemm(Data(M, K, T, seed=21))
+    if M < 30000:
+        check_ffn(Data(M, K, T, n=2, seed=22, lo=-16, hi=-6), "e4m3")
+
+
 @pytest.mark.parametrize("M,K,T", [(12288, 4096, 1), (4096, 12288, 17), (4870, 4096, 333)])
 def test_gemm_of_a_layer(M, K, T):
     check_gemm(Data(M, K, T, seed=7))
@@ -265,3 +274,22 @@ def test_dependent_launches(norm):
         got.append((y.clone(), d.x.clone(), d.dxs.clone()))
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got))
     assert not norm or bool(y.isfinite().all())
+
+
+@pytest.mark.parametrize("M,T", [(72000, 33000), (36000000, 64), (400000, 6000)])
+def test_outputs_past_32_bits(M, T):
+    # y holds more than 2^31 elements; sampled rows and columns against the definition
+    K = 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randint(0, 0x7E, (M, K), dtype=torch.uint8, generator=g, device="cuda")
+    x = torch.randint(0, 0x7E, (T, K), dtype=torch.uint8, generator=g, device="cuda")
+    ws, xs = torch.rand(-(-M // 128), 1, generator=g, device="cuda"), torch.rand(1, T, generator=g, device="cuda")
+    y = torch.full((T, M), -1.0, dtype=torch.bfloat16, device="cuda")
+    bqd.fp8_b128_gemm(w, ws, x, xs, y, bqd.BQD_BF16, M, K, T)
+    ms = torch.tensor([0, 1, 127, M // 2, M // 2 + 1, M - 2, M - 1], device="cuda")
+    ts = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    wv = w[ms].view(torch.float8_e4m3fn).double() * ws[ms // 128].double()
+    xv = x[ts].view(torch.float8_e4m3fn).double() * xs[0, ts].double()[:, None]
+    want, tol = xv @ wv.t(), (xv @ wv.t()) * (2.0 ** -8 + 2.0 ** -15)  # codes are not negative: the sum is its magnitude
+    assert bool(((y[ts][:, ms].double() - want).abs() <= tol + 1e-30).all())
+    assert bool((y >= 0).all())

@@ -179,3 +179,22 @@ def test_calls_are_the_same_twice_and_on_other_streams():
         stream.synchronize()
         out.append((c, s))
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+
+
+def test_rows_past_32_bits():
+    # more than 2^31 elements in and out: the last rows are as alone
+    T, H = 140000, 16384
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(3, H, device="cuda").to(torch.bfloat16)
+    x[-3:] = last
+    w = torch.ones(H, device="cuda")
+    c, s = torch.empty(T, H, dtype=torch.uint8, device="cuda"), torch.empty(H // 128, T, device="cuda")
+    bqd.fp8_x_encode(x, bqd.BQD_BF16, H, c, s, H, T)
+    cl, sl = torch.empty(3, H, dtype=torch.uint8, device="cuda"), torch.empty(H // 128, 3, device="cuda")
+    bqd.fp8_x_encode(last, bqd.BQD_BF16, H, cl, sl, H, 3)
+    assert torch.equal(c[-3:], cl) and torch.equal(s[:, -3:], sl) and not bool(c[:-3].any())
+    r = torch.empty_like(x)
+    bqd.residual_norm(x, bqd.BQD_BF16, H, None, None, 0, 0, 1.0, None, r, bqd.BQD_BF16, w, 1e-6, c, bqd.BQD_E4M3, s, H, T)
+    bqd.residual_norm(last, bqd.BQD_BF16, H, None, None, 0, 0, 1.0, None, None, bqd.BQD_BF16, w, 1e-6, cl, bqd.BQD_E4M3, sl,
+                      H, 3)
+    assert torch.equal(c[-3:], cl) and torch.equal(s[:, -3:], sl) and torch.equal(r[-3:], last) and not bool(c[:-3].any())
