@@ -5,7 +5,9 @@ MoE layer over NVFP4 experts, computed by the CUDA kernels of libbqd.so
 behind the C ABI in include/bqd.h; and the rest of a decode or verify step:
 slots of a paged KV cache (paged_slots), norm, rotary positions and the write
 of K and V (qk_norm_rope_cache), attention of drafted tokens (tree_attention)
-and what the logits answer (token_logprobs). This package holds the ctypes binding
+and what the logits answer (token_logprobs); and for FP8 checkpoints residual and
+norms (residual_norm), 8-bit activations (fp8_x_encode) and their products with
+FP8 block-128 weights (fp8_b128_gemm, fp8_b128_gemm_silu_mul). This package holds the ctypes binding
 (same names as the C ABI), the in-tree build and the seeded workload
 generator.
 """

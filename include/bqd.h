@@ -8,7 +8,9 @@
  * rest of a decode or verify step around its projections: slots of new tokens
  * in a paged KV cache, norm, rotary positions and the write of K and V into
  * it, attention of drafted tokens over it, and the log probabilities, entropy
- * and top alternatives of the step's logits.
+ * and top alternatives of the step's logits; and, for FP8 checkpoints, one
+ * block around its products with 8-bit activations: residual and norms, the
+ * activations' encoder, the product for any number of tokens and the gated pair.
  *
  * Sources (what each call computes):
  *  - "Vemloir/LumenLLM" README, Quantization and Kernels bullets: weights in
@@ -108,7 +110,12 @@ enum {
      * A GEMV call may begin reading its WEIGHTS (codes, scales, q, d) then;
      * its activations are read, and its output written, only after that
      * previous kernel has completed, so chaining layers is safe. The MoE
-     * kernels read nothing before the previous kernel has completed. Do not
+     * kernels read nothing before the previous kernel has completed. The
+     * products with 8-bit activations of up to 64 tokens, and those of more
+     * that are not made by pairs of CTAs, also read their weights' codes then.
+     * (All calls on 8-bit activations may START early with or without this
+     * flag; without it they read and write nothing before that kernel has
+     * completed.) Do not
      * enable it if a call's weights can be written by the kernel immediately
      * before it in the stream. Off by default. */
     BQD_LAUNCH_PDL = 1
@@ -711,7 +718,7 @@ size_t token_logprobs_workspace_bytes(int64_t T, int64_t V, int topk);
  *      [ceil(M/128)][ceil(K/128)]).
  * Arrays of one call must not overlap, but where a call says so. None needs a
  * workspace; all may be captured into graphs and run on any stream of the
- * current device.
+ * current device. A bounded wait that runs out sets a bit of bqd_device_error.
  */
 
 /*
@@ -738,8 +745,8 @@ bqd_status fp8_x_encode(const void* x, int x_type, int64_t x_pitch, uint8_t* cod
  *      gates for all tokens. residual, residual_out: residual_type BQD_F32 or
  *      BQD_BF16, dense. post_weight, pre_weight: fp32 [H].
  *   y: BQD_BF16 [T][H], or BQD_E4M3: codes, with y_scales [ceil(H/128)][T].
- * All arithmetic is fp32 (so a row's sum of squares must fit in it), rounded
- * once where it is stored. Types of absent arrays are not looked at, but for
+ * All arithmetic is fp32 (so a row's sum of squares must fit in it; with
+ * eps 0 a row of zeros gives NaN), rounded once where it is stored. Types of absent arrays are not looked at, but for
  * residual_type. H a multiple of 16, 16 .. 16384; T 0 .. 2^30; eps >= 0.
  */
 bqd_status residual_norm(const void* x, int x_type, int64_t x_pitch, const float* post_weight, const void* gate,
@@ -755,6 +762,9 @@ bqd_status residual_norm(const void* x, int x_type, int64_t x_pitch, const float
  * A block's 128 products are summed by the tensor cores (fp32), the blocks,
  * each times the product of its two scales, in fp32; rounded once where y is
  * BQD_BF16. NaN codes and scales spoil the rows that they meet.
+ * Speed: up to 64 tokens in tiles of 16, 32 or 64 by 128 rows (k shared by CTAs
+ * where there are few), above that 128 by 128 or 256 by 256, whichever goes
+ * through fewer blocks one after the other.
  */
 bqd_status fp8_b128_gemm(const uint8_t* codes, const float* scales, const uint8_t* x, const float* x_scales, void* y,
                          int y_type, int64_t M, int64_t K, int64_t T, cudaStream_t stream);
