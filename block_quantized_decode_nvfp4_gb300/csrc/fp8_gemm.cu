@@ -69,7 +69,11 @@ struct Narrow {
     static constexpr bool kOver = BN > 32;  // they lie over the ring: its room is worth more than a barrier
     static constexpr int kRoom = 109 * 1024 - (kOver ? 0 : kParts);
     static constexpr int kStages = kRoom / kStage / 2 < 4 ? kRoom / kStage / 2 * 2 : 8;  // even: each for one warp
-    static constexpr int kSmem = kStages * kStage + (kOver ? 0 : kParts) + 1024;  // + alignment slack
+    // (+ alignment slack.) No less than two CTAs leave each other: a kernel that takes all of an SM's
+    // tensor memory, and more than half of its shared memory, then never comes to lie beside one of
+    // these, and no CTA of a cluster waits for tensor memory whose holder waits for a peer of its own
+    static constexpr int kNeed = kStages * kStage + (kOver ? 0 : kParts) + 1024, kSmem = kNeed > 109 * 1024 ? kNeed : 109 * 1024;
+    static_assert(2 * (kSmem + 4096) <= 228 * 1024, "two CTAs on an SM, with their static shared memory");
     static constexpr int kBufs = 512 / kCtas / BN < 4 ? 512 / kCtas / BN : 4;
     static constexpr int kTmem = kBufs * BN;
     static constexpr int kCols = BN / kGroups;  // columns of a thread
@@ -89,8 +93,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
     using S = Narrow<BN>;
     constexpr int H = S::kCols, kAhead = S::kAhead;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], dfull[S::kBufs], dempty[S::kBufs],
-        got;
+    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], dfull[S::kBufs], dempty[S::kBufs], got;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_scale[S::kSumWarps][2][H];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
     }
     if (!ok) let_copies_land();
     if (ranks > 1) {
-        // ---- a cluster takes one tile: this CTA's tokens, every so manieth of them in each group of warps
+        // ---- a cluster takes one tile: this CTA's tokens
         __syncwarp();
         if (warp < 4) {
             cluster_wait();

@@ -243,6 +243,28 @@ def test_two_calls_at_once():
     assert np.array_equal(ya.cpu().double().numpy(), alone[0]) and np.array_equal(yb.cpu().double().numpy(), alone[1])
 
 
+def test_beside_other_kernels_of_the_tensor_cores():
+    # clusters here, clusters of the NVFP4 products there, on streams of their own: each ends, with its own answer
+    M, K = 4096, 4096
+    d = [Data(M, K, T, n=2, seed=30 + T) for T in (8, 40, 100)]
+    codes_, scales = codes((M, K // 2), 40), np.full((M, K // 16), 0x38, np.uint8)
+    nv, ns, x = dev(codes_), dev(scales), torch.randn(8, K, device="cuda").to(torch.bfloat16)
+    y = [torch.empty(8, M, device="cuda")] + [torch.empty(e.T, M, device="cuda") for e in d]
+
+    def calls(streams):
+        bqd.nvfp4_gemv(nv, ns, 0.01, x, y[0], M, K, 8, streams[0])
+        for e, o, s in zip(d, y[1:], streams[1:]):
+            bqd.fp8_b128_gemm_silu_mul(e.w[0], e.dws[0], e.w[1], e.dws[1], e.x, e.dxs, o, bqd.BQD_F32, None, M, K, e.T, s)
+    calls([None] * 4)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in y]
+    streams = [torch.cuda.Stream() for _ in y]
+    for _ in range(30):
+        calls(streams)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, y))
+
+
 @pytest.mark.parametrize("norm", [False, True])
 def test_dependent_launches(norm):
     # with programmatic dependent launch on: each call's activations come from the call before it. Without a norm

@@ -198,3 +198,14 @@ def test_rows_past_32_bits():
     bqd.residual_norm(last, bqd.BQD_BF16, H, None, None, 0, 0, 1.0, None, None, bqd.BQD_BF16, w, 1e-6, cl, bqd.BQD_E4M3, sl,
                       H, 3)
     assert torch.equal(c[-3:], cl) and torch.equal(s[:, -3:], sl) and torch.equal(r[-3:], last) and not bool(c[:-3].any())
+
+
+def test_a_tensor_of_the_host_is_refused():
+    t = torch.zeros(16)
+    d = torch.zeros(16, device="cuda")
+    for x, c, y in ((t, d, d), (d, t, d), (d, d, t)):
+        with pytest.raises(ValueError):
+            bqd.fp8_x_encode(x, bqd.BQD_F32, 16, c, y, 16, 1)
+    with pytest.raises(bqd.BqdError) as e:
+        bqd.fp8_x_encode(d, bqd.BQD_F32, 16, d, d, 20, 1)
+    assert e.value.status == 2
