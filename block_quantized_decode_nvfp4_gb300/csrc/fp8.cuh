@@ -40,7 +40,7 @@ __device__ __forceinline__ float block_scale(float amax)
 // product with the rounded reciprocal alone would now and then land on the
 // other side of a boundary between codes: one step from its remainder makes it
 // the quotient, rounded once, as long as the remainder keeps its bits (scales
-// from 2^-60); smaller scales divide, and so does NaN.
+// from 2^-60); smaller scales divide, and so does NaN, but for the smallest.
 __device__ __forceinline__ uint32_t e4m3x2(uint64_t v)  // code of the first in the low byte
 {
     float a, b;
@@ -49,14 +49,15 @@ __device__ __forceinline__ uint32_t e4m3x2(uint64_t v)  // code of the first in 
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// The quotients of v by s through its reciprocal; by division.
+// The quotients of v by s through its reciprocal, negated (the last step then keeps the
+// sign of zeros); by division.
 template <int N>
 __device__ __forceinline__ void quotients(uint64_t (&v)[N], float s)
 {
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     inv = __fmaf_rn(__fmaf_rn(-s, inv, 1.f), inv, inv);
-    const uint64_t i2 = pack(inv, inv), s2 = pack(-s, -s);
+    const uint64_t i2 = pack(-inv, -inv), s2 = pack(s, s);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const uint64_t q = mul2(v[i], i2);
@@ -73,14 +74,25 @@ __device__ __forceinline__ void divide(uint64_t (&v)[N], float s)
         v[i] = pack(__fdiv_rn(a, s), __fdiv_rn(b, s));
     }
 }
+// v to quotients by s; returns what four of their codes are to be XORed with.
 template <int N>
-__device__ __forceinline__ void scale_down(uint64_t (&v)[N], float s)
+__device__ __forceinline__ uint32_t scale_down(uint64_t (&v)[N], float s)
 {
-    if (s >= 8.6736174e-19f)  // 2^-60; false for NaN
+    if (s >= 8.6736174e-19f) {  // 2^-60; false for NaN
         quotients(v, s);
-    else
+        return 0x80808080u;
+    }
+    if (s == 1.17549435e-38f) {  // a block of zeros, such as a row past the last token: 2^126 is exact
+        const uint64_t inv = pack(8.5070592e37f, 8.5070592e37f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = mul2(v[i], inv);
+    } else {
         divide(v, s);
+    }
+    return 0;
 }
+// Codes of four quotients, x (above) included.
+__device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b, uint32_t x) { return (e4m3x2(a) | (e4m3x2(b) << 16)) ^ x; }
 
 __device__ __forceinline__ uint32_t to_bf16x2(float x, float y)
 {
@@ -140,17 +152,12 @@ __device__ __forceinline__ bool fp8_elect()
     asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(pred));
     return pred != 0;
 }
-// 8, 16 or 32 columns of this warp's 32 lanes; several loads may share one wait.
+// 16 or 32 columns of this warp's 32 lanes; several loads may share one wait.
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t* r)
 {
-    static_assert(N == 8 || N == 16 || N == 32, "columns of one load");
-    if constexpr (N == 8)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(at)
-                     : "memory");
-    else if constexpr (N == 16)
+    static_assert(N == 16 || N == 32, "columns of one load");
+    if constexpr (N == 16)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
             "%15}, [%16];"

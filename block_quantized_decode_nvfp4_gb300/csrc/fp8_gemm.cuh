@@ -155,8 +155,8 @@ __device__ __forceinline__ void finish_tokens(const GemmShape& g, const float* p
             // (non-negative floats order as integers, NaN above all)
             const float sc = block_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m))));
             uint64_t w[2] = {pack(v[0], v[1]), pack(v[2], v[3])};
-            scale_down(w, sc);
-            store_codes4(static_cast<uint8_t*>(g.y) + t * g.M + row, e4m3x2(w[0]) | (e4m3x2(w[1]) << 16), live, g.whole);
+            const uint32_t x = scale_down(w, sc);
+            store_codes4(static_cast<uint8_t*>(g.y) + t * g.M + row, e4m3x4(w[0], w[1], x), live, g.whole);
             if (lane == 0) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
         } else {
             store_rows4(g.y, g.y_type, t * g.M + row, v, live, g.whole);

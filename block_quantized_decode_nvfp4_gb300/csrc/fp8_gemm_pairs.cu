@@ -16,14 +16,18 @@
 // Pairs are persistent, so the ring runs on over the outputs of a tile, which go
 // through shared memory to be stored in whole lines.
 //
-// 12288 x 4096 by 8192 tokens 305 us, 2.70 PFLOP/s (343 in a longer run); a gated pair by
-// 4099 tokens 356. A block takes about 840 cycles where the MMAs need 512: without sums
-// the same runs at 3.49 PFLOP/s, without copies too at 4.08. The sums' 128 packed
-// multiply-adds of an SM quarter take about 450 cycles behind the loads, 265 by
-// themselves, and each wait for loads from tensor memory some 100: two rounds of 64
-// columns (305 us) against four of 32, pipelined over the blocks (332), and eight of 16
-// (343); scalar multiply-adds 314; sixteen warps of 64 columns 378; the halves in turns
-// of different sizes, so that one warp's loads meet the other's sums, 348.
+// 12288 x 4096 by 8192 tokens 293 us, 2.81 PFLOP/s (more in a longer run: the power cap); a
+// gated pair by 4099 tokens 337. A block takes about 750 cycles where the MMAs need 512:
+// without the sums' multiply-adds 630, without their loads from tensor memory 620, which is
+// what the L2 gives an SM for its 32 KiB, and without copies 560. The sums' 128 packed
+// multiply-adds of an SM quarter and their loads take 330 cycles by themselves; the rest are
+// the block's scales and barriers, each access of which waits for the tensor cores' reads
+// of shared memory. What did not shorten it: rounds of 32 columns in place of 64, the next
+// on its way or not (308 us where two of 64 took 308), 64 by one load (322), scalar
+// multiply-adds (314), sixteen warps of 64 columns (378), buffers of 128 columns, one for
+// each half of the warps (322), the buffer handed back before it is read (296), scales
+// by warps of their own (380) or by asynchronous copies (362), outputs by the copy engine
+// (330), fewer stages (the same).
 // Every wait is bounded (kErrWaitTimeout in the kernel's error word).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -195,25 +199,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t sum[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) sum[c] = 0;
-            // a block's scales are on their way while the one before it is added up
-            float far_x, far_w, far_u = 0.f;
-            auto fetch = [&](int i) {
-                far_x = i < g.KB && t < g.T ? __ldg(xs + static_cast<int64_t>(i) * g.T) : 0.f;
-                far_w = i < g.KB ? __ldg(ws0 + i) : 0.f;
-                if constexpr (DUAL) far_u = i < g.KB ? __ldg(ws1 + i) : 0.f;
-            };
-            fetch(0);
+            // A block's scales are on their way while the one before it is added up. Nothing may be moved
+            // that is on its way, and waits for tensor memory wait for these loads too, so they come from
+            // the L1, where they were called one block before.
+            const bool live = t < g.T;
+            const int64_t pitch = g.T;
+            float far_x = live ? __ldg(xs) : 0.f, far_w = __ldg(ws0), far_u = DUAL ? __ldg(ws1) : 0.f;
             for (int i = 0; i < g.KB; ++i, ++it) {
-                const float f[2] = {far_x * far_w, DUAL ? far_x * far_u : far_x * far_w};
-                fetch(i + 1);
-                // a token's scale comes from the L2, which may take longer than a block: called into the L1
-                // one block before (the pair's three loads gained nothing from it)
-                if (!DUAL && i + 2 < g.KB && t < g.T)
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(xs + static_cast<int64_t>(i + 2) * g.T));
                 const int b = it % kBufs;
+                // looked at ahead of the scales: beside the tensor cores' reads of shared memory that takes
+                // a hundred cycles
+                const bool ready = mbar_try_wait(&dfull[b], (it / kBufs) & 1);
+                const float f[2] = {far_x * far_w, DUAL ? far_x * far_u : far_x * far_w};
+                if (i + 1 < g.KB) {
+                    xs += pitch;
+                    if (live) far_x = __ldg(xs);
+                    far_w = __ldg(++ws0);
+                    if constexpr (DUAL) far_u = __ldg(++ws1);
+                }
+                if (i + 2 < g.KB && live) asm volatile("prefetch.global.L1 [%0];" ::"l"(xs + pitch));
                 // After a wait that ran out the loops go on without waiting, so that the warps
                 // still meet at every barrier.
-                if (ok) ok = fp8_wait(&dfull[b], (it / kBufs) & 1, &g_fp8_pairs_error);
+                if (!__all_sync(0xFFFFFFFFu, ready) && ok) ok = fp8_wait(&dfull[b], (it / kBufs) & 1, &g_fp8_pairs_error);
                 __syncwarp();
                 tc_after();
                 // 64 columns at a time: the fewer loads wait for one another, the sooner is the buffer free
@@ -254,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // staging, at another place for the next tile
                 const int seen = kOut / 2 + turn * (4 * kWarp) + 4 * lane;
                 *reinterpret_cast<float*>(stage + seen) = most;
+                __syncwarp();
                 named_sync(1 + q, 2 * kWarp);
                 const float sc = block_scale(max_abs(most, *reinterpret_cast<const float*>(stage + (half ? -4 : 4) * kOut + seen)));
                 if (half == 0 && t < g.T) g.ys[static_cast<int64_t>(mt) * g.T + t] = sc;
@@ -263,9 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = pack(acc[16 * i + 2 * e], acc[16 * i + 2 * e + 1]);
-                    scale_down(w, sc);
-                    v[i] = make_uint4(e4m3x2(w[0]) | (e4m3x2(w[1]) << 16), e4m3x2(w[2]) | (e4m3x2(w[3]) << 16),
-                                      e4m3x2(w[4]) | (e4m3x2(w[5]) << 16), e4m3x2(w[6]) | (e4m3x2(w[7]) << 16));
+                    const uint32_t x = scale_down(w, sc);
+                    v[i] = make_uint4(e4m3x4(w[0], w[1], x), e4m3x4(w[2], w[3], x), e4m3x4(w[4], w[5], x), e4m3x4(w[6], w[7], x));
                 }
                 store_lines<64>(stage, v, static_cast<uint8_t*>(g.y) + static_cast<int64_t>(tok0) * g.M + m0, g.M, left, tokens,
                                 g.align);

@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_tmem;
     if (ranks > 1) {
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&got, static_cast<uint32_t>(ranks * own) * kRowBytes);
+        __syncwarp();
         cluster_arrive();  // its barrier may be counted at
     }
 
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 16; ++c)
                     mine[(16 * half + c) ^ (r & 31)] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
                 fence_async_smem();  // read by the copies
+                __syncwarp();
                 named_sync(1, kSumWarps * kWarp);
                 cluster_wait();
                 if (warp == 4 && lane < ranks) {

@@ -115,10 +115,9 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint64_t (&v)[kRuns][4],
     uint64_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = v[i / 4][i % 4];
-    scale_down(w, scale);
-    if (lo) *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(w[0]) | (e4m3x2(w[1]) << 16), e4m3x2(w[2]) | (e4m3x2(w[3]) << 16));
-    if (hi)
-        *reinterpret_cast<uint2*>(p + 64) = make_uint2(e4m3x2(w[4]) | (e4m3x2(w[5]) << 16), e4m3x2(w[6]) | (e4m3x2(w[7]) << 16));
+    const uint32_t x = scale_down(w, scale);
+    if (lo) *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(w[0], w[1], x), e4m3x4(w[2], w[3], x));
+    if (hi) *reinterpret_cast<uint2*>(p + 64) = make_uint2(e4m3x4(w[4], w[5], x), e4m3x4(w[6], w[7], x));
 }
 
 template <bool F32>

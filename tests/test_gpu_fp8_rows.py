@@ -66,6 +66,22 @@ def test_encode_small_large_and_bad_blocks():
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_encode_keeps_the_sign_of_zeros(kind):
+    x = rows(6, 400, 11)
+    x[:, 1::3] = -0.0
+    x[:, 2::5] = 0.0
+    x[1] *= np.float32(2.0 ** -80)       # by division
+    x[2] = -0.0                          # nothing but zeros: the smallest scale
+    x[3, :256] = 0.0
+    x[4] *= np.float32(2.0 ** 100)
+    t, v = to_type(x, kind)
+    c, s = run_encode(t, kind, 6, 400)
+    wc, wsc = ref.encode(v.astype(np.float32))
+    assert (wc == 0x80).sum() > 400
+    assert np.array_equal(s, wsc) and np.array_equal(c, wc)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_encode_of_a_slice_of_wider_rows(kind):
     x, v = to_type(rows(37, 1024, 5), kind)
     c, s = run_encode(x[:, 256:].data_ptr(), kind, 37, 272, pitch=1024)
