@@ -25,12 +25,12 @@
 // one weight, a CTA takes tile after tile, and its ring runs on from one to the
 // next.
 //
-// One token: 151936 x 4096 93 us (6.70 TB/s, the rate of a copy), 12288 x 4096 12.8 us
+// One token: 151936 x 4096 93 us (6.70 TB/s, the rate of a copy), 12288 x 4096 12.4 us
 // back to back, of which the weights stream for 7.8 (6.4 TB/s); the rest is the wait for
 // the call before (1.9), the first bytes (1.4), the last sums and the cluster's
-// exchange (1.5). 16, 32, 64 tokens: 13.6, 15.2, 18.6 us. A gated pair of 12288 x 4096 by
-// 64 tokens 28 us: its 192 CTAs lie unevenly on 152 SMs, which end between 15 and
-// 20 us, and the exchange and outputs take 5 more. Copies by cp.async from four
+// exchange (1.5). 16, 32, 64 tokens: 13.1, 14.6, 16.5 us. A gated pair of 12288 x 4096 by
+// 64 tokens 25 us: its 192 CTAs lie unevenly on 152 SMs, and the exchange and outputs
+// take 5 of them. Copies by cp.async from four
 // warps instead of tensor copies: 14.4 us for one token, and twice as long as now
 // where tokens are many.
 // Every wait is bounded (kErrWaitTimeout in the kernel's error word).
@@ -78,6 +78,12 @@ struct Narrow {
     static constexpr int kTmem = kBufs * BN;
     static constexpr int kCols = BN / kGroups;  // columns of a thread
     static constexpr int kAhead = BN == 64 ? 2 : 4;  // blocks whose scales are on their way
+    // Registers of a thread at launch, of the first four warps and of those of the sums: with the same for
+    // all, a few of them went to memory and back, block after block (12288 x 4096 by 64 tokens 17.7 us, the
+    // pair 28.9, where these take 15.6 and 25.2; 32 tokens 14.1 and 13.8). 16 tokens fit.
+    static constexpr bool kSplit = BN > 16;
+    static constexpr int kRegs = BN == 64 ? 80 : 128, kFewRegs = BN == 64 ? 56 : 72, kSumRegs = BN == 64 ? 88 : 184;
+    static_assert(!kSplit || 4 * kWarp * kFewRegs + kSumWarps * kWarp * kSumRegs <= kThreads * kRegs, "the split of the registers");
     static_assert(BN % 16 == 0 && BN >= 16 && BN <= 64, "the MMA's N, and the threads' registers");
     static_assert(kTmem >= 32 && kTmem <= 512 / kCtas && (kTmem & (kTmem - 1)) == 0, "an SM's CTAs share 512 columns");
     static_assert(kStages >= 2 && kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks_));
     const int ranks = static_cast<int>(ranks_), rank = ranks > 1 ? static_cast<int>(cta_rank()) : 0;
     const int mat = g.mats > 1 ? rank & 1 : 0, cs = ranks / g.mats, ks = rank / g.mats;
-    const int tiles = g.tilesM * g.tilesT, step = static_cast<int>(gridDim.x) / ranks;
+    const int tiles = g.tilesM, step = static_cast<int>(gridDim.x) / ranks;
     const int tile0 = static_cast<int>(blockIdx.x) / ranks;
     const int kb0 = static_cast<int>(static_cast<int64_t>(g.KB) * ks / cs);
     const int nkb = static_cast<int>(static_cast<int64_t>(g.KB) * (ks + 1) / cs) - kb0;
@@ -137,22 +143,28 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
     float* parts = reinterpret_cast<float*>(ring + (S::kOver ? 0 : S::kStages * S::kStage));  // [part][token][row]
     if (ranks > 1) {
         if (threadIdx.x == 0) {
-            const int here = min(BN, g.T - tile0 % g.tilesT * BN);
-            mbar_arrive_expect_tx(&got, ranks * ((here - rank + ranks - 1) / ranks) * (kRows * 4));
+            mbar_arrive_expect_tx(&got, ranks * ((g.T - rank + ranks - 1) / ranks) * (kRows * 4));
         }
+        __syncwarp();
         cluster_arrive();  // its barrier may be counted at
     }
 
     bool ok = true;
+    if constexpr (S::kSplit) {
+        if (warp < 4)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFewRegs));
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSumRegs));
+    }
     if (warp < 2) {
         // ------------------------------------------------ copies, of every other block
         if (lane == 0) {
             auto copy_w = [&](int st, int tile, int kb) {
                 mbar_arrive_expect_tx(&full[st], S::kStage);
-                tma_2d(smem_u32(ring + st * S::kStage), map_w, kb * kBlk, tile / g.tilesT * kRows, &full[st]);
+                tma_2d(smem_u32(ring + st * S::kStage), map_w, kb * kBlk, tile * kRows, &full[st]);
             };
-            auto copy_x = [&](int st, int tile, int kb) {
-                tma_2d(smem_u32(ring + st * S::kStage + kTileBytes), &map_x, kb * kBlk, tile % g.tilesT * BN, &full[st]);
+            auto copy_x = [&](int st, int kb) {
+                tma_2d(smem_u32(ring + st * S::kStage + kTileBytes), &map_x, kb * kBlk, 0, &full[st]);
             };
             // the first stages' weights before the wait for the previous kernel, whose output x may be
             const int first = min(S::kStages, nkb);
@@ -161,7 +173,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
             fp8_pdl_wait();
             for (int i = warp; i < first; i += 2) {
                 if (!g.early) copy_w(i, tile0, kb0 + i);
-                copy_x(i, tile0, kb0 + i);
+                copy_x(i, kb0 + i);
             }
             int it = first;
             for (int tile = tile0; tile < tiles && ok; tile += step) {
@@ -171,7 +183,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                     if (it >= S::kStages) ok = mbar_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, &g_fp8_error);
                     if (!ok) break;
                     copy_w(st, tile, kb0 + i);
-                    copy_x(st, tile, kb0 + i);
+                    copy_x(st, kb0 + i);
                 }
             }
             // The next kernel's start may overlap this one's end. No earlier: CTAs of the calls behind
@@ -211,17 +223,16 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
         int it = 0;
         fp8_pdl_wait();
         for (int tile = tile0; tile < tiles; tile += step) {
-            const int mt = tile / g.tilesT, n0 = tile % g.tilesT * BN + c0;
             uint64_t acc[H / 2];
 #pragma unroll
             for (int c = 0; c < H / 2; ++c) acc[c] = 0;
             float far_x[kAhead][L], far_w[kAhead];
-            const float* ws = g.s[mat] + static_cast<int64_t>(mt) * g.KB + kb0;
-            const float* xs = g.xs + static_cast<int64_t>(kb0) * g.T + n0 + lane;
+            const float* ws = g.s[mat] + static_cast<int64_t>(tile) * g.KB + kb0;
+            const float* xs = g.xs + static_cast<int64_t>(kb0) * g.T + c0 + lane;
             auto fetch = [&](int slot, int i) {
 #pragma unroll
                 for (int l = 0; l < L; ++l)
-                    far_x[slot][l] = i < nkb && n0 + lane + l * kWarp < g.T && (H % kWarp == 0 || lane + l * kWarp < H)
+                    far_x[slot][l] = i < nkb && c0 + lane + l * kWarp < g.T && (H % kWarp == 0 || lane + l * kWarp < H)
                                          ? __ldg(xs + static_cast<int64_t>(i) * g.T + l * kWarp)
                                          : 0.f;
                 far_w[slot] = i < nkb ? __ldg(ws + i) : 0.f;
@@ -270,12 +281,13 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
             }
             if (ranks > 1) {
                 // the parts to their tokens' CTAs
+                __syncwarp();
                 cluster_wait();
                 if (S::kOver) {  // once every ring of the cluster is done with
                     cluster_arrive();
                     cluster_wait();
                 }
-                const int here = min(BN, g.T - (n0 - c0)), most = (here + ranks - 1) / ranks;
+                const int most = (g.T + ranks - 1) / ranks;
                 const uint32_t mine = smem_u32(parts) + static_cast<uint32_t>(rank * most * kRows + r) * 4;
                 int to = c0 % ranks, j = c0 / ranks;
 #pragma unroll
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                     unpack(acc[c / 2], v[0], v[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (c0 + c + e < here)
+                        if (c0 + c + e < g.T)
                             st_async(cta_map(mine + j * (kRows * 4), to), v[e], cta_map(smem_u32(&got), to));
                         if (++to == ranks) {
                             to = 0;
@@ -293,15 +305,15 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
                     }
                 }
             } else {
-                const int64_t row = static_cast<int64_t>(mt) * kRows + r;
+                const int64_t row = static_cast<int64_t>(tile) * kRows + r;
                 if (row < g.M) {
 #pragma unroll
                     for (int c = 0; c < H; c += 2) {
                         float u, v;
                         unpack(acc[c / 2], u, v);
-                        const int64_t at = static_cast<int64_t>(n0 + c) * g.M + row;
-                        if (n0 + c < g.T) store_y(g.y, g.y_type, at, u);
-                        if (n0 + c + 1 < g.T) store_y(g.y, g.y_type, at + g.M, v);
+                        const int64_t at = static_cast<int64_t>(c0 + c) * g.M + row;
+                        if (c0 + c < g.T) store_y(g.y, g.y_type, at, u);
+                        if (c0 + c + 1 < g.T) store_y(g.y, g.y_type, at + g.M, v);
                     }
                 }
             }
@@ -321,9 +333,8 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
         } else {
             // (four times the limit of the other waits: a CTA that gives up one of those still stores)
             if (!fp8_wait_cluster(&got, 0, &g_fp8_error, 4 * kWaitCycles)) ok = false;
-            const int n0 = tile0 % g.tilesT * BN, here = min(BN, g.T - n0);
-            finish_tokens<false>(g, parts, (here + ranks - 1) / ranks, (here - rank + ranks - 1) / ranks, ranks, tile0 / g.tilesT,
-                                 n0 + rank, ranks, 0, warp - 4, S::kSumWarps);
+            finish_tokens<false>(g, parts, (g.T + ranks - 1) / ranks, (g.T - rank + ranks - 1) / ranks, ranks, tile0, rank, ranks, 0,
+                                 warp - 4, S::kSumWarps);
         }
     }
     __syncthreads();
@@ -349,6 +360,13 @@ cudaError_t launch_narrow(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
     auto kern = fp8_gemm_kernel<BN>;
     static OccCache occ;
     blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, S::kThreads, S::kSmem);
+    if constexpr (S::kSplit) {  // it needs what the block is launched with
+        static const int regs = [] {
+            cudaFuncAttributes fa{};
+            return cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN>) == cudaSuccess ? fa.numRegs : 0;
+        }();
+        if (regs < S::kRegs) return cudaErrorInvalidConfiguration;
+    }
     GemmShape g{};
     g.s[0] = a.s0;
     g.s[1] = a.s1;
@@ -359,14 +377,14 @@ cudaError_t launch_narrow(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
     g.T = static_cast<int>(a.T);
     g.KB = static_cast<int>((a.K + kBlk - 1) / kBlk);
     g.tilesM = static_cast<int>((a.M + kRows - 1) / kRows);
-    g.tilesT = static_cast<int>((a.T + BN - 1) / BN);
+    g.tilesT = 1;
     g.mats = dual ? 2 : 1;
     g.y_type = a.y_type;
     g.whole = a.M % 4 == 0;  // y starts on 16 bytes
     g.early = (launch_flags() & kLaunchPdl) != 0;
     // the k blocks of a tile over as many CTAs as may be (with one weight and many tiles: a CTA
     // for tile after tile)
-    const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, slots = static_cast<int64_t>(dev_info(dev).sms) * S::kCtas;
+    const int64_t tiles = g.tilesM, slots = static_cast<int64_t>(dev_info(dev).sms) * S::kCtas;
     static ClusterCache clusters;
     const int ranks =
         g.mats * share_k(clusters, reinterpret_cast<const void*>(kern), dev, S::kThreads, S::kSmem, S::kCtas, tiles, g.mats, g.KB);
