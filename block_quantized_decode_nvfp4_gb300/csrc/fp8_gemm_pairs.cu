@@ -151,6 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fp8_pdl_trigger();
+                // the first CTA's products arrive here: none may be on its way when this CTA ends
+                for (int u = max(it - kStages, 0); u < it && ok; ++u)
+                    if ((u & 1) == warp) ok = mbar_wait(&empty[u % kStages], (u / kStages) & 1, &g_fp8_pairs_error);
             }
             __syncwarp();
         } else if (rank == 0) {
