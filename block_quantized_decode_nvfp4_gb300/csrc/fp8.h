@@ -47,6 +47,8 @@ struct Fp8GemmArgs {
 };
 // Codes [rows][K] in boxes of 128 k x `box` rows (a CUtensorMap); k and rows past the ends read as zero.
 bool fp8_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
+// fp32 or bf16 outputs [rows][M], whole 16 bytes a row, in boxes of `line` (128) bytes x `box` rows.
+bool fp8_rows_map(CUtensorMap* map, void* y, int y_type, int64_t rows, int64_t M, int box, int line);
 // The kernel for more than 64 tokens (fp8_gemm_tokens.cu).
 cudaError_t launch_fp8_gemm_tokens(const Fp8GemmArgs& a, bool dual, cudaStream_t s);
 // The kernel for many tokens (fp8_gemm_pairs.cu), and whether the sizes are its.

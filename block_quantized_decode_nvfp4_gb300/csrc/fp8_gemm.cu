@@ -427,6 +427,20 @@ bool fp8_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool fp8_rows_map(CUtensorMap* map, void* y, int y_type, int64_t rows, int64_t M, int box, int line)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int size = y_type == BQD_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(M) * size};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(line / size), static_cast<cuuint32_t>(box)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, y_type == BQD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dims, strides,
+              boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool fp8_gemm_supported(int64_t M, int64_t K, int64_t T)
 {
     return K >= 16 && K % 16 == 0 && K <= (int64_t(1) << 24) && M >= 1 && M <= (int64_t(1) << 30) && T >= 1 &&

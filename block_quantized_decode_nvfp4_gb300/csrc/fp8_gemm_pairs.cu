@@ -8,16 +8,18 @@
 // memory per product that a CTA alone needs, whose port would be the bound.
 // Tokens lie on the lanes, so a block's scales are one register for a thread's
 // token times one value for its columns. Per CTA:
-//  - warps 0 and 1 copy every other block (counted at the first CTA's barriers);
+//  - warp 0 copies the tokens of a block, warp 1 the weights (counted at the first CTA's
+//    barriers);
 //  - warps 2 and 3 of the first CTA issue every other block's MMAs (M = 256,
 //    N = 256, K = 32) into one of two buffers of 256 columns;
 //  - warps 4..11 read a buffer, 128 columns of a token a thread, scale it and
 //    add it to 128 registers, while the next block's products run.
 // Pairs are persistent, so the ring runs on over the outputs of a tile, which go
-// through shared memory to be stored in whole lines.
+// through shared memory: rows of whole 16 bytes as boxes that the copy engine stores
+// while the sums go on, others in whole lines.
 //
-// 12288 x 4096 by 8192 tokens 293 us, 2.81 PFLOP/s (more in a longer run: the power cap); a
-// gated pair by 4099 tokens 337. A block takes about 750 cycles where the MMAs need 512:
+// 12288 x 4096 by 8192 tokens 286 us, 2.88 PFLOP/s (more in a longer run: the power cap); a
+// gated pair by 4099 tokens 334. A block takes about 750 cycles where the MMAs need 512:
 // without the sums' multiply-adds 630, without their loads from tensor memory 620, which is
 // what the L2 gives an SM for its 32 KiB, and without copies 560. The sums' 128 packed
 // multiply-adds of an SM quarter and their loads take 330 cycles by themselves; the rest are
@@ -26,8 +28,7 @@
 // on its way or not (308 us where two of 64 took 308), 64 by one load (322), scalar
 // multiply-adds (314), sixteen warps of 64 columns (378), buffers of 128 columns, one for
 // each half of the warps (322), the buffer handed back before it is read (296), scales
-// by warps of their own (380) or by asynchronous copies (362), outputs by the copy engine
-// (330), fewer stages (the same).
+// by warps of their own (380) or by asynchronous copies (362). Outputs cost about 30 us of the whole.
 // Every wait is bounded (kErrWaitTimeout in the kernel's error word).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -54,19 +55,21 @@ constexpr int kHalf = 128;                // tokens and weight rows of a CTA's h
 constexpr int kTile = 2 * kHalf;          // tokens of a tile (MMA M), columns of a buffer (N)
 constexpr int kHalfBytes = kHalf * kBlk;
 constexpr int kStage = 2 * kHalfBytes;    // of one CTA
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kBufs = 2;
 constexpr int kSumWarps = 8;
 constexpr int kThreads = (4 + kSumWarps) * kWarp;
 constexpr int kLineBytes = 128;           // of a token's outputs, staged by a warp at once
-constexpr int kOut = kWarp * kLineBytes;  // staging of a warp
+constexpr int kBox = kWarp * kLineBytes;  // 32 tokens' outputs: what a warp copies out at once
+constexpr int kBoxes = 2;                 // of a warp, on their way out one behind the other
+constexpr int kOut = kBoxes * kBox;
 constexpr int kSmem = kStages * kStage + kSumWarps * kOut + 1024;  // + alignment slack
 constexpr int kGroup = 8;                 // token tiles that share a sweep over the weights
 // 128 x 56 + 256 x 224 are the 384 x 168 registers that the block has
 constexpr int kRegs = 168, kFewRegs = 56, kSumRegs = 224;
 static_assert(4 * kWarp * kFewRegs + kSumWarps * kWarp * kSumRegs <= kThreads * kRegs, "the split of the registers");
 static_assert(kSmem <= 227 * 1024 - 512, "shared memory of one CTA, static beside it");
-static_assert(kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer for each of two warps");
+static_assert(kBufs == 2 && kStages >= 5, "a buffer for each of two warps, and what their waits rest on");
 
 struct PairShape {
     const float *s[2], *xs;
@@ -78,6 +81,7 @@ struct PairShape {
     int blocksM;  // of 128 rows
     int y_type;
     int align;    // of y's rows: see row_align
+    int boxes;    // outputs leave as boxes of map_y
 };
 
 // Tile i: kGroup token tiles under each tile of the weights, group after group.
@@ -89,10 +93,25 @@ __device__ __forceinline__ void find_tile(const PairShape& g, int i, int& mt, in
     tt = group * kGroup + in - mt * wide;
 }
 
+// A warp's 32 tokens x 128 bytes of outputs, a lane's token in v: staged, and copied out.
+__device__ __forceinline__ void store_box(uint8_t* stage, const uint4 (&v)[8], const CUtensorMap* map, int64_t m, int tok, bool any)
+{
+    const int lane = threadIdx.x % kWarp;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(stage + lane * kLineBytes + ((i ^ (lane & 7)) << 4)) = v[i];
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (any) tma_store_2d(map, smem_u32(stage), static_cast<int>(m), tok);
+        bulk_commit();
+    }
+}
+
 template <bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_pairs_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
-                     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ PairShape g)
+                     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y,
+                     const __grid_constant__ PairShape g)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], dfull[kBufs], dempty[kBufs];
@@ -107,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_map(map_w);
         prefetch_map(&map_x);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&full[i], 2);  // the first CTA's counts, for both
+            mbar_init(&full[i], 4);  // the first CTA's counts, for both and for both operands
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kBufs; ++i) {
@@ -132,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp < 2) {
-            // -------------------------------------------- copies, of every other block
+            // -------------------------------------------- copies: an operand a warp
             if (lane == 0) {
                 int it = 0;
                 for (int tile = tile0; tile < tiles && ok; tile += step) {
@@ -140,20 +159,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     find_tile(g, tile, mt, tt);
                     const int row = DUAL ? mt * kHalf : mt * kTile + rank * kHalf, tok = tt * kTile + rank * kHalf;
                     for (int i = 0; i < g.KB; ++i, ++it) {
-                        if ((it & 1) != warp) continue;
                         const int st = it % kStages;
                         if (it >= kStages) ok = mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1, &g_fp8_pairs_error);
                         if (!ok) break;
                         const uint32_t at = smem_u32(ring + st * kStage), bar = cta_map(smem_u32(&full[st]), 0);
-                        arrive_expect_cluster(bar, kStage);
-                        tma_2d_pair(at, &map_x, i * kBlk, tok, bar);
-                        tma_2d_pair(at + kHalfBytes, map_w, i * kBlk, row, bar);
+                        arrive_expect_cluster(bar, kHalfBytes);
+                        if (warp == 0)
+                            tma_2d_pair(at, &map_x, i * kBlk, tok, bar);
+                        else
+                            tma_2d_pair(at + kHalfBytes, map_w, i * kBlk, row, bar);
                     }
                 }
                 fp8_pdl_trigger();
                 // the first CTA's products arrive here: none may be on its way when this CTA ends
-                for (int u = max(it - kStages, 0); u < it && ok; ++u)
-                    if ((u & 1) == warp) ok = mbar_wait(&empty[u % kStages], (u / kStages) & 1, &g_fp8_pairs_error);
+                for (int u = warp ? it : max(it - kStages, 0); u < it && ok; ++u)
+                    ok = mbar_wait(&empty[u % kStages], (u / kStages) & 1, &g_fp8_pairs_error);
             }
             __syncwarp();
         } else if (rank == 0) {
@@ -164,6 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < g.KB; ++i, ++it) {
                     if ((it & 1) != warp - 2) continue;
                     const int st = it % kStages, b = it % kBufs;
+                    // (never two rounds behind: the block two before this one waited for the sums of two
+                    // more before it, and so for the copies of all up to it - kStages)
                     ok = fp8_wait(&full[st], (it / kStages) & 1, &g_fp8_pairs_error);
                     if (ok && it >= kBufs) ok = fp8_wait(&dempty[b], ((it / kBufs) & 1) ^ 1, &g_fp8_pairs_error);
                     if (!ok) break;
@@ -290,8 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 4; ++e) w[e] = to_bf16x2(acc[64 * k + 8 * i + 2 * e], acc[64 * k + 8 * i + 2 * e + 1]);
                         v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 2 * (static_cast<int64_t>(tok0) * g.M + m0 + 64 * k),
-                                     2 * g.M, 2 * (left - 64 * k), tokens, g.align);
+                    if (g.boxes) {
+                        if (lane == 0) bulk_wait_read<kBoxes - 1>();  // its place has been left
+                        __syncwarp();
+                        store_box(stage + k % kBoxes * kBox, v, &map_y, m0 + 64 * k, tok0, left > 64 * k && tokens > 0);
+                    } else {
+                        store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 2 * (static_cast<int64_t>(tok0) * g.M + m0 + 64 * k),
+                                         2 * g.M, 2 * (left - 64 * k), tokens, g.align);
+                    }
                 }
             } else {
 #pragma unroll
@@ -301,11 +329,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 8; ++i)
                         v[i] = make_uint4(__float_as_uint(acc[32 * k + 4 * i]), __float_as_uint(acc[32 * k + 4 * i + 1]),
                                           __float_as_uint(acc[32 * k + 4 * i + 2]), __float_as_uint(acc[32 * k + 4 * i + 3]));
-                    store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 4 * (static_cast<int64_t>(tok0) * g.M + m0 + 32 * k),
-                                     4 * g.M, 4 * (left - 32 * k), tokens, g.align);
+                    if (g.boxes) {
+                        if (lane == 0) bulk_wait_read<kBoxes - 1>();  // its place has been left
+                        __syncwarp();
+                        store_box(stage + k % kBoxes * kBox, v, &map_y, m0 + 32 * k, tok0, left > 32 * k && tokens > 0);
+                    } else {
+                        store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 4 * (static_cast<int64_t>(tok0) * g.M + m0 + 32 * k),
+                                         4 * g.M, 4 * (left - 32 * k), tokens, g.align);
+                    }
                 }
             }
         }
+        if (lane == 0) bulk_wait_all();
         tc_before();
     }
     if (!ok) let_copies_land();
@@ -321,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool DUAL>
 cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t s)
 {
-    CUtensorMap w0, w1, x;
+    CUtensorMap w0, w1, x, y;
     if (!fp8_codes_map(&w0, a.w0, a.M, a.K, kHalf) || !fp8_codes_map(&x, a.x, a.T, a.K, kHalf)) return cudaErrorInvalidValue;
     if (!DUAL)
         w1 = w0;
@@ -353,8 +388,14 @@ cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t s)
     g.blocksM = static_cast<int>((a.M + 127) / 128);
     g.y_type = a.y_type;
     g.align = row_align(a.M, a.y_type);
+    // rows of whole 16 bytes leave as boxes of 128 bytes by 32 tokens
+    g.boxes = a.y_type != BQD_E4M3 && g.align == 16;
+    if (!g.boxes)
+        y = x;
+    else if (!fp8_rows_map(&y, a.y, a.y_type, a.T, a.M, kWarp, kLineBytes))
+        return cudaErrorInvalidValue;
     const int64_t tiles = static_cast<int64_t>(g.tilesM) * g.tilesT, pairs = dev_info(dev).sms / 2;
-    return launch_clusters(kern, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 2, kThreads, kSmem, s, w0, w1, x, g);
+    return launch_clusters(kern, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 2, kThreads, kSmem, s, w0, w1, x, y, g);
 }
 
 }  // namespace

@@ -107,6 +107,15 @@ def test_gemm_many_tiles_and_long_k(M, K, T):
         check_ffn(Data(M, K, T, n=2, seed=22, lo=-16, hi=-6), "e4m3")
 
 
+# many tokens, tiles of 256 rows by 256 tokens: rows of y that start on 16 bytes and not, last tiles of a few rows or tokens
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,T", [(2600, 256, 2050), (2568, 128, 2049), (2692, 272, 2100), (2690, 128, 2304), (2816, 1040, 2303)])
+def test_gemm_outputs_of_many_tokens(M, K, T, kind):
+    check_gemm(Data(M, K, T, seed=23), kind)
+    if M % 4 == 0 and K < 1000:
+        check_ffn(Data(M // 2, K, T, n=2, seed=24, lo=-16, hi=-6), kind)
+
+
 @pytest.mark.parametrize("M,K,T", [(12288, 4096, 1), (4096, 12288, 17), (4870, 4096, 333)])
 def test_gemm_of_a_layer(M, K, T):
     check_gemm(Data(M, K, T, seed=7))
