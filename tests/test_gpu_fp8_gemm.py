@@ -307,6 +307,38 @@ def test_dependent_launches(norm):
     assert not norm or bool(y.isfinite().all())
 
 
+@pytest.mark.parametrize("T", [300, 2500])
+def test_dependent_launches_of_many_tokens(T):
+    # outputs that leave after their kernel's last sums are complete for the next call: one call after the other,
+    # against the same with a wait between
+    K, I = 2048, 1024
+    d = Data(I, K, T, n=2, seed=25)
+    down = Data(K, I, T, seed=26)
+    h, hs = torch.empty(T, I, dtype=torch.uint8, device="cuda"), torch.empty(I // 128, T, device="cuda")
+    r, ones = torch.empty(T, K, dtype=torch.bfloat16, device="cuda"), torch.ones(K, device="cuda")
+    got = []
+    for wait in (True, False):
+        for kind, code in ((torch.float32, bqd.BQD_F32), (torch.bfloat16, bqd.BQD_BF16)):
+            d.upload()
+            r.zero_()
+            y = torch.empty(T, K, dtype=kind, device="cuda")
+            calls = [
+                lambda: bqd.fp8_b128_gemm_silu_mul(d.w[0], d.dws[0], d.w[1], d.dws[1], d.x, d.dxs, h, bqd.BQD_E4M3, hs, I, K, T),
+                lambda: bqd.fp8_b128_gemm(down.w[0], down.dws[0], h, hs, y, code, K, I, T),
+                lambda: bqd.residual_norm(y, code, K, ones, None, 0, 0, 1.0, r, r, bqd.BQD_BF16, ones, 1e-6, d.x, bqd.BQD_E4M3,
+                                          d.dxs, K, T)]
+            for _ in range(6):
+                for call in calls:
+                    call()
+                    if wait:
+                        torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            got.append((y.clone(), r.clone(), d.x.clone(), d.dxs.clone()))
+    for a, b in zip(got[:2], got[2:]):
+        assert all(torch.equal(v.view(torch.uint8), w.view(torch.uint8)) for v, w in zip(a, b))
+        assert bool(b[0].isfinite().all()) and bool(b[1].isfinite().all())
+
+
 @pytest.mark.parametrize("M,T", [(72000, 33000), (36000000, 64), (400000, 6000)])
 def test_outputs_past_32_bits(M, T):
     # y holds more than 2^31 elements; sampled rows and columns against the definition
