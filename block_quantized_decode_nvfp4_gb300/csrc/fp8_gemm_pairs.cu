@@ -18,8 +18,8 @@
 // through shared memory: rows of whole 16 bytes as boxes that the copy engine stores
 // while the sums go on, others in whole lines.
 //
-// 12288 x 4096 by 8192 tokens 286 us, 2.88 PFLOP/s (more in a longer run: the power cap); a
-// gated pair by 4099 tokens 334. A block takes about 750 cycles where the MMAs need 512:
+// 12288 x 4096 by 8192 tokens 284 us, 2.90 PFLOP/s (more in a longer run: the power cap); a
+// gated pair by 4099 tokens 331. A block takes about 750 cycles where the MMAs need 512:
 // without the sums' multiply-adds 630, without their loads from tensor memory 620, which is
 // what the L2 gives an SM for its 32 KiB, and without copies 560. The sums' 128 packed
 // multiply-adds of an SM quarter and their loads take 330 cycles by themselves; the rest are
@@ -27,8 +27,8 @@
 // of shared memory. What did not shorten it: rounds of 32 columns in place of 64, the next
 // on its way or not (308 us where two of 64 took 308), 64 by one load (322), scalar
 // multiply-adds (314), sixteen warps of 64 columns (378), buffers of 128 columns, one for
-// each half of the warps (322), the buffer handed back before it is read (296), scales
-// by warps of their own (380) or by asynchronous copies (362). Outputs cost about 30 us of the whole.
+// each half of the warps (322), scales by warps of their own (380) or by asynchronous
+// copies (362). Outputs cost about 30 us of the whole.
 // Every wait is bounded (kErrWaitTimeout in the kernel's error word).
 #include <cuda.h>
 #include <cuda_bf16.h>
