@@ -24,10 +24,11 @@ constexpr int kTileBytes = kRows * kBlk;
 constexpr int kMaxCluster = 8;
 
 struct GemmShape {
+    const uint8_t* w[2];
     const float *s[2], *xs;
     void* y;
     float* ys;
-    int64_t M;
+    int64_t M, K;
     int T, KB;           // tokens, blocks of k
     int tilesM, tilesT;  // tile = row tile * tilesT + token tile
     int mats;            // 2: a gated pair
@@ -36,6 +37,19 @@ struct GemmShape {
     int whole;           // y's rows are so aligned that four elements of one may be stored at once
     int early;           // weights may be read before the previous kernel has completed
 };
+
+// A row's first blocks called into the L2, by a thread that waits for the previous kernel:
+// the memory has less to do at a kernel's end. More than two of them, or by the copy engine
+// (6 blocks: 0.6 us later for small calls), hold up a call that need not wait. The L2 keeps
+// what that kernel may still write.
+__device__ __forceinline__ void call_weights(const GemmShape& g, int mat, int64_t row, int kb, int blocks)
+{
+    constexpr int kMost = 2;
+    if (g.early || row >= g.M) return;
+    const uint8_t* at = g.w[mat] + row * g.K + static_cast<int64_t>(kb) * kBlk;
+    for (int i = 0; i < kMost; ++i)
+        if (i < blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * kBlk) : "memory");
+}
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
 

@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp % 4, half = (warp - 4) / 4, r = 32 * q + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64 * half;
         int it = 0;
+        if (half == 0) call_weights(g, mat, static_cast<int64_t>(tile0 / g.tilesT) * kRows + r, kb0, nkb);
         fp8_pdl_wait();
         for (int tile = tile0; tile < tiles; tile += step) {
             const int mt = tile / g.tilesT, t = tile % g.tilesT * kTok + r;
@@ -325,6 +326,9 @@ cudaError_t launch_fp8_gemm_tokens(const Fp8GemmArgs& a, bool dual, cudaStream_t
     }();
     if (regs < kRegs) return cudaErrorInvalidConfiguration;
     GemmShape g{};
+    g.w[0] = a.w0;
+    g.w[1] = a.w1;
+    g.K = a.K;
     g.s[0] = a.s0;
     g.s[1] = a.s1;
     g.xs = a.xs;

@@ -115,7 +115,7 @@ enum {
      * that are not made by pairs of CTAs, also read their weights' codes then.
      * (All calls on 8-bit activations may START early with or without this
      * flag; without it they read and write nothing before that kernel has
-     * completed.) Do not
+     * completed, but may call weights into the L2.) Do not
      * enable it if a call's weights can be written by the kernel immediately
      * before it in the stream. Off by default. */
     BQD_LAUNCH_PDL = 1

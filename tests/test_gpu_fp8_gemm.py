@@ -307,6 +307,54 @@ def test_dependent_launches(norm):
     assert not norm or bool(y.isfinite().all())
 
 
+@pytest.mark.parametrize("T", [1, 40, 200, 1100])
+def test_weights_written_by_the_call_before(T):
+    # no early reads without the flag: each product's weights are written by the kernel before it, after a product has
+    # let that kernel's neighbours start
+    M, K, n = 1536, 1152, 6
+    ds = [Data(M, K, T, seed=30 + i) for i in range(n)]
+    want = []
+    for d in ds:
+        y = torch.empty(T, M, device="cuda")
+        bqd.fp8_b128_gemm(d.w[0], d.dws[0], d.x, d.dxs, y, bqd.BQD_F32, M, K, T)
+        torch.cuda.synchronize()
+        want.append(y)
+    w, s = torch.empty_like(ds[0].w[0]), torch.empty_like(ds[0].dws[0])
+    rows = [d.w[0].float() for d in ds]  # (of code bytes: any kernel's output)
+    for _ in range(20):
+        got = [torch.empty(T, M, device="cuda") for _ in ds]
+        for d, r, y in zip(ds, rows, got):
+            s.copy_(d.dws[0])
+            w.copy_(r)
+            bqd.fp8_b128_gemm(w, s, d.x, d.dxs, y, bqd.BQD_F32, M, K, T)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [64, 300])
+def test_weights_made_by_an_encoder_that_starts_early(T):
+    # the same behind a call that lets the next one start: fp8_x_encode's codes are the product's weights
+    M, K, n = 640, 1152, 5
+    d = Data(M, K, T, seed=41)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    src = [torch.randn(M, K, generator=g, device="cuda") for _ in range(n)]
+    w, sc = torch.empty(M, K, dtype=torch.uint8, device="cuda"), torch.empty(K // 128, M, device="cuda")
+
+    def run(wait):
+        out = []
+        for _ in range(4):
+            for x in src:
+                y = torch.empty(T, M, device="cuda")
+                bqd.fp8_x_encode(x, bqd.BQD_F32, K, w, sc, K, M)
+                if wait:
+                    torch.cuda.synchronize()
+                bqd.fp8_b128_gemm(w, d.dws[0], d.x, d.dxs, y, bqd.BQD_F32, M, K, T)
+                if wait:
+                    torch.cuda.synchronize()
+                out.append(y)
+        return out
+    assert all(torch.equal(a, b) for a, b in zip(run(True), run(False)))
+
+
 @pytest.mark.parametrize("T", [300, 2500])
 def test_dependent_launches_of_many_tokens(T):
     # outputs that leave after their kernel's last sums are complete for the next call: one call after the other,
