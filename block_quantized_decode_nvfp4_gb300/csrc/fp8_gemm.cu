@@ -25,16 +25,15 @@
 // one weight, a CTA takes tile after tile, and its ring runs on from one to the
 // next.
 //
-// One token: 151936 x 4096 93 us (6.70 TB/s, the rate of a copy), 12288 x 4096 12.4 us
+// One token: 151936 x 4096 93 us (6.70 TB/s, the rate of a copy), 12288 x 4096 11.9 us
 // back to back, of which the weights stream for 7.8 (6.4 TB/s); the rest is the wait for
 // the call before (1.9), the first bytes (1.4), the last sums and the cluster's
-// exchange (1.5). 16, 32, 64 tokens: 13.1, 14.6, 16.5 us. A gated pair of 12288 x 4096 by
-// 64 tokens 25 us: its 192 CTAs lie unevenly on 152 SMs, and the exchange and outputs
-// take 5 of them. Copies by cp.async from four
-// warps instead of tensor copies: 14.4 us for one token, and twice as long as now
-// where tokens are many.
-// The first weights are called into the L2 ahead of the wait for the call before: 12288 x
-// 4096 by 1, 17 and 32 tokens in turn 11.7 to 11.2, 12.9 to 12.4 and 13.7 to 13.0 us.
+// exchange (1.5). 16, 32, 64 tokens: 12.4, 13.8, 15.8 us. A gated pair of 12288 x 4096 by
+// 64 tokens 24 us: its 192 CTAs lie unevenly on 152 SMs, and the exchange and outputs
+// take 5 of them. Copies by cp.async from four warps instead of tensor copies: 14.4 us for
+// one token, and twice as long as now where tokens are many. The first weights are called
+// into the L2 ahead of the wait for the call before: one and 32 tokens in turn 11.6 to 11.0
+// and 13.5 to 12.9 us, 4096 x 12288 by 17 12.7 to 12.2.
 // Every wait is bounded (kErrWaitTimeout in the kernel's error word).
 #include <cuda.h>
 #include <cuda_bf16.h>
