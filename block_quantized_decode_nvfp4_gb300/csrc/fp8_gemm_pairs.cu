@@ -313,9 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (g.boxes) {
+                        // the places follow one another over the tiles too: of a gated pair a tile has one box
+                        const int place = N == 64 ? turn : k % kBoxes;
+                        static_assert(kBoxes == 2, "turn counts tiles by two");
                         if (lane == 0) bulk_wait_read<kBoxes - 1>();  // its place has been left
                         __syncwarp();
-                        store_box(stage + k % kBoxes * kBox, v, &map_y, m0 + 64 * k, tok0, left > 64 * k && tokens > 0);
+                        store_box(stage + place * kBox, v, &map_y, m0 + 64 * k, tok0, left > 64 * k && tokens > 0);
                     } else {
                         store_lines<128>(stage, v, static_cast<uint8_t*>(g.y) + 2 * (static_cast<int64_t>(tok0) * g.M + m0 + 64 * k),
                                          2 * g.M, 2 * (left - 64 * k), tokens, g.align);

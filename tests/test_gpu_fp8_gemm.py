@@ -404,3 +404,18 @@ def test_outputs_past_32_bits(M, T):
     want, tol = xv @ wv.t(), (xv @ wv.t()) * (2.0 ** -8 + 2.0 ** -15)  # codes are not negative: the sum is its magnitude
     assert bool(((y[ts][:, ms].double() - want).abs() <= tol + 1e-30).all())
     assert bool((y >= 0).all())
+
+
+# gated pairs of many tokens whose rows of h are whole 16 bytes and leave as boxes, several tiles for each pair of CTAs: a
+# box of one tile may still be on its way when the next tile's is made, the sooner the fewer blocks of k there are
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("I,K,T", [(1288, 16, 8200), (2048, 128, 4100), (4096, 272, 4099), (4104, 16, 2050)])
+def test_ffn_outputs_of_many_tiles(I, K, T, kind):
+    d = Data(I, K, T, n=2, seed=27, lo=-16, hi=-6)
+    check_ffn(d, kind)
+    want = None
+    for _ in range(10):
+        h = torch.full((T, I), 7.0, dtype=TYPES[kind][0], device="cuda")
+        bqd.fp8_b128_gemm_silu_mul(d.w[0], d.dws[0], d.w[1], d.dws[1], d.x, d.dxs, h, TYPES[kind][1], None, I, K, T)
+        assert want is None or torch.equal(h, want)
+        want = h
