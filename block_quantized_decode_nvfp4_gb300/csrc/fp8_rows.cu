@@ -210,9 +210,15 @@ struct Runs {
         for (int n = 0; n < N; ++n) v[n].get(x[n]);
     }
 };
-__device__ __forceinline__ void weight8(const float* p, uint64_t (&v)[4])
+// Eight weights; of a run past the row's end zeros, with which its zeros stay zeros: another channel's weight may be
+// no number, and would spoil the row's sum and its last block.
+__device__ __forceinline__ void weight8(const float* p, bool in, uint64_t (&v)[4])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (in) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
     v[0] = pack(a.x, a.y);
     v[1] = pack(a.z, a.w);
     v[2] = pack(b.x, b.y);
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(MOST, CTAS) residual_norm_kernel(const NormArg
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 uint64_t w[4];
-                weight8(a.post_weight + (in[n] ? e[n] : 0u), w);
+                weight8(a.post_weight + e[n], in[n], w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) z[n][j] = mul2(mul2(z[n][j], rs2), w[j]);
             }
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(MOST, CTAS) residual_norm_kernel(const NormArg
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         uint64_t w[4];
-        weight8(a.pre_weight + (in[n] ? e[n] : 0u), w);
+        weight8(a.pre_weight + e[n], in[n], w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[n][j] = mul2(mul2(r[n][j], rs2), w[j]);
     }

@@ -225,3 +225,37 @@ def test_a_tensor_of_the_host_is_refused():
     with pytest.raises(bqd.BqdError) as e:
         bqd.fp8_x_encode(d, bqd.BQD_F32, 16, d, d, 20, 1)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H", [16, 144, 272, 4112, 8224])
+def test_bad_weights_spoil_their_own_channels(H, bad):
+    # weights of a few channels are no numbers: what they meet is none, the other blocks are as without them
+    T, at = 9, [0, 5]
+    x, _ = to_type(rows(T, H, H, spread=2), "f32")
+    w = torch.ones(H, device="cuda")
+
+    def run(post, pre):
+        y, s = Out((T, H), "e4m3"), Out((-(-H // 128), T), "f32")
+        r = Out((T, H), "f32")
+        bqd.residual_norm(x, bqd.BQD_F32, H, post, None, 0, 0, 1.0, None, r.ptr, bqd.BQD_F32, pre, 1e-6, y.ptr, bqd.BQD_E4M3,
+                          s.ptr, H, T)
+        return y.get(), s.get(), r.get()
+    v = w.clone()
+    v[at] = bad
+    y, s, r = run(None, w)
+    by, bs, br = run(None, v)
+    assert np.array_equal(br, r)
+    assert (by[:, :128] == 0x7F).all() and np.isnan(bs[0]).all()
+    assert np.array_equal(by[:, 128:], y[:, 128:]) and np.array_equal(bs[1:], s[1:])
+    # the norm after the block: its bad channels enter the sum of squares; infinite ones leave zeros beside them
+    y, s, r = run(w, w)
+    by, bs, br = run(v, w)
+    keep = np.ones(H, bool)
+    keep[at] = False
+    assert np.array_equal(br[:, keep], r[:, keep]) and not np.isfinite(br[:, ~keep]).any()
+    assert (by[:, :128] == 0x7F).all() and np.isnan(bs[0]).all()
+    if np.isnan(bad):
+        assert (by == 0x7F).all() and np.isnan(bs).all()
+    else:
+        assert ((by[:, 128:] & 0x7F) == 0).all() and (bs[1:] == 2.0 ** -126).all()
