@@ -51,7 +51,14 @@ __device__ __forceinline__ void call_weights(const GemmShape& g, int mat, int64_
         if (i < blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i * kBlk) : "memory");
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
+// SiLU(g) u = g / (1 + e^-g) u, with e = e^-|g|: 1 / (1 + e) for g from 0 on, e / (1 + e) below, so that the divisor
+// stays between 1 and 2. By 1 + e^-g the fast division would give 0 from g = -87.3 on, where it passes 2^126, and an
+// infinity from -88.7 on, while the product with a large u is still a normal number.
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    const float e = expf(-fabsf(g));
+    return __fdividef(g >= 0.f ? g : g * e, 1.f + e) * u;
+}
 
 __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v)
 {

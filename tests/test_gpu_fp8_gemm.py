@@ -419,3 +419,31 @@ def test_ffn_outputs_of_many_tiles(I, K, T, kind):
         bqd.fp8_b128_gemm_silu_mul(d.w[0], d.dws[0], d.w[1], d.dws[1], d.x, d.dxs, h, TYPES[kind][1], None, I, K, T)
         assert want is None or torch.equal(h, want)
         want = h
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 20, 50, 200, 2500])
+def test_gates_far_below_zero_keep_their_bits(T, kind):
+    # one k counts: g[i] = code value * (1 + i / 2^12 of a tile's scale), u = 2^70, so that h is a normal number from g = -120
+    # on. The products are exact but for one rounding each of g's scale and sum: |dg| <= 2^-22 |g|, times |SiLU'| <= |g| e^g
+    # for g < -2; e^-|g| and g e are off by a step of 2^-149 where they are subnormal, the rest by 2^-20
+    I, K = 1100, 16
+    d = Data(I, K, T, n=2, seed=28)
+    d.xc[:], d.xc[:, 3] = 0, 0x38                       # 1.0
+    d.xs[:] = 1.0
+    d.wc[0][:], d.wc[1][:] = 0, 0
+    gates = np.array([-2, -20, -40, -64, -72, -80, -88, -96, -104, 88, 0], np.float32)
+    table = {float(v): c for c, v in enumerate(ref.VALUES) if v == v}
+    d.wc[0][:, 3] = [table[float(g)] for g in np.resize(gates, I)]
+    d.wc[1][:, 3] = 0x38
+    d.ws[0][:, 0] = 1 + np.arange(len(d.ws[0])) * np.float32(2.0 ** -12)
+    d.ws[1][:] = 2.0 ** 70
+    d.upload()
+    h = Out((T, I), kind)
+    bqd.fp8_b128_gemm_silu_mul(d.w[0], d.dws[0], d.w[1], d.dws[1], d.x, d.dxs, h.ptr, TYPES[kind][1], None, I, K, T)
+    g = np.resize(gates, I).astype(np.float64) * np.repeat(d.ws[0][:, 0].astype(np.float64), 128)[:I]
+    want = ref.silu(g) * 2.0 ** 70
+    tol = 2.0 ** -22 * np.maximum(np.abs(g), 1) * np.abs(want) + 2.0 ** -20 * np.abs(want) + (np.abs(g) + 1) * 2.0 ** (70 - 149)
+    got = h.get()
+    assert (np.abs(got - want) <= tol + HALF[kind] * (np.abs(want) + tol)).all()
+    assert (got[:, (g < -60) & (g > -100)] < 0).all()
