@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    pdl_trigger();
     pdl_wait();  // x may come from the previous kernel in the stream; y may be read by it
+    pdl_trigger();  // not before the wait: the next kernel may read weights that one before the last wrote
 
     bool ok = true;
     if (warp == 0) {

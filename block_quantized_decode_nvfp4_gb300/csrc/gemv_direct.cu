@@ -402,9 +402,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                              sp + F::srow(pr) * spitch + (d % CPL) * F::kSChunk);
         }
     }
-    pdl_trigger();
     __syncthreads();
     pdl_wait();  // the activations may come from the previous kernel; y may be read by it
+    pdl_trigger();  // not before the wait: the next kernel may read weights that one before the last wrote
 
     // activations, one global read into registers: exponent range of the
     // nonzero values (bf16 biased exponents), then the prescaled f16 copy

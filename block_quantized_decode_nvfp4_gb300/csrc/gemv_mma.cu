@@ -332,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    pdl_trigger();
 
     // ---- activations, pass 1 (warps 1..17; warp 0 has just issued the
     // ring's first copies): B = f16(x * 2^4) written while each token's
@@ -340,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // eight 16-byte loads in flight together. The 2^4 prescale is exact for
     // 2^-21 <= |x| < 2^11; a token outside that window takes pass 2.
     pdl_wait();  // the activations may come from the previous kernel in the stream
+    pdl_trigger();  // not before the wait: the next kernel may read weights that one before the last wrote
     const int groups = nsr * (kStageK / 8);  // B covers the CTA's stages once; 8 k = one 16-byte piece
     {
         constexpr int kStagers = kThreads - kWarp;

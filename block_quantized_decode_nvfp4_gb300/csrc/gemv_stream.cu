@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         fence_barrier_init();
     }
     __syncthreads();
-    pdl_trigger();  // one resident CTA per SM: a dependent grid can only start as CTAs here exit
 
     if (warp == 0) {
         // ------------------------------------------------ producer
@@ -258,6 +257,9 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     // ---------------------------------------------------- consumers
     const int ctid = threadIdx.x - kWarp;
     pdl_wait();  // the activations may come from the previous kernel in the stream
+    // not before the wait: the next kernel may read weights that one before the last wrote (one resident CTA per
+    // SM: a dependent grid can only start as CTAs here exit)
+    pdl_trigger();
     // exponent range of the nonzero activations (bf16 biased exponents)
     int emax = 0, emin = INT_MAX, flags = 0;
     for (int64_t i = ctid; i < K / 2; i += kCT) {

@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kThT, 1)
             }
         }
     }
-    pdl_trigger();
     pdl_wait();  // x may come from the previous kernel; y may be read by it
+    pdl_trigger();  // not before the wait: the next kernel may read weights that one before the last wrote
 
     // Activations, one pass through registers: each thread loads its 16-byte
     // pieces (consecutive per warp, so a warp's 32 pieces lie in one token),

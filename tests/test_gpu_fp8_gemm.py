@@ -447,3 +447,48 @@ def test_gates_far_below_zero_keep_their_bits(T, kind):
     got = h.get()
     assert (np.abs(got - want) <= tol + HALF[kind] * (np.abs(want) + tol)).all()
     assert (got[:, (g < -60) & (g > -100)] < 0).all()
+
+
+BETWEEN = {"direct": (1, "nvfp4", bqd.BQD_PATH_DIRECT), "stream": (1, "nvfp4", bqd.BQD_PATH_STREAM), "mma": (8, "nvfp4", bqd.BQD_PATH_MMA),
+           "tiles": (4, "nvfp4", bqd.BQD_PATH_TILES), "gemm": (64, "gemm", None)}
+
+
+@pytest.mark.parametrize("between", BETWEEN)
+@pytest.mark.parametrize("T", [1, 50, 300])
+def test_weights_written_two_calls_before_a_dependent_launch(T, between):
+    # with the flag a product may read weights while the call before it runs; that call (a GEMV that writes something
+    # else) lets it start only when the one before itself, the weights' encoder, is over
+    M, K, n = 2048, 4096, 5
+    N, form, path = BETWEEN[between]
+    d = Data(128, K, T, seed=43)
+    ws = torch.full((M // 128, K // 128), 0.01, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    src = [torch.randn(M, K, generator=g, device="cuda") for _ in range(n)]
+    w, sc = torch.empty(M, K, dtype=torch.uint8, device="cuda"), torch.empty(K // 128, M, device="cuda")
+    nv, ns = dev(codes((256, K // 2), 44)), dev(np.full((256, K // 16), 0x38, np.uint8))
+    x, o = torch.randn(N, K, device="cuda").to(torch.bfloat16), torch.empty(N, 256, device="cuda")
+
+    def run(wait):
+        out = []
+        for _ in range(6):
+            for s in src:
+                y = torch.empty(T, M, device="cuda")
+                bqd.fp8_x_encode(s, bqd.BQD_F32, K, w, sc, K, M)
+                if wait:
+                    torch.cuda.synchronize()
+                if form == "gemm":
+                    bqd.nvfp4_gemm(nv, ns, 0.01, x, o, 256, K, N)
+                else:
+                    bqd.nvfp4_gemv_path(nv, ns, 0.01, x, o, 256, K, N, path)
+                bqd.fp8_b128_gemm(w, ws, d.x, d.dxs, y, bqd.BQD_F32, M, K, T)
+                if wait:
+                    torch.cuda.synchronize()
+                out.append(y)
+        return out
+    old = bqd.set_launch_flags(bqd.BQD_LAUNCH_PDL)
+    try:
+        got = run(False)
+        torch.cuda.synchronize()
+    finally:
+        bqd.set_launch_flags(old)
+    assert all(torch.equal(a, b) for a, b in zip(run(True), got))
