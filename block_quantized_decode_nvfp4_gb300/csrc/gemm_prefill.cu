@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     __syncthreads();
     if (offsets) {
+        pdl_wait();  // the offsets may come from the previous kernel, and CTAs without tokens end here
         const int slot = static_cast<int>(blockIdx.y);
         for (int c0 = 0; c0 < E; c0 += kGThreads) {
             const int x = c0 + threadIdx.x;
