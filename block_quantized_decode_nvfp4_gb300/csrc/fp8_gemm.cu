@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(Narrow<BN>::kThreads, Narrow<BN>::kCtas)
         __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------ products, of every other block
+        // (the tokens come after the kernel before this one has completed, however long it stays: no time of it counts
+        // for the bounded waits)
+        fp8_pdl_wait();
         constexpr uint32_t idesc = fp8_idesc(kRows, BN);
         int it = 0;
         for (int tile = tile0; tile < tiles && ok; tile += step) {

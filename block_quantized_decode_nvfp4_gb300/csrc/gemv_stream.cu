@@ -227,6 +227,8 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         int64_t issued = 0;
         for (int64_t t = 0; t < nstages; ++t) {
             const int slot = static_cast<int>(t % ns);
+            // the consumers begin after the previous kernel: none of its time counts for the bounded waits for them
+            if (t == ns || t == kInitStagesS) pdl_wait();
             if (t >= ns)
                 ok = mbar_wait(&empty[slot], static_cast<uint32_t>(((t / ns) - 1) & 1), &g_stream_error, wait_limit);
             if (t == kInitStagesS && ok) ok = mbar_wait(&xready, 0u, &g_stream_error, wait_limit);
