@@ -365,13 +365,8 @@ cudaError_t launch_narrow(const Fp8GemmArgs& a, bool dual, cudaStream_t s)
     auto kern = fp8_gemm_kernel<BN>;
     static OccCache occ;
     blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, S::kThreads, S::kSmem);
-    if constexpr (S::kSplit) {  // it needs what the block is launched with
-        static const int regs = [] {
-            cudaFuncAttributes fa{};
-            return cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN>) == cudaSuccess ? fa.numRegs : 0;
-        }();
-        if (regs < S::kRegs) return cudaErrorInvalidConfiguration;
-    }
+    // the split of the registers needs what the block is launched with
+    if (S::kSplit && launch_regs(occ, reinterpret_cast<const void*>(kern), dev) < S::kRegs) return cudaErrorInvalidConfiguration;
     GemmShape g{};
     g.w[0] = a.w0;
     g.w[1] = a.w1;

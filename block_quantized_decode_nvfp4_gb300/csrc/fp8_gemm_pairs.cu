@@ -372,11 +372,7 @@ cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t s)
     static OccCache occ;
     blocks_per_sm(occ, reinterpret_cast<const void*>(kern), dev, kThreads, kSmem);
     // the split of the registers needs what the block is launched with
-    static const int regs = [] {
-        cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, fp8_pairs_kernel<DUAL>) == cudaSuccess ? fa.numRegs : 0;
-    }();
-    if (regs < kRegs) return cudaErrorInvalidConfiguration;
+    if (launch_regs(occ, reinterpret_cast<const void*>(kern), dev) < kRegs) return cudaErrorInvalidConfiguration;
     PairShape g{};
     g.s[0] = a.s0;
     g.s[1] = a.s1;

@@ -323,11 +323,7 @@ cudaError_t launch_fp8_gemm_tokens(const Fp8GemmArgs& a, bool dual, cudaStream_t
     const void* kern = reinterpret_cast<const void*>(fp8_tokens_kernel);
     blocks_per_sm(occ, kern, dev, kThreads, kSmem);
     // the split of the registers needs what the block is launched with
-    static const int regs = [] {
-        cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, fp8_tokens_kernel) == cudaSuccess ? fa.numRegs : 0;
-    }();
-    if (regs < kRegs) return cudaErrorInvalidConfiguration;
+    if (launch_regs(occ, kern, dev) < kRegs) return cudaErrorInvalidConfiguration;
     GemmShape g{};
     g.w[0] = a.w0;
     g.w[1] = a.w1;

@@ -45,6 +45,7 @@ struct OccCache {
     bool wide_clusters[64] = {};
     size_t smem[64][4] = {};
     int val[64][4] = {};
+    int regs[64] = {};
 };
 
 inline int blocks_per_sm(OccCache& c, const void* kern, int dev, int threads, size_t smem)
@@ -54,22 +55,26 @@ inline int blocks_per_sm(OccCache& c, const void* kern, int dev, int threads, si
     if (!c.attr_set[dev]) {
         // Allow dynamic shared memory up to the opt-in limit minus the
         // kernel's static shared memory. Errors of these calls are consumed
-        // here so that they cannot surface as a launch error later.
+        // here so that they cannot surface as a launch error later, and are
+        // not kept: the next call asks again.
         cudaFuncAttributes fa{};
-        size_t static_smem = 0;
-        if (cudaFuncGetAttributes(&fa, kern) == cudaSuccess) static_smem = fa.sharedSizeBytes;
         const int optin = dev_info(dev).max_smem_optin;
-        if (optin > static_cast<int>(static_smem))
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 optin - static_cast<int>(static_smem));
-        cudaGetLastError();
-        c.attr_set[dev] = true;
+        bool set = cudaFuncGetAttributes(&fa, kern) == cudaSuccess;
+        const int static_smem = set ? static_cast<int>(fa.sharedSizeBytes) : 0;
+        if (optin > static_smem)
+            set &= cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - static_smem) == cudaSuccess;
+        if (!set) cudaGetLastError();
+        c.attr_set[dev] = set;
     }
     for (int i = 0; i < 4; ++i)
         if (c.val[dev][i] && c.smem[dev][i] == smem) return c.val[dev][i];
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess) cudaGetLastError();
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return 1;
+    }
     if (n < 1) n = 1;
+    if (!c.attr_set[dev]) return n;
     for (int i = 0; i < 4; ++i)
         if (!c.val[dev][i]) {
             c.smem[dev][i] = smem;
@@ -77,6 +82,21 @@ inline int blocks_per_sm(OccCache& c, const void* kern, int dev, int threads, si
             break;
         }
     return n;
+}
+
+// Registers that a thread of the kernel is launched with; 0 if that cannot be
+// told now (not kept).
+inline int launch_regs(OccCache& c, const void* kern, int dev)
+{
+    std::lock_guard<std::mutex> g(c.mu);
+    if (dev >= 0 && dev < 64 && c.regs[dev]) return c.regs[dev];
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) {
+        cudaGetLastError();  // consumed: it must not surface as a launch error later
+        return 0;
+    }
+    if (dev >= 0 && dev < 64) c.regs[dev] = fa.numRegs;
+    return fa.numRegs;
 }
 
 // Allows a kernel clusters of more than 8 CTAs on the device: an attribute of
