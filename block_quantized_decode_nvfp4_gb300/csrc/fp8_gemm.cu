@@ -25,16 +25,20 @@
 // one weight, a CTA takes tile after tile, and its ring runs on from one to the
 // next.
 //
-// One token: 151936 x 4096 93 us (6.70 TB/s, the rate of a copy), 12288 x 4096 11.9 us
-// back to back, of which the weights stream for 7.8 (6.4 TB/s); the rest is the wait for
-// the call before (1.9), the first bytes (1.4), the last sums and the cluster's
-// exchange (1.5). 16, 32, 64 tokens: 12.4, 13.8, 15.8 us. A gated pair of 12288 x 4096 by
-// 64 tokens 24 us: its 192 CTAs lie unevenly on 152 SMs, and the exchange and outputs
+// One token: 151936 x 4096 92 to 94 us (6.7 TB/s, the rate of a copy), 12288 x 4096 11.0
+// us in calls that follow one another (10.7 with BQD_LAUNCH_PDL), of which the weights
+// stream for 7.8 (6.4 TB/s); the rest is the wait for the call before, the first bytes
+// and the last sums with the cluster's exchange, 1 to 1.5 us each. 16, 32, 64 tokens:
+// 11.6, 12.9, 14.8 us. A gated pair of 12288 x 4096 by 64 tokens 25 us: its 192 CTAs lie
+// unevenly on 152 SMs, and the exchange, whole fp32 parts of both weights, and outputs
 // take 5 of them. Copies by cp.async from four warps instead of tensor copies: 14.4 us for
 // one token, and twice as long as now where tokens are many. The first weights are called
-// into the L2 ahead of the wait for the call before: one and 32 tokens in turn 11.6 to 11.0
-// and 13.5 to 12.9 us, 4096 x 12288 by 17 12.7 to 12.2.
-// Every wait is bounded (kErrWaitTimeout in the kernel's error word).
+// into the L2 ahead of the wait for the call before: without that one and 32 tokens take
+// 11.6 and 13.5 us, 4096 x 12288 by 17 12.7 in place of 12.2.
+// Every wait for an mbarrier is bounded (kErrWaitTimeout in the kernel's error word), and
+// begins after the kernel before has completed. The others have no limit: all warps reach
+// the barriers of the block and of the cluster, after a wait that ran out too, and tensor
+// memory is there when it is asked for (see kSmem: who may lie beside one of these CTAs).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

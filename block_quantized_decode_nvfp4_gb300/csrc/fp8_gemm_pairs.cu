@@ -18,18 +18,25 @@
 // through shared memory: rows of whole 16 bytes as boxes that the copy engine stores
 // while the sums go on, others in whole lines.
 //
-// 12288 x 4096 by 8192 tokens 284 us, 2.90 PFLOP/s (more in a longer run: the power cap); a
-// gated pair by 4099 tokens 331. A block takes about 750 cycles where the MMAs need 512:
-// without the sums' multiply-adds 630, without their loads from tensor memory 620, which is
-// what the L2 gives an SM for its 32 KiB, and without copies 560. The sums' 128 packed
-// multiply-adds of an SM quarter and their loads take 330 cycles by themselves; the rest are
-// the block's scales and barriers, each access of which waits for the tensor cores' reads
-// of shared memory. What did not shorten it: rounds of 32 columns in place of 64, the next
+// 12288 x 4096 by 8192 tokens: 284 to 297 us in a few calls (2.8 to 2.9 PFLOP/s), 316 to 328
+// in many one after the other, under the power cap (2.5 to 2.6). A gated pair by 4099
+// tokens, the same: 331 to 340 and 354 to 368 with 8-bit outputs, 312 to 319 with bf16 and
+// 333 to 338 with fp32 ones in a few calls. A block takes about 750 cycles where the MMAs
+// need 512: without the sums' multiply-adds 630, without their loads from tensor memory
+// too 620, and without copies as well 560. A CTA's 32 KiB a block are 64 bytes a cycle at
+// the MMAs' rate, and an SM is given about 55 by the L2: 600 cycles are the least for this
+// tile, whatever the sums do. Those take 330 cycles by themselves (128 packed multiply-adds
+// of an SM quarter and their loads); the rest are the block's scales and barriers, each
+// access of which waits for the tensor cores' reads of shared memory. What did not shorten
+// it, all with this tile (a wider one is not tried): rounds of 32 columns in place of 64, the next
 // on its way or not (308 us where two of 64 took 308), 64 by one load (322), scalar
 // multiply-adds (314), sixteen warps of 64 columns (378), buffers of 128 columns, one for
 // each half of the warps (322), scales by warps of their own (380) or by asynchronous
 // copies (362). Outputs cost about 30 us of the whole.
-// Every wait is bounded (kErrWaitTimeout in the kernel's error word).
+// Every wait for an mbarrier is bounded (kErrWaitTimeout in the kernel's error word). The
+// others have no limit: all warps reach the barriers of the block and of the pair, after a
+// wait that ran out too, the copies out end by themselves, and no kernel with tensor memory
+// fits beside a CTA's shared memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -10,9 +10,10 @@
 // with two norms).
 //   fp8_x_encode: 4099 x 12288 fp32 38 us (6.6 TB/s), bf16 27 us (5.6 TB/s);
 //   residual_norm: 8191 x 4096, all fp32 to bf16, 71 us (6.6 TB/s); all bf16 with both
-//   norms, gates of each token and 8-bit outputs 53 us (5.7 TB/s; reductions one behind
-//   the other, 46 % of the warps); one token 1.8 us. Rows of more than 8192 channels
-//   fill an SM with one CTA: 2048 x 12288, the same, 58 us (3.9 TB/s).
+//   norms, gates of each token and 8-bit outputs 52 us (5.8 TB/s; reductions one behind
+//   the other, 46 % of the warps); one token 2.0 us. The same of 65536 x 512, a warp a
+//   row, 48 us (6.3 TB/s). Rows of more than 8192 channels fill an SM with one CTA:
+//   2048 x 12288, the same, 56 us (4.0 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -118,8 +118,8 @@ enum {
      * completed, but may call weights into the L2.) Do not
      * enable it if a call's weights can be written by the kernel immediately
      * before it in the stream. (Those before that one have completed when a
-     * call starts: every kernel lets its successor start only after its own
-     * wait.) Off by default. */
+     * call starts: a kernel that starts early lets its successor start only
+     * after its own wait.) Off by default. */
     BQD_LAUNCH_PDL = 1
 };
 
